@@ -15,7 +15,7 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhetlora.so")
 
-LORA_ABI_VERSION = 10
+LORA_ABI_VERSION = 11
 LORA_STATIC_SCRATCH_BYTES = 64 << 20
 LORA_MAX_RANK = 128
 LORA_MAX_PROJ = 8
@@ -26,7 +26,11 @@ LORA_INLINE_ITEMS = 64
 LORA_PREPARE_INLINE = 0x100
 WORK_INTS = 8  # int32 fields of lora_work_t
 LORA_OK, LORA_EINVAL, LORA_EADAPTER, LORA_ERANK, LORA_ESHAPE, LORA_ECAPACITY, LORA_EHIP = 0, -1, -2, -3, -4, -5, -6
+LORA_EPAGE, LORA_ENOMEM = -7, -8
 LORA_OP_SHRINK, LORA_OP_EXPAND, LORA_OP_APPLY = 0, 1, 2
+LORA_KV_BF16, LORA_KV_E4M3 = 0, 1
+LORA_F32, LORA_BF16 = 0, 1
+LORA_ATTN_NARROW, LORA_ATTN_WIDE = 0, 1
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built: run `python __graft_entry__.py` (build()) first")
@@ -109,6 +113,35 @@ class lora_merge_mat_t(ctypes.Structure):
                 ("B", lora_rows_t), ("adapter", _i32), ("rank", _i32), ("scale", _f32)]
 
 
+class lora_kv_t(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("dtype", _i32), ("n_pages", _i32),
+                ("page_tokens", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("reserved", _i32),
+                ("page_stride", _i64), ("head_stride", _i64), ("token_stride", _i64)]
+
+
+class lora_attn_shape_t(ctypes.Structure):
+    _fields_ = [("n_heads", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("page_tokens", _i32),
+                ("n_pages", _i32), ("kv_dtype", _i32), ("window", _i32), ("sinks", _i32)]
+
+
+class lora_attn_info_t(ctypes.Structure):
+    _fields_ = [("shape", lora_attn_shape_t), ("n_seq", _i32), ("n_rows", _i32), ("n_tokens", _i32),
+                ("max_kv", _i32), ("ld_table", _i32), ("n_work", _i32 * 2), ("n_merge", _i32), ("part_rows", _i64),
+                ("workspace_floats", _i64), ("off_work", _i64 * 2), ("off_merge", _i64), ("off_q_start", _i64),
+                ("off_kv_len", _i64), ("off_kv_start", _i64), ("off_row_pos", _i64), ("off_row_slot", _i64),
+                ("off_table", _i64), ("n_staged", _i64)]
+
+
+class lora_attn_launch_t(ctypes.Structure):
+    _fields_ = [("meta", _vp), ("info", lora_attn_info_t)]
+
+
+class lora_kv_write_args_t(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("ldq", _i64), ("ldk", _i64), ("ldv", _i64), ("rope", _vp),
+                ("q_out", _vp), ("ld_out", _i64), ("dtype", _i32), ("rope_len", _i32), ("rope_dim", _i32),
+                ("reserved", _i32)]
+
+
 _sig = {
     "lora_abi_version": (_i32, []),
     "lora_status_string": (ctypes.c_char_p, [_i32]),
@@ -136,6 +169,12 @@ _sig = {
     "lora_pool_stats": (_i32, [_vp, _P(_i32), _P(_i64), _P(_i32)]),
     "lora_pool_load_list": (_i32, [_vp, _i32, _vp, _i64, _vp, _vp, _vp, _P(_i64), _P(_i64)]),
     "lora_pool_scatter": (_i32, [_vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "lora_attn_plan": (_i32, [_P(lora_attn_shape_t), _i32, _vp, _vp, _vp, _i64, _vp, _i64, _P(lora_attn_info_t)]),
+    "lora_attn_prepare": (_i32, [_P(lora_attn_shape_t), _i32, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
+                                 _P(lora_attn_launch_t)]),
+    "lora_kv_write": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _P(lora_kv_write_args_t), _vp]),
+    "lora_kv_read": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _vp, _vp, _i64, _vp]),
+    "lora_attn": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _vp, _i64, _vp, _i64, _f32, _vp, _i64, _vp]),
 }
 # HIP runtime calls the binding makes itself (events), resolved through the
 # library's handle so they bind to the runtime the library uses
@@ -285,6 +324,29 @@ class LoraPool:
 def lora_pool_scatter(src_ptr, pool_ptr, n, src_off_ptr, dst_off_ptr, len_ptr, stream=None):
     _check(_lib.lora_pool_scatter(src_ptr, pool_ptr, int(n), src_off_ptr, dst_off_ptr, len_ptr, stream),
            "lora_pool_scatter")
+
+
+def lora_attn_plan(shape, q_len, kv_len, block_table=None, staging_capacity=None, raw=False):
+    """Attention plan of a batch (host).  block_table: int32 [n_seq, pages], or
+    None when nothing is cached.  Returns (staging int32 [n_staged], info), or
+    (status, staging, info) with raw=True."""
+    ql = np.ascontiguousarray(q_len, dtype=np.int32)
+    kl = np.ascontiguousarray(kv_len, dtype=np.int32)
+    assert ql.shape == kl.shape and ql.ndim == 1
+    tab = None if block_table is None else np.ascontiguousarray(block_table, dtype=np.int32)
+    assert tab is None or (tab.ndim == 2 and tab.shape[0] == ql.shape[0])
+    info = lora_attn_info_t()
+    args = (ctypes.byref(shape), ql.shape[0], ql.ctypes.data, kl.ctypes.data, _ptr(tab),
+            0 if tab is None else tab.shape[1])
+    if staging_capacity is None:
+        st = _lib.lora_attn_plan(*args, None, 0, ctypes.byref(info))
+        staging_capacity = int(info.n_staged) if st in (LORA_OK, LORA_ECAPACITY) else 0
+    staging = np.zeros(max(1, int(staging_capacity)), np.int32)
+    st = _lib.lora_attn_plan(*args, staging.ctypes.data, int(staging_capacity), ctypes.byref(info))
+    if raw:
+        return st, staging[:int(staging_capacity)], info
+    _check(st, "lora_attn_plan")
+    return staging[:int(info.n_staged)], info
 
 
 def _ptr(a):

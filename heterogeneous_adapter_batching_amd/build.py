@@ -1,13 +1,14 @@
 """Build libhetlora.so in-tree for gfx950.
 
-host.cpp and pool.cpp (no HIP) are compiled by g++, kernels.hip by hipcc;
-hipcc links the shared library next to this file.  Every build compiles from
+host.cpp, pool.cpp and attn_plan.cpp (no HIP) are compiled by g++, kernels.hip
+and attn.hip by hipcc; hipcc links the shared library next to this file.  Every build compiles from
 scratch.
 """
 import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -41,15 +42,17 @@ def build(verbose=False, out=LIB, defines=(), build_dir=None):
     (tuning constants); the default build uses none."""
     out_dir = build_dir or os.path.join(HERE, "_build")
     os.makedirs(out_dir, exist_ok=True)
-    host_o = [os.path.join(out_dir, f"{n}.o") for n in ("host", "pool")]
-    kern_o = os.path.join(out_dir, "kernels.o")
     dflags = [f"-D{d}" for d in defines]
-    for n, o in zip(("host", "pool"), host_o):
-        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", f"-I{INCLUDE}", *dflags, "-c",
-              os.path.join(CSRC, f"{n}.cpp"), "-o", o])
-    _run([_hipcc(), *HIP_FLAGS, *dflags, "-c", os.path.join(CSRC, "kernels.hip"), "-o", kern_o])
+    host, kern = ("host", "pool", "attn_plan"), ("kernels", "attn")
+    cmds = [["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", f"-I{INCLUDE}", *dflags, "-c",
+             os.path.join(CSRC, f"{n}.cpp"), "-o", os.path.join(out_dir, f"{n}.o")] for n in host]
+    cmds += [[_hipcc(), *HIP_FLAGS, *dflags, "-c", os.path.join(CSRC, f"{n}.hip"), "-o",
+              os.path.join(out_dir, f"{n}.o")] for n in kern]
+    with ThreadPoolExecutor() as pool:
+        list(pool.map(_run, cmds))
+    objs = [os.path.join(out_dir, f"{n}.o") for n in host + kern]
     tmp = out + ".tmp"
-    _run([_hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *host_o, kern_o, "-o", tmp])
+    _run([_hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp])
     os.replace(tmp, out)
     if verbose:
         print("built", out)

@@ -1,0 +1,936 @@
+// gfx950 kernels of the paged cache and the attention over it, and their C-ABI
+// launchers.
+//
+//   write  k, v of the batch's new tokens into the cache's pages, q and k turned
+//          by their positions' angles first
+//   read   a batch's cached tokens back as bf16
+//   attn   out_i = sum_j w_ij v_j, w_ij = exp(scale q_i . k_j) / sum, over the
+//          tokens that row i sees
+//
+// Attention works on the transposed products S^T = K Q^T and O^T = V^T P^T, so
+// that a query is a column of every MFMA: its running maximum and sum live in
+// the lanes of that column, and S^T leaves the first product in the registers
+// in which the second one takes P^T.  In the 32x32 result a lane of half h =
+// lane / 32 holds rows 8b + 4h + 0..3 (b = 0..3) of its column; the second
+// product's operand wants 8 reduction elements per lane, any 8 as long as V^T
+// brings the same ones.  So slots 0..3 stand for tokens 8b + 4h + 0..3 and
+// slots 4..7 for 8(b+1) + 4h + 0..3: the registers as they are.  The 16x16
+// form works alike with tokens 4g + 0..3 and 16 + 4g + 0..3 of lane group g.
+// V^T's fragments come out of row-major V tiles by transposing LDS reads
+// (16 lanes read 4 rows x 16 columns, 8 bytes each, and get a column of 4).
+//
+// The scores are kept in base 2 (scale * log2 e is folded into one multiply-add)
+// and the accumulator is rescaled only when a row's maximum grows by more than
+// 2^8 over the one in use: weights then stay below 2^8, far inside fp32 and
+// bf16, and the common tile pays neither the rescale nor a reduction over
+// lanes.  Weights are rounded to bf16 for the second product, and the rounded
+// weights are what the row's sum adds up, so the rounding cancels where few
+// tokens dominate.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "../../include/hetlora.h"
+#define AT_FN static __host__ __device__ inline
+#include "attn_rules.h"
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.0f;  // growth of a maximum (in powers of two) that is let pass
+
+__device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                   c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                   c, 0, 0, 0);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// Two fp32 -> packed bf16, round to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const bf16x2_t p = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, p);
+}
+// acc + lo(w) + hi(w)
+__device__ __forceinline__ float add_bf16_pair(uint32_t w, float acc) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w),
+                                           __builtin_bit_cast(bf16x2_t, 0x3F803F80u), acc, false);
+}
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// Transposing LDS read: within each 16 lanes, lane i reads 8 bytes (4 bf16) and
+// gets element i of the four 16-element rows that 4 lanes each supply.
+__device__ __forceinline__ u32x2_t ds_tr16(const char* p) {
+    typedef __attribute__((address_space(3))) s16x4_t lds_t;
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)p));
+}
+
+// ------------------------------------------------------------------ the cache
+struct Kv {
+    const char* k;
+    const char* v;
+    const uint8_t* k_scale;
+    const uint8_t* v_scale;
+    int64_t page_stride, head_stride, token_stride;
+    int32_t n_pages, page_shift, n_kv_heads;
+};
+// A page id that is not one of the cache's (the host checks the table it
+// stages) is read as the last page instead of outside the cache.
+__device__ __forceinline__ int32_t clamp_page(const Kv& c, int32_t page) {
+    return (int32_t)min((uint32_t)page, (uint32_t)(c.n_pages - 1));
+}
+__device__ __forceinline__ int64_t kv_off(const Kv& c, int32_t page, int32_t head, int32_t slot) {
+    return page * c.page_stride + head * c.head_stride + slot * c.token_stride;
+}
+__device__ __forceinline__ int64_t scale_off(const Kv& c, int32_t page, int32_t head, int32_t slot) {
+    return (((int64_t)page * c.n_kv_heads + head) << c.page_shift) + slot;
+}
+__device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
+// 8 e4m3 codes times a power of two -> 8 bf16 (exact)
+__device__ __forceinline__ u32x4_t dequant8(u32x2_t c, float scale) {
+    u32x4_t r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], scale, false));
+        r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], scale, true));
+    }
+    return r;
+}
+
+// ------------------------------------------------------------------ write
+struct WriteArgs {
+    Kv kv;
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    const float* rope;
+    uint16_t* q_out;
+    int64_t ld_out;
+    const int32_t* row_pos;
+    const int32_t* row_slot;
+    int32_t n_heads, n_vec, n_rows, rope_dim, rope_len;
+};
+
+template <bool F32>
+__device__ __forceinline__ f32x4_t load4(const void* p, int64_t i) {
+    if constexpr (F32) {
+        return *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + i);
+    } else {
+        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(p) + i);
+        return f32x4_t{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+    }
+}
+__device__ __forceinline__ float finite_abs(float x) {
+    x = fabsf(x);
+    return x < INFINITY ? x : 0.f;
+}
+// The e4m3 code of x * inv (inv a power of two), as lora_kv_t describes it.
+__device__ __forceinline__ float e4m3_input(float x, float inv) {
+    const float y = fminf(fmaxf(x * inv, -448.f), 448.f);
+    return fabsf(x) < INFINITY ? y : __builtin_nanf("");
+}
+
+// D/8 lanes take one head's vector, 8 elements each: the pair elements c and c +
+// rope_dim/2 of a turn lie in the same lane (4 and 4 of them), so nothing
+// crosses lanes but the maximum.  The turn is written without multiply-adds:
+// every product is rounded, as in the formula's plain evaluation in fp32, so
+// that codes next to a rounding border do not depend on how it is evaluated.
+template <int D, bool F32, bool E4M3>
+__global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
+    constexpr int LPV = D / 8, VPB = 256 / LPV;
+    const int row = blockIdx.y + gridDim.y * blockIdx.z;
+    const int vec = blockIdx.x * VPB + threadIdx.x / LPV, i = threadIdx.x % LPV;
+    if (row >= a.n_rows || vec >= a.n_vec) return;
+    const int pos = a.row_pos[row], slot = a.row_slot[row];
+    const int hk = a.kv.n_kv_heads;
+    const bool is_q = vec < a.n_heads, is_k = !is_q && vec < a.n_heads + hk;
+    const int head = is_q ? vec : is_k ? vec - a.n_heads : vec - a.n_heads - hk;
+    const int half = a.rope_dim >> 1;
+    const bool in_turn = 8 * i < a.rope_dim;
+    const int c0 = in_turn ? 4 * i : 8 * i, c1 = in_turn ? half + 4 * i : 8 * i + 4;
+    const void* src = is_q ? a.q : is_k ? a.k : a.v;
+    const int64_t at = row * (is_q ? a.ldq : is_k ? a.ldk : a.ldv) + (int64_t)head * D;
+    f32x4_t x = load4<F32>(src, at + c0), y = load4<F32>(src, at + c1);
+    if (in_turn && (is_q || is_k) && pos >= 0 && pos < a.rope_len) {
+#pragma clang fp contract(off)
+        const f32x4_t c = *reinterpret_cast<const f32x4_t*>(a.rope + (int64_t)pos * a.rope_dim + c0);
+        const f32x4_t s = *reinterpret_cast<const f32x4_t*>(a.rope + (int64_t)pos * a.rope_dim + c1);
+        const f32x4_t u = x * c - y * s, w = x * s + y * c;
+        x = u;
+        y = w;
+    }
+    if (is_q) {
+        uint16_t* o = a.q_out + row * a.ld_out + (int64_t)head * D;
+        if (pos < 0) x = y = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        *reinterpret_cast<u32x2_t*>(o + c0) = u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+        *reinterpret_cast<u32x2_t*>(o + c1) = u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        return;
+    }
+    const int32_t page = slot >> a.kv.page_shift;
+    const bool held = slot >= 0 && page < a.kv.n_pages;
+    const int32_t place = slot & ((1 << a.kv.page_shift) - 1);
+    char* cache = const_cast<char*>(is_k ? a.kv.k : a.kv.v);
+    if constexpr (!E4M3) {
+        if (!held) return;
+        uint16_t* o = reinterpret_cast<uint16_t*>(cache) + kv_off(a.kv, page, head, place);
+        *reinterpret_cast<u32x2_t*>(o + c0) = u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+        *reinterpret_cast<u32x2_t*>(o + c1) = u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+    } else {
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(finite_abs(x[j]), finite_abs(y[j])));
+#pragma unroll
+        for (int o = 1; o < LPV; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+        // least e with top <= 1.75 * 2^8 * 2^e, from the bits of top = m * 2^t
+        // (a subnormal top reads as t = -127, which the clamp covers)
+        const uint32_t bits = __float_as_uint(top);
+        int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        e = min(max(e, -100), 119);
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        uint32_t lo = 0, hi = 0;
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_input(x[0], inv), e4m3_input(x[1], inv), lo, false);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_input(x[2], inv), e4m3_input(x[3], inv), lo, true);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_input(y[0], inv), e4m3_input(y[1], inv), hi, false);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_input(y[2], inv), e4m3_input(y[3], inv), hi, true);
+        if (!held) return;
+        char* o = cache + kv_off(a.kv, page, head, place);
+        *reinterpret_cast<uint32_t*>(o + c0) = lo;
+        *reinterpret_cast<uint32_t*>(o + c1) = hi;
+        uint8_t* sc = const_cast<uint8_t*>(is_k ? a.kv.k_scale : a.kv.v_scale);
+        if (i == 0) sc[scale_off(a.kv, page, head, place)] = (uint8_t)(e + 127);
+    }
+}
+
+// ------------------------------------------------------------------ read
+struct ReadArgs {
+    Kv kv;
+    uint16_t *k_out, *v_out;
+    int64_t ld;
+    const int32_t* kv_start;
+    const int32_t* table;
+    int32_t n_seq, n_tokens, ld_table;
+};
+
+// D/8 lanes take one (token, head): 8 elements of k and 8 of v each.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
+    constexpr int LPV = D / 8, VPB = 256 / LPV;
+    const int c = 8 * (threadIdx.x % LPV), hk = a.kv.n_kv_heads;
+    const int64_t n_vec = (int64_t)a.n_tokens * hk;
+    for (int64_t vec = (int64_t)blockIdx.x * VPB + threadIdx.x / LPV; vec < n_vec; vec += (int64_t)gridDim.x * VPB) {
+        const int token = (int)(vec / hk), head = (int)(vec % hk);
+        int lo = 0, hi = a.n_seq;  // the sequence: kv_start[lo] <= token < kv_start[lo + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.kv_start[mid] <= token) lo = mid;
+            else hi = mid;
+        }
+        const int t = token - a.kv_start[lo];
+        const int32_t page = clamp_page(a.kv, a.table[(int64_t)lo * a.ld_table + (t >> a.kv.page_shift)]);
+        const int32_t place = t & ((1 << a.kv.page_shift) - 1);
+        const int64_t off = kv_off(a.kv, page, head, place) + c, out = (int64_t)token * a.ld + (int64_t)head * D + c;
+        u32x4_t k, v;
+        if constexpr (E4M3) {
+            const int64_t so = scale_off(a.kv, page, head, place);
+            const float ks = scale_of(a.kv.k_scale[so]), vs = scale_of(a.kv.v_scale[so]);
+            k = dequant8(*reinterpret_cast<const u32x2_t*>(a.kv.k + off), ks);
+            v = dequant8(*reinterpret_cast<const u32x2_t*>(a.kv.v + off), vs);
+        } else {
+            k = *reinterpret_cast<const u32x4_t*>(a.kv.k + 2 * off);
+            v = *reinterpret_cast<const u32x4_t*>(a.kv.v + 2 * off);
+        }
+        *reinterpret_cast<u32x4_t*>(a.k_out + out) = k;
+        *reinterpret_cast<u32x4_t*>(a.v_out + out) = v;
+    }
+}
+
+// ------------------------------------------------------------------ attention
+struct AttnArgs {
+    Kv kv;
+    const lora_attn_work_t* work;
+    const int32_t *q_start, *kv_len, *table;
+    const uint16_t* q;
+    uint16_t* out;
+    float* part;  // [n_kv_heads][part_rows][D] partial sums, then [n_kv_heads][part_rows][2] of (maximum, sum)
+    int64_t ldq, ldo, part_rows;
+    int32_t n_seq, ld_table, n_work, group, window, sinks;
+    float sl2;  // scale * log2 e
+};
+
+// What every lane of an item needs to know.
+struct Item {
+    int32_t seq, row0, nrows, it0, it1, nsplits, part;
+    int32_t q0, n_new, kv, p0;  // first row, new tokens, cached tokens, position of the first new token
+    const int32_t* table;
+    AtSpan span;
+};
+// Items that do not lie inside the batch are skipped, so a corrupted work list
+// cannot index outside the buffers.
+__device__ __forceinline__ bool load_item(const AttnArgs& a, int i, int max_rows, Item& it) {
+    const lora_attn_work_t w = a.work[i];
+    if (w.seq < 0 || w.seq >= a.n_seq) return false;
+    it.seq = w.seq;
+    it.row0 = w.row0;
+    it.nrows = w.nrows;
+    it.nsplits = w.nsplits;
+    it.part = w.part;
+    it.q0 = a.q_start[w.seq];
+    it.n_new = a.q_start[w.seq + 1] - it.q0;
+    it.kv = a.kv_len[w.seq];
+    it.p0 = it.kv - it.n_new;
+    it.table = a.table + (int64_t)w.seq * a.ld_table;
+    if (w.nrows < 1 || w.nrows > max_rows || w.row0 < 0 || (int64_t)w.row0 + w.nrows > (int64_t)it.n_new * a.group)
+        return false;
+    if (w.nsplits > 1 && (w.part < 0 || (int64_t)w.part + w.nrows > a.part_rows)) return false;
+    it.span = at_span(it.p0 + w.row0 / a.group, it.p0 + (w.row0 + w.nrows - 1) / a.group, a.window, a.sinks);
+    it.it0 = max(w.it0, 0);
+    it.it1 = min(w.it1, at_span_tiles(it.span));
+    return true;
+}
+// Element offset of row r of the item's sequence (head r % group of kv head h, new token r / group).
+__device__ __forceinline__ int64_t row_off(const AttnArgs& a, const Item& it, int r, int h, int64_t ld, int D) {
+    return (int64_t)(it.q0 + r / a.group) * ld + (int64_t)(h * a.group + r % a.group) * D;
+}
+__device__ __forceinline__ bool sees(const AttnArgs& a, int pos, int token) {
+    return token <= pos && (a.window == 0 || token > pos - a.window || token < a.sinks);
+}
+// Every row of positions p_lo .. p_hi sees all of tokens t0 .. t1; and: none sees any.
+__device__ __forceinline__ bool all_see(const AttnArgs& a, int p_lo, int p_hi, int t0, int t1) {
+    return t1 <= p_lo && (a.window == 0 || t0 > p_hi - a.window || t1 < a.sinks);
+}
+__device__ __forceinline__ bool none_sees(const AttnArgs& a, int p_lo, int p_hi, int t0, int t1) {
+    return t0 > p_hi || (a.window != 0 && t1 <= p_lo - a.window && t0 >= a.sinks);
+}
+
+// Tiles in LDS are row-major bf16, D * 2 bytes a row, with the 16-byte chunks of
+// a row permuted: K by the row (32 lanes read one chunk of 32 rows), V by the
+// row in pairs of chunks (16 lanes read 32 bytes of 4 rows).
+template <int D>
+__device__ __forceinline__ int k_chunk(int row, int c) { return c ^ (row & (D / 8 - 1)); }
+template <int D>
+__device__ __forceinline__ int v_chunk(int row, int c) { return c ^ (2 * (row & (D / 16 - 1))); }
+
+// Tokens [t0, t0 + ROWS) of one kv head on their way from the cache to LDS, 8
+// elements per lane and step.  Tokens past the end of the sequence take its
+// last token's place: nothing sees them.
+template <int D, bool E4M3, int ROWS, int NT>
+struct Stage {
+    static constexpr int CPR = D / 8, RPS = NT / CPR, STEPS = ROWS / RPS;
+    typedef typename std::conditional<E4M3, u32x2_t, u32x4_t>::type raw_t;
+    raw_t k[STEPS], v[STEPS];
+    uint32_t ke[STEPS], ve[STEPS];
+
+    __device__ __forceinline__ void load(const Kv& c, const Item& it, int head, int t0, int t) {
+        const int chunk = t % CPR;
+        int32_t page[STEPS], place[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int tok = min(t0 + s * RPS + t / CPR, it.kv - 1);
+            page[s] = it.table[tok >> c.page_shift];
+            place[s] = tok & ((1 << c.page_shift) - 1);
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int32_t pg = clamp_page(c, page[s]);
+            const int64_t off = kv_off(c, pg, head, place[s]) + 8 * chunk;
+            k[s] = *reinterpret_cast<const raw_t*>(c.k + off * (E4M3 ? 1 : 2));
+            v[s] = *reinterpret_cast<const raw_t*>(c.v + off * (E4M3 ? 1 : 2));
+            if constexpr (E4M3) {
+                const int64_t so = scale_off(c, pg, head, place[s]);
+                ke[s] = c.k_scale[so];
+                ve[s] = c.v_scale[so];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(char* kt, char* vt, int t) const {
+        const int chunk = t % CPR;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int row = s * RPS + t / CPR;
+            u32x4_t kk, vv;
+            if constexpr (E4M3) {
+                kk = dequant8(k[s], scale_of(ke[s]));
+                vv = dequant8(v[s], scale_of(ve[s]));
+            } else {
+                kk = k[s];
+                vv = v[s];
+            }
+            *reinterpret_cast<u32x4_t*>(kt + row * (2 * D) + 16 * k_chunk<D>(row, chunk)) = kk;
+            *reinterpret_cast<u32x4_t*>(vt + row * (2 * D) + 16 * v_chunk<D>(row, chunk)) = vv;
+        }
+    }
+};
+
+__device__ __forceinline__ float v_elem(const char* vt, int row_bytes, int row, int chunk, int e) {
+    return __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(vt + row * row_bytes + 16 * chunk + 2 * e)
+                           << 16);
+}
+
+// Four waves, 32 rows each; tiles of 64 tokens go through LDS, the next one's
+// loads in flight while one is worked on.
+//
+// A value that is infinite or NaN in a place that a row does not see would
+// still reach it through the second product (0 * NaN).  Looking for such values
+// in every masked tile costs more than it is worth, so the item looks at its
+// result: when that is not finite, it is computed again, and the tiles in which
+// some row is masked take each row's visible tokens alone.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a) {
+    constexpr int RB = 2 * D, DB = D / 32, KS = D / 16;
+    __shared__ __align__(16) char lds[2][2][AT_TILE * RB];
+    const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
+    const int col = lane & 31, h = lane >> 5;
+    Item it;
+    if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_WIDE_ROWS, it)) return;
+
+    // this lane's row; lanes past the item's rows repeat its last one
+    const int row = min(32 * w + col, it.nrows - 1);
+    const bool active = 32 * w < it.nrows;
+    const int pos = it.p0 + (it.row0 + row) / a.group;
+    const int p_lo = it.p0 + (it.row0 + min(32 * w, it.nrows - 1)) / a.group;
+    const int p_hi = it.p0 + (it.row0 + min(32 * w + 31, it.nrows - 1)) / a.group;
+    u32x4_t qf[KS];
+    {
+        const uint16_t* q = a.q + row_off(a, it, it.row0 + row, head, a.ldq, D) + 8 * h;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4_t*>(q + 16 * s);
+    }
+
+    f32x16_t acc[DB];
+    float m, l;
+    for (bool careful = false;; careful = true) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d) acc[d] = f32x16_t{};
+        m = -INFINITY;
+        l = 0.f;
+        Stage<D, E4M3, AT_TILE, 256> st;
+        if (it.it0 < it.it1) st.load(a.kv, it, head, AT_TILE * at_span_tile(it.span, it.it0), threadIdx.x);
+        for (int i = it.it0; i < it.it1; ++i) {
+            const int t0 = AT_TILE * at_span_tile(it.span, i);
+            char *kt = lds[i & 1][0], *vt = lds[i & 1][1];
+            st.store(kt, vt, threadIdx.x);
+            __syncthreads();
+            if (i + 1 < it.it1) st.load(a.kv, it, head, AT_TILE * at_span_tile(it.span, i + 1), threadIdx.x);
+            if (!active || none_sees(a, p_lo, p_hi, t0, t0 + AT_TILE - 1)) continue;
+
+            f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int r = 32 * b + col;
+                    s[b] = mfma32(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 2 * ks + h)),
+                                  qf[ks], s[b]);
+                }
+            const bool masked = !all_see(a, p_lo, p_hi, t0, t0 + AT_TILE - 1);
+            if (masked) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (!sees(a, pos, t0 + 32 * b + 8 * (r >> 2) + 4 * h + (r & 3))) s[b][r] = -INFINITY;
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+            if (__ballot(top * a.sl2 > m + kGrow)) {
+                const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
+                const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
+                m = up;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) acc[d] *= f;
+            }
+            const float off = m == -INFINITY ? 0.f : -m;
+            uint32_t pw[16];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; r += 2) {
+                    const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
+                    const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
+                    const uint32_t pk = pack_bf16(p0, p1);
+                    l = add_bf16_pair(pk, l);
+                    pw[8 * b + r / 2] = pk;
+                }
+            if (careful && masked) {
+                // one pair of rows' weights after the other, each register moved
+                // down to the first: a rolled loop over registers
+#pragma unroll 1
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t cur = pw[0];
+#pragma unroll
+                    for (int k = 0; k < 15; ++k) pw[k] = pw[k + 1];
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t both = __shfl(cur, col + 32 * (x >> 1));
+                        const float p = x & 1 ? bf16_hi(both) : bf16_lo(both);
+                        const int r = 2 * (j & 7) + (x & 1);
+                        const int tok = 32 * (j >> 3) + 8 * (r >> 2) + 4 * (x >> 1) + (r & 3);
+                        const bool vis = sees(a, pos, t0 + tok);
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const int el = 32 * d + 8 * (e >> 2) + 4 * h + (e & 3);
+                                const float v = v_elem(vt, RB, tok, v_chunk<D>(tok, el >> 3), el & 7);
+                                acc[d][e] = vis ? fmaf(p, v, acc[d][e]) : acc[d][e];
+                            }
+                    }
+                }
+                continue;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const u32x4_t pf = {pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]};
+                const int i16 = lane & 15, g = (lane >> 4) & 1;
+                const int r = 16 * c + 4 * h + (i16 >> 2);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const int ch = 4 * d + 2 * g + ((i16 & 3) >> 1), by = 8 * (i16 & 1);
+                    const u32x2_t lo = ds_tr16(vt + r * RB + 16 * v_chunk<D>(r, ch) + by);
+                    const u32x2_t hi = ds_tr16(vt + (r + 8) * RB + 16 * v_chunk<D>(r + 8, ch) + by);
+                    acc[d] = mfma32(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
+                }
+            }
+        }
+        float bad = 0.f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) bad = fmaf(acc[d][e], 0.f, bad);
+        if (careful || !__syncthreads_or(active && bad != 0.f)) break;
+    }
+
+    if (!active) return;
+    l += __shfl_xor(l, 32);
+    if (32 * w + col >= it.nrows) return;
+    if (it.nsplits == 1) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* o = a.out + row_off(a, it, it.row0 + row, head, a.ldo, D) + 4 * h;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                *reinterpret_cast<u32x2_t*>(o + 32 * d + 8 * b) =
+                    u32x2_t{pack_bf16(acc[d][4 * b] * inv, acc[d][4 * b + 1] * inv),
+                            pack_bf16(acc[d][4 * b + 2] * inv, acc[d][4 * b + 3] * inv)};
+    } else {
+        const int64_t pr = head * a.part_rows + it.part + row;
+        float* o = a.part + pr * D + 4 * h;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                *reinterpret_cast<f32x4_t*>(o + 32 * d + 8 * b) =
+                    f32x4_t{acc[d][4 * b], acc[d][4 * b + 1], acc[d][4 * b + 2], acc[d][4 * b + 3]};
+        if (h == 0) {
+            float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D + 2 * pr;
+            ml[0] = m;
+            ml[1] = l;
+        }
+    }
+}
+
+// Up to 16 rows (the query heads of a kv head, for a few new tokens): the four
+// waves take tiles of 32 tokens in turn, each through LDS of its own, so that
+// no barrier stands between the loads, and join their results at the end.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
+    constexpr int RB = 2 * D, DB = D / 16, KS = D / 32, T = 32;
+    __shared__ __align__(16) char lds[4][2][T * RB];
+    __shared__ float s_m[4][16], s_l[4][16];
+    const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
+    const int col = lane & 15, g = lane >> 4;
+    Item it;
+    if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_NARROW_ROWS, it)) return;
+
+    const int row = min(col, it.nrows - 1);
+    const int pos = it.p0 + (it.row0 + row) / a.group;
+    const int p_lo = it.p0 + it.row0 / a.group, p_hi = it.p0 + (it.row0 + it.nrows - 1) / a.group;
+    u32x4_t qf[KS];
+    {
+        const uint16_t* q = a.q + row_off(a, it, it.row0 + row, head, a.ldq, D) + 8 * g;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4_t*>(q + 32 * s);
+    }
+    char *kt = lds[w][0], *vt = lds[w][1];
+    const auto tile_of = [&](int i) { return AT_TILE * at_span_tile(it.span, i >> 1) + T * (i & 1); };
+
+    f32x4_t acc[DB];
+    float m, l;
+    for (bool careful = false;; careful = true) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d) acc[d] = f32x4_t{};
+        m = -INFINITY;
+        l = 0.f;
+        Stage<D, E4M3, T, 64> st;
+        int i = 2 * it.it0 + w;
+        const int end = 2 * it.it1;
+        if (i < end) st.load(a.kv, it, head, tile_of(i), lane);
+        for (; i < end; i += 4) {
+            const int t0 = tile_of(i);
+            st.store(kt, vt, lane);
+            if (i + 4 < end) st.load(a.kv, it, head, tile_of(i + 4), lane);
+            if (none_sees(a, p_lo, p_hi, t0, t0 + T - 1)) continue;
+
+            f32x4_t s[2] = {f32x4_t{}, f32x4_t{}};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int r = 16 * b + col;
+                    s[b] = mfma16(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 4 * ks + g)),
+                                  qf[ks], s[b]);
+                }
+            const bool masked = !all_see(a, p_lo, p_hi, t0, t0 + T - 1);
+            if (masked) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (!sees(a, pos, t0 + 16 * b + 4 * g + r)) s[b][r] = -INFINITY;
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
+            if (__ballot(top * a.sl2 > m + kGrow)) {
+                top = fmaxf(top, __shfl_xor(top, 16));
+                const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
+                const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
+                m = up;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) acc[d] *= f;
+            }
+            const float off = m == -INFINITY ? 0.f : -m;
+            uint32_t pw[4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; r += 2) {
+                    const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
+                    const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
+                    const uint32_t pk = pack_bf16(p0, p1);
+                    l = add_bf16_pair(pk, l);
+                    pw[2 * b + r / 2] = pk;
+                }
+            if (careful && masked) {
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t cur = pw[0];
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) pw[k] = pw[k + 1];
+#pragma unroll 1
+                    for (int x = 0; x < 8; ++x) {
+                        const uint32_t both = __shfl(cur, col + 16 * (x >> 1));
+                        const float p = x & 1 ? bf16_hi(both) : bf16_lo(both);
+                        const int tok = 16 * (j >> 1) + 4 * (x >> 1) + 2 * (j & 1) + (x & 1);
+                        const bool vis = sees(a, pos, t0 + tok);
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int el = 16 * d + 4 * g + e;
+                                const float v = v_elem(vt, RB, tok, v_chunk<D>(tok, el >> 3), el & 7);
+                                acc[d][e] = vis ? fmaf(p, v, acc[d][e]) : acc[d][e];
+                            }
+                    }
+                }
+                continue;
+            }
+            const u32x4_t pf = {pw[0], pw[1], pw[2], pw[3]};
+            const int r = 4 * g + (col >> 2);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const int ch = 2 * d + ((col & 3) >> 1), by = 8 * (col & 1);
+                const u32x2_t lo = ds_tr16(vt + r * RB + 16 * v_chunk<D>(r, ch) + by);
+                const u32x2_t hi = ds_tr16(vt + (r + 16) * RB + 16 * v_chunk<D>(r + 16, ch) + by);
+                acc[d] = mfma16(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
+            }
+        }
+        float bad = 0.f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad = fmaf(acc[d][e], 0.f, bad);
+        if (careful || !__ballot(bad != 0.f)) break;
+    }
+
+    // join the waves: each leaves its maximum, sum and [row][D] accumulator in LDS
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) {
+        s_m[w][col] = m;
+        s_l[w][col] = l;
+    }
+    float* mine = reinterpret_cast<float*>(lds[w][0]);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) *reinterpret_cast<f32x4_t*>(mine + col * D + 16 * d + 4 * g) = acc[d];
+    __syncthreads();
+    constexpr int EPT = D / 16;  // elements per thread: 16 threads a row
+    const int r = threadIdx.x / 16, e0 = (threadIdx.x % 16) * EPT;
+    if (r >= it.nrows) return;
+    float top = s_m[0][r], sum = 0.f, o[EPT];
+#pragma unroll
+    for (int x = 1; x < 4; ++x) top = fmaxf(top, s_m[x][r]);
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const float mx = s_m[x][r];
+        if (mx == -INFINITY) continue;
+        const float f = __builtin_amdgcn_exp2f(mx - top);
+        sum = fmaf(f, s_l[x][r], sum);
+        const float* p = reinterpret_cast<const float*>(lds[x][0]) + r * D + e0;
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) o[e] = fmaf(f, p[e], o[e]);
+    }
+    if (it.nsplits == 1) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row_off(a, it, it.row0 + r, head, a.ldo, D) + e0);
+#pragma unroll
+        for (int e = 0; e < EPT; e += 2) dst[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
+    } else {
+        const int64_t pr = head * a.part_rows + it.part + r;
+        float* dst = a.part + pr * D + e0;
+#pragma unroll
+        for (int e = 0; e < EPT; e += 4) *reinterpret_cast<f32x4_t*>(dst + e) = f32x4_t{o[e], o[e + 1], o[e + 2], o[e + 3]};
+        if (threadIdx.x % 16 == 0) {
+            float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D + 2 * pr;
+            ml[0] = top;
+            ml[1] = sum;
+        }
+    }
+}
+
+// Joins the splits of one row tile, in their order: D/4 lanes a row.
+template <int D>
+__global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
+    constexpr int LPR = D / 4, RPB = 256 / LPR, PARTS = AT_WIDE_ROWS / RPB;  // workgroups per tile and head
+    const int head = blockIdx.x % a.kv.n_kv_heads, block = blockIdx.x / a.kv.n_kv_heads;
+    Item it;
+    if (!load_item(a, block / PARTS, AT_WIDE_ROWS, it)) return;
+    if ((int64_t)it.part + (int64_t)it.nsplits * it.nrows > a.part_rows) return;
+    const int r = (block % PARTS) * RPB + threadIdx.x / LPR, e0 = 4 * (threadIdx.x % LPR);
+    if (r >= it.nrows) return;
+    const int64_t first = head * a.part_rows + it.part + r;
+    const float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D;
+    float top = -INFINITY;
+    for (int s = 0; s < it.nsplits; ++s) top = fmaxf(top, ml[2 * (first + (int64_t)s * it.nrows)]);
+    float sum = 0.f;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < it.nsplits; ++s) {
+        const int64_t pr = first + (int64_t)s * it.nrows;
+        const float mx = ml[2 * pr], lx = ml[2 * pr + 1];
+        const f32x4_t p = *reinterpret_cast<const f32x4_t*>(a.part + pr * D + e0);
+        if (mx == -INFINITY) continue;
+        const float f = __builtin_amdgcn_exp2f(mx - top);
+        sum = fmaf(f, lx, sum);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = fmaf(f, p[e], o[e]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<u32x2_t*>(a.out + row_off(a, it, it.row0 + r, head, a.ldo, D) + e0) =
+        u32x2_t{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+}
+
+// ------------------------------------------------------------------ launchers
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // of one launch (256 threads each: a grid holds under 2^32)
+
+template <typename A>
+hipError_t launch(void (*fn)(A), dim3 grid, dim3 block, hipStream_t s, A& args) {
+    void* p[] = {&args};
+    return hipLaunchKernel(reinterpret_cast<const void*>(fn), grid, block, p, 0, s);
+}
+
+int32_t check_kv(const lora_attn_launch_t* L, const lora_kv_t* c) {
+    if (!L || !c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return LORA_EINVAL;
+    const lora_attn_info_t& I = L->info;
+    const lora_attn_shape_t& s = I.shape;
+    if (I.n_seq < 0 || I.n_rows < 0 || I.n_tokens < 0 || (I.n_staged > 0 && !L->meta) || !aligned16(L->meta))
+        return LORA_EINVAL;
+    if (c->n_pages != s.n_pages || c->page_tokens != s.page_tokens || c->n_kv_heads != s.n_kv_heads ||
+        c->head_dim != s.head_dim || c->dtype != s.kv_dtype)
+        return LORA_ESHAPE;
+    if (s.head_dim != 64 && s.head_dim != 128) return LORA_ESHAPE;
+    if (s.n_kv_heads < 1 || s.n_heads < 1 || s.n_heads % s.n_kv_heads || s.page_tokens < 1 ||
+        (s.page_tokens & (s.page_tokens - 1)) || s.n_pages < 1)
+        return LORA_ESHAPE;
+    if (s.kv_dtype != LORA_KV_BF16 && s.kv_dtype != LORA_KV_E4M3) return LORA_EINVAL;
+    const int64_t per = s.kv_dtype == LORA_KV_E4M3 ? 16 : 8;
+    if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0 || c->page_stride % per ||
+        c->head_stride % per || c->token_stride % per)
+        return LORA_EINVAL;
+    if (s.kv_dtype == LORA_KV_E4M3 && (!c->k_scale || !c->v_scale)) return LORA_EINVAL;
+    return LORA_OK;
+}
+Kv to_kv(const lora_kv_t& c) {
+    return Kv{static_cast<const char*>(c.k), static_cast<const char*>(c.v), c.k_scale, c.v_scale, c.page_stride,
+              c.head_stride, c.token_stride, c.n_pages, __builtin_ctz((unsigned)c.page_tokens), c.n_kv_heads};
+}
+bool bad_rows(const void* p, int64_t ld, int64_t d) { return !p || !aligned16(p) || ld < d || ld % 8 != 0; }
+
+}  // namespace
+
+extern "C" int32_t lora_attn_prepare(const lora_attn_shape_t* shape, int32_t n_seq, const int32_t* q_len,
+                                     const int32_t* kv_len, const int32_t* block_table, int64_t ld_table,
+                                     int32_t* staging, int64_t staging_capacity, void* dev_staging, void* hip_stream,
+                                     lora_attn_launch_t* out) {
+    if (!out || !dev_staging || !aligned16(dev_staging)) return LORA_EINVAL;
+    const int32_t st = lora_attn_plan(shape, n_seq, q_len, kv_len, block_table, ld_table, staging, staging_capacity,
+                                      &out->info);
+    if (st != LORA_OK) return st;
+    out->meta = static_cast<const int32_t*>(dev_staging);
+    if (out->info.n_staged == 0) return LORA_OK;
+    const hipError_t e = hipMemcpyAsync(dev_staging, staging, (size_t)out->info.n_staged * sizeof(int32_t),
+                                        hipMemcpyHostToDevice, reinterpret_cast<hipStream_t>(hip_stream));
+    return e == hipSuccess ? LORA_OK : LORA_EHIP;
+}
+
+extern "C" int32_t lora_kv_write(const lora_attn_launch_t* L, const lora_kv_t* kv, const lora_kv_write_args_t* w,
+                                 void* hip_stream) {
+    const int32_t st = check_kv(L, kv);
+    if (st != LORA_OK) return st;
+    if (!w || (w->dtype != LORA_F32 && w->dtype != LORA_BF16)) return LORA_EINVAL;
+    const lora_attn_info_t& I = L->info;
+    if (I.n_rows == 0) return LORA_OK;
+    const int32_t d = I.shape.head_dim, hq = w->q ? I.shape.n_heads : 0, hk = I.shape.n_kv_heads;
+    if (bad_rows(w->k, w->ldk, (int64_t)hk * d) || bad_rows(w->v, w->ldv, (int64_t)hk * d)) return LORA_EINVAL;
+    if (w->q && (bad_rows(w->q, w->ldq, (int64_t)hq * d) || bad_rows(w->q_out, w->ld_out, (int64_t)hq * d)))
+        return LORA_EINVAL;
+    if (w->rope_dim < 0 || w->rope_dim > d || w->rope_dim % 16 != 0) return LORA_ESHAPE;
+    if ((w->rope_dim > 0) != (w->rope != nullptr) || !aligned16(w->rope)) return LORA_EINVAL;
+    if (w->rope && w->rope_len < I.max_kv) return LORA_EINVAL;
+    WriteArgs a;
+    memset(&a, 0, sizeof(a));
+    a.kv = to_kv(*kv);
+    a.q = w->q;
+    a.k = w->k;
+    a.v = w->v;
+    a.ldq = w->ldq;
+    a.ldk = w->ldk;
+    a.ldv = w->ldv;
+    a.rope = w->rope;
+    a.q_out = w->q_out;
+    a.ld_out = w->ld_out;
+    a.row_pos = L->meta + I.off_row_pos;
+    a.row_slot = L->meta + I.off_row_slot;
+    a.n_heads = hq;
+    a.n_vec = hq + 2 * hk;
+    a.n_rows = I.n_rows;
+    a.rope_dim = w->rope_dim;
+    a.rope_len = w->rope_len;
+    typedef void (*fn_t)(WriteArgs);
+    static const fn_t fn[2][2][2] = {
+        {{kv_write_kernel<64, false, false>, kv_write_kernel<64, false, true>},
+         {kv_write_kernel<64, true, false>, kv_write_kernel<64, true, true>}},
+        {{kv_write_kernel<128, false, false>, kv_write_kernel<128, false, true>},
+         {kv_write_kernel<128, true, false>, kv_write_kernel<128, true, true>}}};
+    const int vpb = 256 / (d / 8);
+    const unsigned gy = (unsigned)(I.n_rows < 32768 ? I.n_rows : 32768);
+    const dim3 grid((unsigned)((a.n_vec + vpb - 1) / vpb), gy, (unsigned)((I.n_rows + gy - 1) / gy));
+    const hipError_t e = launch(fn[d == 128][w->dtype == LORA_F32][kv->dtype == LORA_KV_E4M3], grid, dim3(256),
+                                reinterpret_cast<hipStream_t>(hip_stream), a);
+    return e == hipSuccess ? LORA_OK : LORA_EHIP;
+}
+
+extern "C" int32_t lora_kv_read(const lora_attn_launch_t* L, const lora_kv_t* kv, uint16_t* k_out, uint16_t* v_out,
+                                int64_t ld, void* hip_stream) {
+    const int32_t st = check_kv(L, kv);
+    if (st != LORA_OK) return st;
+    const lora_attn_info_t& I = L->info;
+    const int32_t d = I.shape.head_dim, hk = I.shape.n_kv_heads;
+    if (I.n_tokens == 0) return LORA_OK;
+    if (bad_rows(k_out, ld, (int64_t)hk * d) || bad_rows(v_out, ld, (int64_t)hk * d)) return LORA_EINVAL;
+    ReadArgs a{to_kv(*kv), k_out, v_out, ld, L->meta + I.off_kv_start, L->meta + I.off_table, I.n_seq, I.n_tokens,
+               I.ld_table};
+    typedef void (*fn_t)(ReadArgs);
+    static const fn_t fn[2][2] = {{kv_read_kernel<64, false>, kv_read_kernel<64, true>},
+                                  {kv_read_kernel<128, false>, kv_read_kernel<128, true>}};
+    const int64_t vpb = 256 / (d / 8), blocks = ((int64_t)I.n_tokens * hk + vpb - 1) / vpb;
+    const hipError_t e = launch(fn[d == 128][kv->dtype == LORA_KV_E4M3],
+                                dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256),
+                                reinterpret_cast<hipStream_t>(hip_stream), a);
+    return e == hipSuccess ? LORA_OK : LORA_EHIP;
+}
+
+extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, const uint16_t* q, int64_t ldq,
+                             uint16_t* out, int64_t ldo, float scale, float* workspace, int64_t workspace_floats,
+                             void* hip_stream) {
+    const int32_t st = check_kv(L, kv);
+    if (st != LORA_OK) return st;
+    const lora_attn_info_t& I = L->info;
+    const int32_t d = I.shape.head_dim, hk = I.shape.n_kv_heads;
+    const int64_t width = (int64_t)I.shape.n_heads * d;
+    if (I.n_rows == 0) return LORA_OK;
+    if (bad_rows(q, ldq, width) || bad_rows(out, ldo, width)) return LORA_EINVAL;
+    if (!(scale > 0.f) || !(scale < INFINITY)) return LORA_EINVAL;
+    if (I.workspace_floats > 0) {
+        if (workspace_floats < I.workspace_floats) return LORA_ECAPACITY;
+        if (!workspace || !aligned16(workspace)) return LORA_EINVAL;
+    }
+    const int64_t parts = AT_WIDE_ROWS / (256 / (d / 4));  // merge workgroups per row tile and head
+    for (const int64_t n : {(int64_t)I.n_work[0], (int64_t)I.n_work[1], I.n_merge * parts})
+        if (n < 0 || n * hk > kMaxBlocks) return LORA_EINVAL;
+    AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.kv = to_kv(*kv);
+    a.q_start = L->meta + I.off_q_start;
+    a.kv_len = L->meta + I.off_kv_len;
+    a.table = L->meta + I.off_table;
+    a.q = q;
+    a.out = out;
+    a.part = workspace;
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.part_rows = I.part_rows;
+    a.n_seq = I.n_seq;
+    a.ld_table = I.ld_table;
+    a.group = I.shape.n_heads / hk;
+    a.window = I.shape.window;
+    a.sinks = I.shape.sinks;
+    a.sl2 = scale * kLog2e;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+    const bool e4m3 = kv->dtype == LORA_KV_E4M3;
+    typedef void (*fn_t)(AttnArgs);
+    static const fn_t fn[2][2][2] = {
+        {{attn_narrow_kernel<64, false>, attn_narrow_kernel<64, true>},
+         {attn_narrow_kernel<128, false>, attn_narrow_kernel<128, true>}},
+        {{attn_wide_kernel<64, false>, attn_wide_kernel<64, true>},
+         {attn_wide_kernel<128, false>, attn_wide_kernel<128, true>}}};
+    for (int kind = 1; kind >= 0; --kind) {  // the longer items first
+        if (I.n_work[kind] == 0) continue;
+        a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_work[kind]);
+        a.n_work = I.n_work[kind];
+        if (launch(fn[kind][d == 128][e4m3], dim3((unsigned)(a.n_work * hk)), dim3(256), s, a) != hipSuccess)
+            return LORA_EHIP;
+    }
+    if (I.n_merge > 0) {
+        a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_merge);
+        a.n_work = I.n_merge;
+        const dim3 grid((unsigned)((int64_t)hk * I.n_merge * parts));
+        if (launch(d == 128 ? attn_merge_kernel<128> : attn_merge_kernel<64>, grid, dim3(256), s, a) != hipSuccess)
+            return LORA_EHIP;
+    }
+    return LORA_OK;
+}

@@ -1,0 +1,176 @@
+// Host planner of the attention over a paged cache: batch metadata and work
+// items.  Plain C++17 with no HIP dependency, like host.cpp.
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "../../include/hetlora.h"
+#include "attn_rules.h"
+
+namespace {
+
+// Workgroups that the chip works on at once: 256 compute units, two each.
+constexpr int64_t kSlots = 512;
+// Fewest tiles of one split: below four (256 tokens) a split's partial result
+// costs more than the tiles it takes off the longest workgroup.
+constexpr int64_t kMinTiles = 4;
+
+struct Tile {  // one row tile of one sequence before it is split
+    int32_t seq, row0, nrows, tiles;
+};
+
+int32_t check_shape(const lora_attn_shape_t& s) {
+    if (s.n_heads < 1 || s.n_kv_heads < 1 || s.n_pages < 1 || s.window < 0 || s.sinks < 0) return LORA_EINVAL;
+    if (s.kv_dtype != LORA_KV_BF16 && s.kv_dtype != LORA_KV_E4M3) return LORA_EINVAL;
+    if ((s.head_dim != 64 && s.head_dim != 128) || s.n_heads % s.n_kv_heads != 0 || s.n_kv_heads > 65535)
+        return LORA_ESHAPE;
+    if (s.page_tokens < 1 || s.page_tokens > 1024 || (s.page_tokens & (s.page_tokens - 1)) != 0) return LORA_ESHAPE;
+    if ((int64_t)s.n_pages * s.page_tokens > INT32_MAX) return LORA_EINVAL;
+    return LORA_OK;
+}
+
+// Cuts every row tile of `kind` into splits of about equal tiles, so that all
+// heads' splits together fill the chip, and appends items and merges.
+void split(const std::vector<Tile>& tiles, int32_t n_kv_heads, std::vector<lora_attn_work_t>& work,
+           std::vector<lora_attn_work_t>& merge, int64_t& part_rows) {
+    int64_t total = 0;
+    for (const Tile& t : tiles) total += t.tiles;
+    const int64_t most = std::max(kMinTiles, (total * n_kv_heads + kSlots - 1) / kSlots);
+    for (const Tile& t : tiles) {
+        const int32_t n = (int32_t)std::max<int64_t>(1, (t.tiles + most - 1) / most);
+        const int32_t first = (int32_t)part_rows;
+        for (int32_t s = 0; s < n; ++s) {
+            const int32_t it0 = (int32_t)((int64_t)t.tiles * s / n), it1 = (int32_t)((int64_t)t.tiles * (s + 1) / n);
+            work.push_back({t.seq, t.row0, t.nrows, it0, it1, s, n, n > 1 ? (int32_t)part_rows : -1});
+            if (n > 1) part_rows += t.nrows;
+        }
+        if (n > 1) merge.push_back({t.seq, t.row0, t.nrows, 0, 0, 0, n, first});
+    }
+    // longest first, so that the last workgroups to start are short
+    std::stable_sort(work.begin(), work.end(), [](const lora_attn_work_t& a, const lora_attn_work_t& b) {
+        return a.it1 - a.it0 > b.it1 - b.it0;
+    });
+}
+
+int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_len, const int32_t* kv_len,
+                  const int32_t* table, int64_t ld_table, int32_t* staging, int64_t capacity,
+                  lora_attn_info_t* info) {
+    const int32_t group = s.n_heads / s.n_kv_heads;
+    int64_t n_rows = 0, n_tokens = 0;
+    int32_t pages = 0, max_kv = 0;
+    for (int32_t b = 0; b < n_seq; ++b) {
+        if (q_len[b] < 0 || kv_len[b] < 0 || kv_len[b] > (1 << 30) || q_len[b] > (1 << 30)) return LORA_EINVAL;
+        n_rows += q_len[b];
+        n_tokens += kv_len[b];
+        if ((int64_t)q_len[b] * group > INT32_MAX / 2) return LORA_EINVAL;
+        const int32_t need = (kv_len[b] + s.page_tokens - 1) / s.page_tokens;
+        if (need > ld_table) return LORA_EINVAL;
+        pages = std::max(pages, need);
+        max_kv = std::max(max_kv, kv_len[b]);
+    }
+    if (n_rows * group > INT32_MAX / 2 || n_tokens > INT32_MAX) return LORA_EINVAL;
+    if (pages > 0 && table == nullptr) return LORA_EINVAL;
+    for (int32_t b = 0; b < n_seq; ++b) {
+        const int32_t need = (kv_len[b] + s.page_tokens - 1) / s.page_tokens;
+        const int32_t* row = table + (need ? b * ld_table : 0);
+        for (int32_t i = 0; i < need; ++i)
+            if (row[i] < 0 || row[i] >= s.n_pages) return LORA_EPAGE;
+    }
+
+    std::vector<Tile> tiles[2];
+    for (int32_t b = 0; b < n_seq; ++b) {
+        const int32_t rows = q_len[b] * group, p0 = kv_len[b] - q_len[b];
+        const int kind = rows <= AT_NARROW_ROWS ? LORA_ATTN_NARROW : LORA_ATTN_WIDE;
+        const int32_t step = kind == LORA_ATTN_NARROW ? AT_NARROW_ROWS : AT_WIDE_ROWS;
+        for (int32_t r = 0; r < rows; r += step) {
+            const int32_t n = std::min(step, rows - r);
+            const AtSpan sp = at_span(p0 + r / group, p0 + (r + n - 1) / group, s.window, s.sinks);
+            tiles[kind].push_back({b, r, n, at_span_tiles(sp)});
+        }
+    }
+    std::vector<lora_attn_work_t> work[2], merge;
+    int64_t part_rows = 0;
+    for (int kind = 0; kind < 2; ++kind) split(tiles[kind], s.n_kv_heads, work[kind], merge, part_rows);
+
+    if (part_rows > INT32_MAX) return LORA_EINVAL;
+    constexpr int64_t wi = sizeof(lora_attn_work_t) / sizeof(int32_t);
+    lora_attn_info_t out;
+    memset(&out, 0, sizeof(out));
+    out.shape = s;
+    out.n_seq = n_seq;
+    out.n_rows = (int32_t)n_rows;
+    out.n_tokens = (int32_t)n_tokens;
+    out.max_kv = max_kv;
+    out.ld_table = pages;
+    out.n_merge = (int32_t)merge.size();
+    out.part_rows = part_rows;
+    out.workspace_floats = part_rows * s.n_kv_heads * (s.head_dim + 2);
+    int64_t off = 0;
+    const auto place = [&off](int64_t n) {  // parts start at multiples of four elements (16 bytes)
+        const int64_t at = off;
+        off += (n + 3) / 4 * 4;
+        return at;
+    };
+    for (int kind = 0; kind < 2; ++kind) {
+        out.n_work[kind] = (int32_t)work[kind].size();
+        out.off_work[kind] = place(wi * out.n_work[kind]);
+    }
+    out.off_merge = place(wi * out.n_merge);
+    out.off_q_start = place(n_seq + 1);
+    out.off_kv_len = place(n_seq);
+    out.off_kv_start = place(n_seq + 1);
+    out.off_row_pos = place(n_rows);
+    out.off_row_slot = place(n_rows);
+    out.off_table = place((int64_t)n_seq * pages);
+    out.n_staged = off;
+    *info = out;
+    if (off > capacity) return LORA_ECAPACITY;
+    if (off > 0 && staging == nullptr) return LORA_EINVAL;
+
+    const auto put = [staging](int64_t at, const std::vector<lora_attn_work_t>& v) {
+        if (!v.empty()) memcpy(staging + at, v.data(), v.size() * sizeof(lora_attn_work_t));
+    };
+    for (int kind = 0; kind < 2; ++kind) put(out.off_work[kind], work[kind]);
+    put(out.off_merge, merge);
+    int32_t *q_start = staging + out.off_q_start, *kv_start = staging + out.off_kv_start;
+    int32_t row = 0, token = 0;
+    for (int32_t b = 0; b < n_seq; ++b) {
+        q_start[b] = row;
+        kv_start[b] = token;
+        staging[out.off_kv_len + b] = kv_len[b];
+        const int32_t* src = table + (pages ? b * ld_table : 0);
+        for (int32_t i = 0; i < q_len[b]; ++i, ++row) {
+            const int32_t p = kv_len[b] - q_len[b] + i;
+            staging[out.off_row_pos + row] = p;
+            staging[out.off_row_slot + row] =
+                p < 0 ? -1 : src[p / s.page_tokens] * s.page_tokens + p % s.page_tokens;
+        }
+        token += kv_len[b];
+        const int32_t need = (kv_len[b] + s.page_tokens - 1) / s.page_tokens;
+        int32_t* dst = staging + out.off_table + (int64_t)b * pages;
+        if (need) memcpy(dst, src, sizeof(int32_t) * (size_t)need);
+        std::fill(dst + need, dst + pages, 0);
+    }
+    q_start[n_seq] = row;
+    kv_start[n_seq] = token;
+    return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" int32_t lora_attn_plan(const lora_attn_shape_t* shape, int32_t n_seq, const int32_t* q_len,
+                                  const int32_t* kv_len, const int32_t* block_table, int64_t ld_table,
+                                  int32_t* staging, int64_t staging_capacity, lora_attn_info_t* info) {
+    if (!shape || !info || n_seq < 0 || ld_table < 0 || staging_capacity < 0 || (n_seq > 0 && (!q_len || !kv_len)))
+        return LORA_EINVAL;
+    const int32_t st = check_shape(*shape);
+    if (st != LORA_OK) return st;
+    try {
+        return plan_impl(*shape, n_seq, q_len, kv_len, block_table, ld_table, staging, staging_capacity, info);
+    } catch (const std::bad_alloc&) {
+        return LORA_ENOMEM;
+    }
+}

@@ -1,0 +1,39 @@
+// Rules of the attention plan that the host planner and the kernels share:
+// how a range of query positions maps to tiles of cached tokens.  Plain
+// C/C++ with no HIP dependency.
+#ifndef HETLORA_ATTN_RULES_H
+#define HETLORA_ATTN_RULES_H
+
+#include <stdint.h>
+
+#ifndef AT_FN
+#define AT_FN static inline
+#endif
+
+#define AT_TILE 64          // cached tokens of one tile
+#define AT_WIDE_ROWS 128    // query rows of one item of the wide kernel
+#define AT_NARROW_ROWS 16   // and of the narrow one
+
+// Tiles that queries at positions p_lo .. p_hi may see, as a list: the first
+// `sinks` tiles 0 .. sinks-1, then `first` .. `end`-1.
+struct AtSpan {
+    int32_t sinks, first, end;
+};
+
+AT_FN int32_t at_min(int32_t a, int32_t b) { return a < b ? a : b; }
+AT_FN int32_t at_max(int32_t a, int32_t b) { return a > b ? a : b; }
+
+AT_FN struct AtSpan at_span(int32_t p_lo, int32_t p_hi, int32_t window, int32_t sinks) {
+    struct AtSpan s = {0, 0, 0};
+    if (p_hi < 0) return s;
+    s.end = p_hi / AT_TILE + 1;
+    if (window > 0) {
+        s.first = at_max(0, p_lo - window + 1) / AT_TILE;
+        s.sinks = at_min((int32_t)(((int64_t)sinks + AT_TILE - 1) / AT_TILE), s.first);
+    }
+    return s;
+}
+AT_FN int32_t at_span_tiles(struct AtSpan s) { return s.sinks + s.end - s.first; }
+AT_FN int32_t at_span_tile(struct AtSpan s, int32_t i) { return i < s.sinks ? i : s.first + (i - s.sinks); }
+
+#endif

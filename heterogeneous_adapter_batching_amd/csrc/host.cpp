@@ -29,6 +29,8 @@ extern "C" const char* lora_status_string(int32_t status) {
         case LORA_ESHAPE: return "dimension or chunk length not a positive multiple of 64";
         case LORA_ECAPACITY: return "output capacity too small";
         case LORA_EHIP: return "HIP launch error";
+        case LORA_EPAGE: return "page id out of range";
+        case LORA_ENOMEM: return "out of host memory";
         default: return "unknown status";
     }
 }

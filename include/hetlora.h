@@ -73,7 +73,7 @@
 extern "C" {
 #endif
 
-#define LORA_ABI_VERSION 10
+#define LORA_ABI_VERSION 11
 #define LORA_MAX_RANK 128   /* ranks are 1..128                              */
 #define LORA_MAX_PROJ 8     /* projections per shrink/expand call            */
 #define LORA_MAX_RANGES 48  /* kernel variants in one plan                   */
@@ -89,6 +89,8 @@ extern "C" {
 #define LORA_ESHAPE    -4  /* d_in / d_out / chunk_len not a positive multiple of 64   */
 #define LORA_ECAPACITY -5  /* an output capacity is too small                          */
 #define LORA_EHIP      -6  /* a HIP launch reported an error                           */
+#define LORA_EPAGE     -7  /* page id outside [0, n_pages)                             */
+#define LORA_ENOMEM    -8  /* host memory ran out                                      */
 
 #define LORA_OP_SHRINK 0
 #define LORA_OP_EXPAND 1
@@ -628,6 +630,213 @@ int32_t lora_pool_load_list(const lora_pool_t* pool, int32_t n, const int32_t* a
 int32_t lora_pool_scatter(const uint16_t* src, uint16_t* pool, int64_t n,
                           const int64_t* src_off, const int64_t* dst_off, const int32_t* len,
                           void* hip_stream);
+
+/* ------------------------------------------------------------------ paged cache and attention
+ * What lies between the q/k/v projections' lora_apply and the o projection's
+ * in a layer: the new tokens' k and v go into a paged cache (S-LoRA article,
+ * "Unified Paging": a sequence of S tokens occupies pages of the pool beside
+ * the adapters'), and the new tokens' queries attend over it.
+ *
+ * A batch has n_seq sequences.  Sequence b brings q_len[b] new tokens (rows of
+ * q, k, v and out, in order, sequence after sequence) and has kv_len[b] tokens
+ * in the cache with them; row i of b is token p = kv_len[b] - q_len[b] + i.
+ *
+ *   write  k and v of row i go to token p of b; q and k are first turned by
+ *          the angles of p on their first rope_dim elements (element c with
+ *          element c + rope_dim/2); q is rounded to bf16
+ *   attn   out_i = sum_j w_ij v_j,  w_ij = exp(scale q_i . k_j) / sum over
+ *          the tokens j that row i sees: j <= p, and with a window > 0 also
+ *          (j > p - window or j < sinks).  A row that sees nothing, or whose
+ *          weights sum to zero, is zero.  n_heads query heads share
+ *          n_kv_heads key and value heads: head h reads kv head
+ *          h / (n_heads / n_kv_heads)
+ *   read   the cached values of all kv_len[b] tokens, sequence after sequence
+ *
+ * Rows with p < 0 (q_len above kv_len) see nothing and are not written to the
+ * cache.  What is in the cache past kv_len, or hidden from a row, does not
+ * reach that row's output, be it infinite or NaN. */
+
+#define LORA_KV_BF16 0      /* cached values are bf16                                   */
+#define LORA_KV_E4M3 1      /* e4m3 codes, one power of two per (token, kv head)        */
+#define LORA_F32 0          /* types of the write's inputs                              */
+#define LORA_BF16 1
+
+/* A layer's cache.  Token t of page p, kv head h starts at element
+ * p * page_stride + h * head_stride + t * token_stride of k and of v; its
+ * head_dim elements are contiguous.
+ *   k, v     device, 16-byte aligned; strides in elements, multiples of 8
+ *            (bf16) or 16 (e4m3), not negative
+ *   k_scale, v_scale  LORA_KV_E4M3: device uint8 [n_pages][n_kv_heads]
+ *            [page_tokens], exponents e biased by 127 (the e8m0 type): a
+ *            cached value is code * 2^e.  lora_kv_write takes the least e with
+ *            |x| <= 448 * 2^e over the finite x of the head's row, in
+ *            [-100, 119], so that every value is exact in bf16; a code is
+ *            the nearest e4m3 value (ties to even), values beyond 448 * 2^e
+ *            take that, infinities and NaN become NaN.  LORA_KV_BF16: NULL */
+typedef struct lora_kv {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int32_t dtype;              /* LORA_KV_*                                 */
+    int32_t n_pages;
+    int32_t page_tokens;        /* tokens of a page: a power of two, 1..1024 */
+    int32_t n_kv_heads;
+    int32_t head_dim;           /* 64 or 128                                 */
+    int32_t reserved;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t token_stride;
+} lora_kv_t;
+
+/* What a plan is made for. */
+typedef struct lora_attn_shape {
+    int32_t n_heads;            /* a multiple of n_kv_heads                  */
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_tokens;
+    int32_t n_pages;
+    int32_t kv_dtype;
+    int32_t window;             /* tokens a row sees, itself among them; 0: all */
+    int32_t sinks;              /* first tokens that stay visible with a window */
+} lora_attn_shape_t;
+
+/* One unit of attention work, for every kv head: rows [row0, row0 + nrows) of
+ * sequence `seq`, where row r is query head r % group of the kv head's group
+ * at new token r / group, over the tiles [it0, it1) of 64 tokens in the list
+ * of tiles that these rows may see.  With nsplits > 1 the partial result goes
+ * to rows part.. of the workspace; a merge entry (it0 = it1 = 0, part = the
+ * first split's) joins the splits of one row tile. */
+typedef struct lora_attn_work {
+    int32_t seq;
+    int32_t row0;
+    int32_t nrows;
+    int32_t it0;
+    int32_t it1;
+    int32_t split;
+    int32_t nsplits;
+    int32_t part;
+} lora_attn_work_t;
+
+#define LORA_ATTN_NARROW 0  /* kernels: up to 16 rows, four waves share the tokens */
+#define LORA_ATTN_WIDE 1    /* up to 128 rows, four waves share the rows           */
+
+/* Host-side summary of an attention plan, and where its parts lie in the
+ * staging buffer (off_*, in int32 elements). */
+typedef struct lora_attn_info {
+    lora_attn_shape_t shape;
+    int32_t n_seq;
+    int32_t n_rows;             /* rows of q, k, v and out                   */
+    int32_t n_tokens;           /* rows of lora_kv_read's outputs            */
+    int32_t max_kv;             /* longest kv_len                            */
+    int32_t ld_table;           /* pages per sequence in the staged table    */
+    int32_t n_work[2];          /* items by kernel (LORA_ATTN_*)             */
+    int32_t n_merge;
+    int64_t part_rows;          /* rows of partial results per kv head       */
+    int64_t workspace_floats;   /* fp32 elements lora_attn needs             */
+    int64_t off_work[2];        /* lora_attn_work_t [n_work[kind]]           */
+    int64_t off_merge;          /* lora_attn_work_t [n_merge]                */
+    int64_t off_q_start;        /* [n_seq + 1] first row of each sequence    */
+    int64_t off_kv_len;         /* [n_seq]                                   */
+    int64_t off_kv_start;       /* [n_seq + 1] first output row of the read  */
+    int64_t off_row_pos;        /* [n_rows] token each row is                */
+    int64_t off_row_slot;       /* [n_rows] page * page_tokens + place, or -1 */
+    int64_t off_table;          /* [n_seq][ld_table] page ids                */
+    int64_t n_staged;           /* int32 elements in all                     */
+} lora_attn_info_t;
+
+/* What the calls below need to launch one plan. */
+typedef struct lora_attn_launch {
+    const int32_t* meta;        /* device copy of the staging buffer         */
+    lora_attn_info_t info;
+} lora_attn_launch_t;
+
+/* Attention plan of a batch (host only): validates the batch, lists the work
+ * items (row tiles, split over their tokens where there are too few of them
+ * to fill the chip, so that all splits take about as long) and lays out
+ * everything the kernels read in one buffer.
+ *   q_len, kv_len  host int32 [n_seq], 0 .. 2^30
+ *   block_table    host int32 [n_seq][ld_table]: page of tokens
+ *                  [i * page_tokens, (i + 1) * page_tokens) of each sequence;
+ *                  entries past its last token are not read.  May be NULL when
+ *                  every kv_len is 0
+ *   staging        host int32 [staging_capacity]
+ * Errors: LORA_EINVAL (null pointer, negative or too large count, a kv_len
+ * that the table does not hold), LORA_ESHAPE (head_dim, page_tokens, or
+ * n_heads not a multiple of n_kv_heads), LORA_EPAGE, LORA_ECAPACITY (info is
+ * written: n_staged holds the size needed), LORA_ENOMEM. */
+int32_t lora_attn_plan(const lora_attn_shape_t* shape, int32_t n_seq,
+                       const int32_t* q_len, const int32_t* kv_len,
+                       const int32_t* block_table, int64_t ld_table,
+                       int32_t* staging, int64_t staging_capacity,
+                       lora_attn_info_t* info);
+
+/* lora_attn_plan, and the staging buffer's copy to dev_staging (device,
+ * 16-byte aligned, as large) enqueued on hip_stream; `staging` is as in
+ * lora_batch_prepare.  out is ready for the calls below; one plan serves every
+ * layer of a step whose caches have the same shape.  Errors: as
+ * lora_attn_plan, LORA_EHIP. */
+int32_t lora_attn_prepare(const lora_attn_shape_t* shape, int32_t n_seq,
+                          const int32_t* q_len, const int32_t* kv_len,
+                          const int32_t* block_table, int64_t ld_table,
+                          int32_t* staging, int64_t staging_capacity,
+                          void* dev_staging, void* hip_stream,
+                          lora_attn_launch_t* out);
+
+/* Inputs of the write.
+ *   q, k, v  device, of `dtype` (LORA_F32 or LORA_BF16), rows of
+ *            n_heads * head_dim (q) or n_kv_heads * head_dim elements, ld
+ *            apart; 16-byte aligned, ld a multiple of 8.  q may be NULL: then
+ *            only k and v are written
+ *   rope     device fp32 [rope_len][rope_dim]: cosines, then sines, of the
+ *            rope_dim / 2 angles of each position; rope_len >= info.max_kv.
+ *            NULL with rope_dim 0: nothing is turned
+ *   q_out    device bf16, rows of n_heads * head_dim, ld_out apart, aligned as
+ *            the inputs (with q only); rows with p < 0 are zero           */
+typedef struct lora_kv_write_args {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t ldq;
+    int64_t ldk;
+    int64_t ldv;
+    const float* rope;
+    uint16_t* q_out;
+    int64_t ld_out;
+    int32_t dtype;
+    int32_t rope_len;
+    int32_t rope_dim;           /* 0, or a multiple of 16 up to head_dim     */
+    int32_t reserved;
+} lora_kv_write_args_t;
+
+/* Write the batch's new tokens into the cache, one launch.  Two rows of a
+ * batch must not be the same token of the same page.  Errors: LORA_EINVAL,
+ * LORA_ESHAPE (the cache is not the plan's shape; rope_dim), LORA_EHIP. */
+int32_t lora_kv_write(const lora_attn_launch_t* launch, const lora_kv_t* kv,
+                      const lora_kv_write_args_t* args, void* hip_stream);
+
+/* Read all tokens of the batch's sequences back as bf16 (exact for both
+ * cache types): k_out and v_out device bf16 [info.n_tokens] rows of n_kv_heads
+ * * head_dim elements, ld apart, 16-byte aligned, ld % 8 == 0.  Errors: as
+ * lora_kv_write. */
+int32_t lora_kv_read(const lora_attn_launch_t* launch, const lora_kv_t* kv,
+                     uint16_t* k_out, uint16_t* v_out, int64_t ld, void* hip_stream);
+
+/* Attention of the batch's rows over the cache.
+ *   q      device bf16 [info.n_rows] rows of n_heads * head_dim, ldq apart,
+ *          16-byte aligned, ldq % 8 == 0
+ *   out    device bf16, the same layout with ldo; must not overlap q
+ *   scale  > 0, finite
+ *   workspace  device fp32 [workspace_floats >= info.workspace_floats],
+ *          16-byte aligned; may be NULL when info.workspace_floats is 0.
+ *          Calls that overlap in time need one each
+ * Scores and weights' sums are fp32; the weights enter the product with v as
+ * bf16, and the same rounded weights are summed.  Results do not depend on
+ * the launch order.  Errors: as lora_kv_write; LORA_ECAPACITY (workspace). */
+int32_t lora_attn(const lora_attn_launch_t* launch, const lora_kv_t* kv,
+                  const uint16_t* q, int64_t ldq, uint16_t* out, int64_t ldo,
+                  float scale, float* workspace, int64_t workspace_floats,
+                  void* hip_stream);
 
 #ifdef __cplusplus
 }
