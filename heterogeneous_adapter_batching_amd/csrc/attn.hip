@@ -323,53 +323,131 @@ __device__ __forceinline__ int k_chunk(int row, int c) { return c ^ (row & (D / 
 template <int D>
 __device__ __forceinline__ int v_chunk(int row, int c) { return c ^ (2 * (row & (D / 16 - 1))); }
 
-// Tokens [t0, t0 + ROWS) of one kv head on their way from the cache to LDS, 8
-// elements per lane and step.  Tokens past the end of the sequence take its
-// last token's place: nothing sees them.
-template <int D, bool E4M3, int ROWS, int NT>
-struct Stage {
-    static constexpr int CPR = D / 8, RPS = NT / CPR, STEPS = ROWS / RPS;
-    typedef typename std::conditional<E4M3, u32x2_t, u32x4_t>::type raw_t;
-    raw_t k[STEPS], v[STEPS];
-    uint32_t ke[STEPS], ve[STEPS];
+// Wave-uniform read of a page id through the scalar cache (the table is read-only
+// for the whole launch).
+__device__ __forceinline__ int32_t ld_uniform(const int32_t* p, int32_t i) {
+    return ((const __attribute__((address_space(4))) int32_t*)p)[i];
+}
 
-    __device__ __forceinline__ void load(const Kv& c, const Item& it, int head, int t0, int t) {
-        const int chunk = t % CPR;
-        int32_t page[STEPS], place[STEPS];
+// 16 bytes per lane from memory to LDS, past the registers: lane i's go to lds +
+// 16 i.  They have arrived after wait_loads().  Written in assembly because the
+// compiler, which cannot tell one half of LDS from the other behind the
+// transposing reads, would wait for the next tile's copies before reading this
+// one's; there is no register result that it could misplace.
+__device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void copy_to_lds(const char* from, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_addr(const char* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+
+// Tokens [t0, t0 + ROWS) of one kv head on their way from the cache to LDS: NT
+// lanes (t of them, waves of 64 from `wave`) move 8 elements each a step, RPS
+// rows.  Tokens past the end of the sequence take its last token's place:
+// nothing sees them.
+//
+// UNI: a page holds RPS tokens at least, so a step's rows lie in one page, whose
+// address is scalar, and the strides fit 32 bits; otherwise every lane looks its
+// own page up.
+//
+// DIRECT: bf16 rows go straight to LDS, the permutation of a row's chunks made
+// by the lanes' source addresses.  Otherwise they go through registers, and e4m3
+// codes become bf16 (exactly) on the way.
+template <int D, bool E4M3, bool UNI, bool DIRECT, int ROWS, int NT>
+struct Stage {
+    static_assert(!(E4M3 && DIRECT), "codes are converted on the way");
+    static constexpr int CPR = D / 8, RPS = NT / CPR, STEPS = ROWS / RPS, HELD = DIRECT ? 1 : STEPS, ES = E4M3 ? 1 : 2;
+    typedef typename std::conditional<E4M3, u32x2_t, u32x4_t>::type raw_t;
+    const char *kbase, *vbase;  // the head's first element
+    const int32_t* table;
+    int32_t t, wave, kv;
+    uint32_t row_bytes, page_bytes;
+    int32_t page[STEPS];
+    raw_t k[HELD], v[HELD];
+    uint32_t ke[E4M3 ? STEPS : 1], ve[E4M3 ? STEPS : 1];
+
+    __device__ __forceinline__ void init(const Kv& c, const Item& it, int head, int lane, int wave_) {
+        kbase = c.k + head * c.head_stride * ES;
+        vbase = c.v + head * c.head_stride * ES;
+        table = it.table;
+        t = lane;
+        wave = wave_;
+        kv = it.kv;
+        row_bytes = (uint32_t)c.token_stride * ES;
+        page_bytes = (uint32_t)c.page_stride * ES;
+    }
+    // the pages of a tile, some time before its load
+    __device__ __forceinline__ void look_up(const Kv& c, int t0) {
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            const int tok = min(t0 + s * RPS + t / CPR, it.kv - 1);
-            page[s] = it.table[tok >> c.page_shift];
-            place[s] = tok & ((1 << c.page_shift) - 1);
-        }
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int32_t pg = clamp_page(c, page[s]);
-            const int64_t off = kv_off(c, pg, head, place[s]) + 8 * chunk;
-            k[s] = *reinterpret_cast<const raw_t*>(c.k + off * (E4M3 ? 1 : 2));
-            v[s] = *reinterpret_cast<const raw_t*>(c.v + off * (E4M3 ? 1 : 2));
-            if constexpr (E4M3) {
-                const int64_t so = scale_off(c, pg, head, place[s]);
-                ke[s] = c.k_scale[so];
-                ve[s] = c.v_scale[so];
-            }
+            if constexpr (UNI) page[s] = ld_uniform(table, min(t0 + s * RPS, kv - 1) >> c.page_shift);
+            else page[s] = table[min(t0 + s * RPS + t / CPR, kv - 1) >> c.page_shift];
         }
     }
-    __device__ __forceinline__ void store(char* kt, char* vt, int t) const {
-        const int chunk = t % CPR;
+    __device__ __forceinline__ void load(const Kv& c, int head, int t0, char* kt, char* vt) {
+        const int mask = (1 << c.page_shift) - 1;
+        const uint32_t lane_row = (t / CPR) * row_bytes;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             const int row = s * RPS + t / CPR;
-            u32x4_t kk, vv;
-            if constexpr (E4M3) {
-                kk = dequant8(k[s], scale_of(ke[s]));
-                vv = dequant8(v[s], scale_of(ve[s]));
+            const int first = min(t0 + s * RPS, kv - 1), tok = min(t0 + row, kv - 1);
+            const int32_t pg = clamp_page(c, page[s]);
+            const int kc = (DIRECT ? k_chunk<D>(row, t % CPR) : t % CPR) * 8 * ES;
+            const int vc = (DIRECT ? v_chunk<D>(row, t % CPR) : t % CPR) * 8 * ES;
+            const uint32_t to = s * RPS * (2 * D) + wave * 1024;
+            if constexpr (UNI) {
+                // scalar: the step's first row; by lane: its row and chunk
+                const uint64_t base = (uint64_t)(uint32_t)pg * page_bytes + (uint64_t)(uint32_t)(first & mask) * row_bytes;
+                uint32_t at = lane_row;
+                if (t0 + (s + 1) * RPS > kv) at = (uint32_t)(tok - first) * row_bytes;
+                if constexpr (DIRECT) {
+                    copy_to_lds(kbase + base, at + kc, lds_addr(kt) + to);
+                    copy_to_lds(vbase + base, at + vc, lds_addr(vt) + to);
+                } else {
+                    k[s] = *reinterpret_cast<const raw_t*>(kbase + base + (at + kc));
+                    v[s] = *reinterpret_cast<const raw_t*>(vbase + base + (at + vc));
+                }
             } else {
-                kk = k[s];
-                vv = v[s];
+                const int64_t at = ES * (pg * c.page_stride + (tok & mask) * c.token_stride);
+                if constexpr (DIRECT) {
+                    copy_to_lds(kbase + at + kc, lds_addr(kt) + to);
+                    copy_to_lds(vbase + at + vc, lds_addr(vt) + to);
+                } else {
+                    k[s] = *reinterpret_cast<const raw_t*>(kbase + at + kc);
+                    v[s] = *reinterpret_cast<const raw_t*>(vbase + at + vc);
+                }
             }
-            *reinterpret_cast<u32x4_t*>(kt + row * (2 * D) + 16 * k_chunk<D>(row, chunk)) = kk;
-            *reinterpret_cast<u32x4_t*>(vt + row * (2 * D) + 16 * v_chunk<D>(row, chunk)) = vv;
+            if constexpr (E4M3) {
+                const int64_t so = scale_off(c, pg, head, UNI ? first & mask : tok & mask);
+                ke[s] = (c.k_scale + so)[UNI ? (uint32_t)(tok - first) : 0u];
+                ve[s] = (c.v_scale + so)[UNI ? (uint32_t)(tok - first) : 0u];
+            }
+        }
+    }
+    // what load() has left in registers, or its end
+    __device__ __forceinline__ void store(char* kt, char* vt) const {
+        if constexpr (!DIRECT) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int row = s * RPS + t / CPR, chunk = t % CPR;
+                u32x4_t kk, vv;
+                if constexpr (E4M3) {
+                    kk = dequant8(k[s], scale_of(ke[s]));
+                    vv = dequant8(v[s], scale_of(ve[s]));
+                } else {
+                    kk = k[s];
+                    vv = v[s];
+                }
+                *reinterpret_cast<u32x4_t*>(kt + row * (2 * D) + 16 * k_chunk<D>(row, chunk)) = kk;
+                *reinterpret_cast<u32x4_t*>(vt + row * (2 * D) + 16 * v_chunk<D>(row, chunk)) = vv;
+            }
+        } else {
+            wait_loads();
         }
     }
 };
@@ -379,150 +457,189 @@ __device__ __forceinline__ float v_elem(const char* vt, int row_bytes, int row, 
                            << 16);
 }
 
-// Four waves, 32 rows each; tiles of 64 tokens go through LDS, the next one's
-// loads in flight while one is worked on.
+// One wave's rows in the wide kernel.
+struct WideRows {
+    int row, pos, p_lo, p_hi;  // this lane's row and its position; the wave's first and last position
+    bool active;
+};
+
+// One wave's 32 rows over one tile in LDS: scores, weights, and their product
+// with v added to acc (rows d of O^T), m and l brought up to date.
+template <int D, bool CAREFUL>
+__device__ __forceinline__ void wide_tile(const AttnArgs& a, const WideRows& wr, const u32x4_t (&qf)[D / 16],
+                                          const char* kt, const char* vt, int t0, f32x16_t (&acc)[D / 32], float& m,
+                                          float& l) {
+    constexpr int RB = 2 * D, DB = D / 32, KS = D / 16;
+    const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+    f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int r = 32 * b + col;
+            s[b] = mfma32(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 2 * ks + h)), qf[ks], s[b]);
+        }
+    const bool masked = !all_see(a, wr.p_lo, wr.p_hi, t0, t0 + AT_TILE - 1);
+    if (masked) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (!sees(a, wr.pos, t0 + 32 * b + 8 * (r >> 2) + 4 * h + (r & 3))) s[b][r] = -INFINITY;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+    if (__ballot(top * a.sl2 > m + kGrow)) {
+        const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
+        m = up;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) acc[d] *= f;
+    }
+    const float off = m == -INFINITY ? 0.f : -m;
+    uint32_t pw[16];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) {
+            const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
+            const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
+            const uint32_t pk = pack_bf16(p0, p1);
+            l = add_bf16_pair(pk, l);
+            pw[8 * b + r / 2] = pk;
+        }
+    if (CAREFUL && masked) {
+        // one pair of rows' weights after the other, each register moved down
+        // to the first: a rolled loop over registers
+#pragma unroll 1
+        for (int j = 0; j < 16; ++j) {
+            const uint32_t cur = pw[0];
+#pragma unroll
+            for (int k = 0; k < 15; ++k) pw[k] = pw[k + 1];
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t both = __shfl(cur, col + 32 * (x >> 1));
+                const float p = x & 1 ? bf16_hi(both) : bf16_lo(both);
+                const int r = 2 * (j & 7) + (x & 1);
+                const int tok = 32 * (j >> 3) + 8 * (r >> 2) + 4 * (x >> 1) + (r & 3);
+                const bool vis = sees(a, wr.pos, t0 + tok);
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int el = 32 * d + 8 * (e >> 2) + 4 * h + (e & 3);
+                        const float v = v_elem(vt, RB, tok, v_chunk<D>(tok, el >> 3), el & 7);
+                        acc[d][e] = vis ? fmaf(p, v, acc[d][e]) : acc[d][e];
+                    }
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const u32x4_t pf = {pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]};
+        const int i16 = lane & 15, g = (lane >> 4) & 1;
+        const int r = 16 * c + 4 * h + (i16 >> 2);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+            const int ch = 4 * d + 2 * g + ((i16 & 3) >> 1), by = 8 * (i16 & 1);
+            const u32x2_t lo = ds_tr16(vt + r * RB + 16 * v_chunk<D>(r, ch) + by);
+            const u32x2_t hi = ds_tr16(vt + (r + 8) * RB + 16 * v_chunk<D>(r + 8, ch) + by);
+            acc[d] = mfma32(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
+        }
+    }
+}
+
+// The item's tiles, the next one on its way to one half of LDS while the other
+// is worked on; true where the result is not finite.
+template <int D, bool E4M3, bool UNI, bool CAREFUL>
+__device__ __forceinline__ bool wide_pass(const AttnArgs& a, const Item& it, const WideRows& wr, int head,
+                                          const u32x4_t (&qf)[D / 16], char (&even)[2][AT_TILE * 2 * D],
+                                          char (&odd)[2][AT_TILE * 2 * D], f32x16_t (&acc)[D / 32], float& m, float& l) {
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) acc[d] = f32x16_t{};
+    m = -INFINITY;
+    l = 0.f;
+    Stage<D, E4M3, UNI, !E4M3, AT_TILE, 256> st;
+    st.init(a.kv, it, head, threadIdx.x, wave_id());
+    const int n = it.it1 - it.it0;
+    const auto tile = [&](int i) { return AT_TILE * at_span_tile(it.span, min(it.it0 + i, it.it1 - 1)); };
+    if (n > 0) {
+        st.look_up(a.kv, tile(0));
+        st.load(a.kv, head, tile(0), even[0], even[1]);
+        st.look_up(a.kv, tile(1));
+    }
+    const auto step = [&](int i, char (&mine)[2][AT_TILE * 2 * D], char (&next)[2][AT_TILE * 2 * D]) {
+        st.store(mine[0], mine[1]);
+        __syncthreads();
+        const int t0 = tile(i);
+        if (i + 1 < n) {
+            st.load(a.kv, head, tile(i + 1), next[0], next[1]);
+            st.look_up(a.kv, tile(i + 2));
+        }
+        if (wr.active && !none_sees(a, wr.p_lo, wr.p_hi, t0, t0 + AT_TILE - 1))
+            wide_tile<D, CAREFUL>(a, wr, qf, mine[0], mine[1], t0, acc, m, l);
+    };
+    for (int i = 0; i < n; i += 2) {
+        step(i, even, odd);
+        if (i + 1 < n) step(i + 1, odd, even);
+    }
+    float bad = 0.f;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) bad = fmaf(acc[d][e], 0.f, bad);
+    return wr.active && bad != 0.f;
+}
+
+// Four waves, 32 rows each; tiles of 64 tokens go through LDS.
 //
 // A value that is infinite or NaN in a place that a row does not see would
 // still reach it through the second product (0 * NaN).  Looking for such values
 // in every masked tile costs more than it is worth, so the item looks at its
 // result: when that is not finite, it is computed again, and the tiles in which
 // some row is masked take each row's visible tokens alone.
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool UNI>
 __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a) {
-    constexpr int RB = 2 * D, DB = D / 32, KS = D / 16;
-    __shared__ __align__(16) char lds[2][2][AT_TILE * RB];
+    constexpr int DB = D / 32;
+    __shared__ __align__(16) char even[2][AT_TILE * 2 * D];
+    __shared__ __align__(16) char odd[2][AT_TILE * 2 * D];
     const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
     const int col = lane & 31, h = lane >> 5;
     Item it;
     if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_WIDE_ROWS, it)) return;
 
-    // this lane's row; lanes past the item's rows repeat its last one
-    const int row = min(32 * w + col, it.nrows - 1);
-    const bool active = 32 * w < it.nrows;
-    const int pos = it.p0 + (it.row0 + row) / a.group;
-    const int p_lo = it.p0 + (it.row0 + min(32 * w, it.nrows - 1)) / a.group;
-    const int p_hi = it.p0 + (it.row0 + min(32 * w + 31, it.nrows - 1)) / a.group;
-    u32x4_t qf[KS];
+    WideRows wr;
+    wr.row = min(32 * w + col, it.nrows - 1);  // lanes past the item's rows repeat its last one
+    wr.active = 32 * w < it.nrows;
+    wr.pos = it.p0 + (it.row0 + wr.row) / a.group;
+    wr.p_lo = it.p0 + (it.row0 + min(32 * w, it.nrows - 1)) / a.group;
+    wr.p_hi = it.p0 + (it.row0 + min(32 * w + 31, it.nrows - 1)) / a.group;
+    u32x4_t qf[D / 16];
     {
-        const uint16_t* q = a.q + row_off(a, it, it.row0 + row, head, a.ldq, D) + 8 * h;
+        const uint16_t* q = a.q + row_off(a, it, it.row0 + wr.row, head, a.ldq, D) + 8 * h;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4_t*>(q + 16 * s);
+        for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const u32x4_t*>(q + 16 * s);
+        // they arrive here: a wait for them inside the loop over tiles would
+        // be one for the copies that are under way there
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(qf[s]));
     }
-
     f32x16_t acc[DB];
     float m, l;
-    for (bool careful = false;; careful = true) {
-#pragma unroll
-        for (int d = 0; d < DB; ++d) acc[d] = f32x16_t{};
-        m = -INFINITY;
-        l = 0.f;
-        Stage<D, E4M3, AT_TILE, 256> st;
-        if (it.it0 < it.it1) st.load(a.kv, it, head, AT_TILE * at_span_tile(it.span, it.it0), threadIdx.x);
-        for (int i = it.it0; i < it.it1; ++i) {
-            const int t0 = AT_TILE * at_span_tile(it.span, i);
-            char *kt = lds[i & 1][0], *vt = lds[i & 1][1];
-            st.store(kt, vt, threadIdx.x);
-            __syncthreads();
-            if (i + 1 < it.it1) st.load(a.kv, it, head, AT_TILE * at_span_tile(it.span, i + 1), threadIdx.x);
-            if (!active || none_sees(a, p_lo, p_hi, t0, t0 + AT_TILE - 1)) continue;
+    if (__syncthreads_or(wide_pass<D, E4M3, UNI, false>(a, it, wr, head, qf, even, odd, acc, m, l)))
+        wide_pass<D, E4M3, UNI, true>(a, it, wr, head, qf, even, odd, acc, m, l);
 
-            f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int r = 32 * b + col;
-                    s[b] = mfma32(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 2 * ks + h)),
-                                  qf[ks], s[b]);
-                }
-            const bool masked = !all_see(a, p_lo, p_hi, t0, t0 + AT_TILE - 1);
-            if (masked) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (!sees(a, pos, t0 + 32 * b + 8 * (r >> 2) + 4 * h + (r & 3))) s[b][r] = -INFINITY;
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
-            if (__ballot(top * a.sl2 > m + kGrow)) {
-                const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
-                const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
-                m = up;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DB; ++d) acc[d] *= f;
-            }
-            const float off = m == -INFINITY ? 0.f : -m;
-            uint32_t pw[16];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; r += 2) {
-                    const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
-                    const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
-                    const uint32_t pk = pack_bf16(p0, p1);
-                    l = add_bf16_pair(pk, l);
-                    pw[8 * b + r / 2] = pk;
-                }
-            if (careful && masked) {
-                // one pair of rows' weights after the other, each register moved
-                // down to the first: a rolled loop over registers
-#pragma unroll 1
-                for (int j = 0; j < 16; ++j) {
-                    const uint32_t cur = pw[0];
-#pragma unroll
-                    for (int k = 0; k < 15; ++k) pw[k] = pw[k + 1];
-#pragma unroll 1
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t both = __shfl(cur, col + 32 * (x >> 1));
-                        const float p = x & 1 ? bf16_hi(both) : bf16_lo(both);
-                        const int r = 2 * (j & 7) + (x & 1);
-                        const int tok = 32 * (j >> 3) + 8 * (r >> 2) + 4 * (x >> 1) + (r & 3);
-                        const bool vis = sees(a, pos, t0 + tok);
-#pragma unroll
-                        for (int d = 0; d < DB; ++d)
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int el = 32 * d + 8 * (e >> 2) + 4 * h + (e & 3);
-                                const float v = v_elem(vt, RB, tok, v_chunk<D>(tok, el >> 3), el & 7);
-                                acc[d][e] = vis ? fmaf(p, v, acc[d][e]) : acc[d][e];
-                            }
-                    }
-                }
-                continue;
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const u32x4_t pf = {pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]};
-                const int i16 = lane & 15, g = (lane >> 4) & 1;
-                const int r = 16 * c + 4 * h + (i16 >> 2);
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const int ch = 4 * d + 2 * g + ((i16 & 3) >> 1), by = 8 * (i16 & 1);
-                    const u32x2_t lo = ds_tr16(vt + r * RB + 16 * v_chunk<D>(r, ch) + by);
-                    const u32x2_t hi = ds_tr16(vt + (r + 8) * RB + 16 * v_chunk<D>(r + 8, ch) + by);
-                    acc[d] = mfma32(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
-                }
-            }
-        }
-        float bad = 0.f;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) bad = fmaf(acc[d][e], 0.f, bad);
-        if (careful || !__syncthreads_or(active && bad != 0.f)) break;
-    }
-
-    if (!active) return;
+    if (!wr.active) return;
     l += __shfl_xor(l, 32);
     if (32 * w + col >= it.nrows) return;
     if (it.nsplits == 1) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* o = a.out + row_off(a, it, it.row0 + row, head, a.ldo, D) + 4 * h;
+        uint16_t* o = a.out + row_off(a, it, it.row0 + wr.row, head, a.ldo, D) + 4 * h;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -531,7 +648,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a) {
                     u32x2_t{pack_bf16(acc[d][4 * b] * inv, acc[d][4 * b + 1] * inv),
                             pack_bf16(acc[d][4 * b + 2] * inv, acc[d][4 * b + 3] * inv)};
     } else {
-        const int64_t pr = head * a.part_rows + it.part + row;
+        const int64_t pr = head * a.part_rows + it.part + wr.row;
         float* o = a.part + pr * D + 4 * h;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -547,13 +664,131 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a) {
     }
 }
 
+// The narrow kernel's tiles of 32 tokens of one wave, every fourth of the item's;
+// true where the result is not finite.
+template <int D, bool E4M3, bool UNI, bool CAREFUL>
+__device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, int pos, int p_lo, int p_hi, int head,
+                                            int w, const u32x4_t (&qf)[D / 32], char* kt, char* vt,
+                                            f32x4_t (&acc)[D / 16], float& m, float& l) {
+    constexpr int RB = 2 * D, DB = D / 16, KS = D / 32, T = 32;
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int first = 2 * it.it0 + w, end = 2 * it.it1;
+    const auto tile = [&](int i) {
+        i = min(i, end - 1);
+        return AT_TILE * at_span_tile(it.span, i >> 1) + T * (i & 1);
+    };
+#pragma unroll
+    for (int d = 0; d < DB; ++d) acc[d] = f32x4_t{};
+    m = -INFINITY;
+    l = 0.f;
+    Stage<D, E4M3, UNI, false, T, 64> st;
+    st.init(a.kv, it, head, lane, 0);
+    if (first < end) {
+        st.look_up(a.kv, tile(first));
+        st.load(a.kv, head, tile(first), kt, vt);
+        st.look_up(a.kv, tile(first + 4));
+    }
+    for (int i = first; i < end; i += 4) {
+        const int t0 = tile(i);
+        st.store(kt, vt);
+        if (i + 4 < end) {
+            st.load(a.kv, head, tile(i + 4), kt, vt);
+            st.look_up(a.kv, tile(i + 8));
+        }
+        if (none_sees(a, p_lo, p_hi, t0, t0 + T - 1)) continue;
+
+        f32x4_t s[2] = {f32x4_t{}, f32x4_t{}};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int r = 16 * b + col;
+                s[b] = mfma16(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 4 * ks + g)), qf[ks],
+                              s[b]);
+            }
+        const bool masked = !all_see(a, p_lo, p_hi, t0, t0 + T - 1);
+        if (masked) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (!sees(a, pos, t0 + 16 * b + 4 * g + r)) s[b][r] = -INFINITY;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
+        if (__ballot(top * a.sl2 > m + kGrow)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
+            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
+            m = up;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) acc[d] *= f;
+        }
+        const float off = m == -INFINITY ? 0.f : -m;
+        uint32_t pw[4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; r += 2) {
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
+                const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
+                const uint32_t pk = pack_bf16(p0, p1);
+                l = add_bf16_pair(pk, l);
+                pw[2 * b + r / 2] = pk;
+            }
+        if (CAREFUL && masked) {
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t cur = pw[0];
+#pragma unroll
+                for (int k = 0; k < 3; ++k) pw[k] = pw[k + 1];
+#pragma unroll 1
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t both = __shfl(cur, col + 16 * (x >> 1));
+                    const float p = x & 1 ? bf16_hi(both) : bf16_lo(both);
+                    const int tok = 16 * (j >> 1) + 4 * (x >> 1) + 2 * (j & 1) + (x & 1);
+                    const bool vis = sees(a, pos, t0 + tok);
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int el = 16 * d + 4 * g + e;
+                            const float v = v_elem(vt, RB, tok, v_chunk<D>(tok, el >> 3), el & 7);
+                            acc[d][e] = vis ? fmaf(p, v, acc[d][e]) : acc[d][e];
+                        }
+                }
+            }
+            continue;
+        }
+        const u32x4_t pf = {pw[0], pw[1], pw[2], pw[3]};
+        const int r = 4 * g + (col >> 2);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+            const int ch = 2 * d + ((col & 3) >> 1), by = 8 * (col & 1);
+            const u32x2_t lo = ds_tr16(vt + r * RB + 16 * v_chunk<D>(r, ch) + by);
+            const u32x2_t hi = ds_tr16(vt + (r + 16) * RB + 16 * v_chunk<D>(r + 16, ch) + by);
+            acc[d] = mfma16(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
+        }
+    }
+    float bad = 0.f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bad = fmaf(acc[d][e], 0.f, bad);
+    return __ballot(bad != 0.f) != 0;
+}
+
 // Up to 16 rows (the query heads of a kv head, for a few new tokens): the four
 // waves take tiles of 32 tokens in turn, each through LDS of its own, so that
 // no barrier stands between the loads, and join their results at the end.
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool UNI>
 __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
-    constexpr int RB = 2 * D, DB = D / 16, KS = D / 32, T = 32;
-    __shared__ __align__(16) char lds[4][2][T * RB];
+    constexpr int DB = D / 16, KS = D / 32, T = 32;
+    __shared__ __align__(16) char lds[4][2][T * 2 * D];
     __shared__ float s_m[4][16], s_l[4][16];
     const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
     const int col = lane & 15, g = lane >> 4;
@@ -569,110 +804,10 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4_t*>(q + 32 * s);
     }
-    char *kt = lds[w][0], *vt = lds[w][1];
-    const auto tile_of = [&](int i) { return AT_TILE * at_span_tile(it.span, i >> 1) + T * (i & 1); };
-
     f32x4_t acc[DB];
     float m, l;
-    for (bool careful = false;; careful = true) {
-#pragma unroll
-        for (int d = 0; d < DB; ++d) acc[d] = f32x4_t{};
-        m = -INFINITY;
-        l = 0.f;
-        Stage<D, E4M3, T, 64> st;
-        int i = 2 * it.it0 + w;
-        const int end = 2 * it.it1;
-        if (i < end) st.load(a.kv, it, head, tile_of(i), lane);
-        for (; i < end; i += 4) {
-            const int t0 = tile_of(i);
-            st.store(kt, vt, lane);
-            if (i + 4 < end) st.load(a.kv, it, head, tile_of(i + 4), lane);
-            if (none_sees(a, p_lo, p_hi, t0, t0 + T - 1)) continue;
-
-            f32x4_t s[2] = {f32x4_t{}, f32x4_t{}};
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int r = 16 * b + col;
-                    s[b] = mfma16(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 4 * ks + g)),
-                                  qf[ks], s[b]);
-                }
-            const bool masked = !all_see(a, p_lo, p_hi, t0, t0 + T - 1);
-            if (masked) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (!sees(a, pos, t0 + 16 * b + 4 * g + r)) s[b][r] = -INFINITY;
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
-            if (__ballot(top * a.sl2 > m + kGrow)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
-                const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
-                m = up;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DB; ++d) acc[d] *= f;
-            }
-            const float off = m == -INFINITY ? 0.f : -m;
-            uint32_t pw[4];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 4; r += 2) {
-                    const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
-                    const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
-                    const uint32_t pk = pack_bf16(p0, p1);
-                    l = add_bf16_pair(pk, l);
-                    pw[2 * b + r / 2] = pk;
-                }
-            if (careful && masked) {
-#pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t cur = pw[0];
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) pw[k] = pw[k + 1];
-#pragma unroll 1
-                    for (int x = 0; x < 8; ++x) {
-                        const uint32_t both = __shfl(cur, col + 16 * (x >> 1));
-                        const float p = x & 1 ? bf16_hi(both) : bf16_lo(both);
-                        const int tok = 16 * (j >> 1) + 4 * (x >> 1) + 2 * (j & 1) + (x & 1);
-                        const bool vis = sees(a, pos, t0 + tok);
-#pragma unroll
-                        for (int d = 0; d < DB; ++d)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int el = 16 * d + 4 * g + e;
-                                const float v = v_elem(vt, RB, tok, v_chunk<D>(tok, el >> 3), el & 7);
-                                acc[d][e] = vis ? fmaf(p, v, acc[d][e]) : acc[d][e];
-                            }
-                    }
-                }
-                continue;
-            }
-            const u32x4_t pf = {pw[0], pw[1], pw[2], pw[3]};
-            const int r = 4 * g + (col >> 2);
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const int ch = 2 * d + ((col & 3) >> 1), by = 8 * (col & 1);
-                const u32x2_t lo = ds_tr16(vt + r * RB + 16 * v_chunk<D>(r, ch) + by);
-                const u32x2_t hi = ds_tr16(vt + (r + 16) * RB + 16 * v_chunk<D>(r + 16, ch) + by);
-                acc[d] = mfma16(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
-            }
-        }
-        float bad = 0.f;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) bad = fmaf(acc[d][e], 0.f, bad);
-        if (careful || !__ballot(bad != 0.f)) break;
-    }
+    if (narrow_pass<D, E4M3, UNI, false>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w][0], lds[w][1], acc, m, l))
+        narrow_pass<D, E4M3, UNI, true>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w][0], lds[w][1], acc, m, l);
 
     // join the waves: each leaves its maximum, sum and [row][D] accumulator in LDS
     l += __shfl_xor(l, 16);
@@ -913,16 +1048,19 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     const hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
     const bool e4m3 = kv->dtype == LORA_KV_E4M3;
     typedef void (*fn_t)(AttnArgs);
-    static const fn_t fn[2][2][2] = {
-        {{attn_narrow_kernel<64, false>, attn_narrow_kernel<64, true>},
-         {attn_narrow_kernel<128, false>, attn_narrow_kernel<128, true>}},
-        {{attn_wide_kernel<64, false>, attn_wide_kernel<64, true>},
-         {attn_wide_kernel<128, false>, attn_wide_kernel<128, true>}}};
+#define AT_FORMS(kernel, d) \
+    {{kernel<d, false, false>, kernel<d, false, true>}, {kernel<d, true, false>, kernel<d, true, true>}}
+    static const fn_t fn[2][2][2][2] = {{AT_FORMS(attn_narrow_kernel, 64), AT_FORMS(attn_narrow_kernel, 128)},
+                                        {AT_FORMS(attn_wide_kernel, 64), AT_FORMS(attn_wide_kernel, 128)}};
+#undef AT_FORMS
+    // where Stage can work with scalar page addresses: 32-bit strides in bytes, 64 rows' offsets among them
+    const bool small = kv->token_stride <= INT32_MAX / 128 && kv->page_stride <= INT32_MAX / 2;
     for (int kind = 1; kind >= 0; --kind) {  // the longer items first
         if (I.n_work[kind] == 0) continue;
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_work[kind]);
         a.n_work = I.n_work[kind];
-        if (launch(fn[kind][d == 128][e4m3], dim3((unsigned)(a.n_work * hk)), dim3(256), s, a) != hipSuccess)
+        const bool uni = small && kv->page_tokens >= (kind == LORA_ATTN_WIDE ? 256 : 64) / (d / 8);
+        if (launch(fn[kind][d == 128][e4m3][uni], dim3((unsigned)(a.n_work * hk)), dim3(256), s, a) != hipSuccess)
             return LORA_EHIP;
     }
     if (I.n_merge > 0) {
