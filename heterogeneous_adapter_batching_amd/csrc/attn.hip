@@ -25,7 +25,8 @@
 // bf16, and the common tile pays neither the rescale nor a reduction over
 // lanes.  Weights are rounded to bf16 for the second product, and the rounded
 // weights are what the row's sum adds up, so the rounding cancels where few
-// tokens dominate.
+// tokens dominate: the 4x4x4 MFMA with a first operand of ones gives each lane
+// the sum of the four weights that it holds itself.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -65,10 +66,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const bf16x2_t p = {(__bf16)lo, (__bf16)hi};
     return __builtin_bit_cast(uint32_t, p);
 }
-// acc + lo(w) + hi(w)
-__device__ __forceinline__ float add_bf16_pair(uint32_t w, float acc) {
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w),
-                                           __builtin_bit_cast(bf16x2_t, 0x3F803F80u), acc, false);
+// l[0] += the four weights in w
+__device__ __forceinline__ f32x4_t add_weights(uint32_t w0, uint32_t w1, f32x4_t l) {
+    const u32x2_t ones = {0x3F803F80u, 0x3F803F80u}, w = {w0, w1};
+    return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4_t, ones), __builtin_bit_cast(s16x4_t, w), l, 0,
+                                                  0, 0);
 }
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
@@ -307,6 +309,26 @@ __device__ __forceinline__ int64_t row_off(const AttnArgs& a, const Item& it, in
 __device__ __forceinline__ bool sees(const AttnArgs& a, int pos, int token) {
     return token <= pos && (a.window == 0 || token > pos - a.window || token < a.sinks);
 }
+// Calls `each` with a function of e that says whether token `first` + e is hidden
+// from the row at `pos`: once for what comes after the row and, with a window,
+// once for what lies between the sinks and the window.  One comparison each, and
+// one after the other: scheduled together, the comparisons' results took the
+// scalar registers of the whole loop.
+template <typename F>
+__device__ __forceinline__ void hide(const AttnArgs& a, int pos, int first, F each) {
+    const int left = pos - first;
+    each([&](int e) {
+        __builtin_amdgcn_sched_barrier(0);
+        return e > left;
+    });
+    if (a.window) {
+        const uint32_t from = (uint32_t)first - (uint32_t)a.sinks, count = (uint32_t)max(0, pos - a.window + 1 - a.sinks);
+        each([&](int e) {
+            __builtin_amdgcn_sched_barrier(0);
+            return from + (uint32_t)e < count;
+        });
+    }
+}
 // Every row of positions p_lo .. p_hi sees all of tokens t0 .. t1; and: none sees any.
 __device__ __forceinline__ bool all_see(const AttnArgs& a, int p_lo, int p_hi, int t0, int t1) {
     return t1 <= p_lo && (a.window == 0 || t0 > p_hi - a.window || t1 < a.sinks);
@@ -316,17 +338,17 @@ __device__ __forceinline__ bool none_sees(const AttnArgs& a, int p_lo, int p_hi,
 }
 
 // Tiles in LDS are row-major bf16, D * 2 bytes a row, with the 16-byte chunks of
-// a row permuted: K by the row (32 lanes read one chunk of 32 rows), V by the
-// row in pairs of chunks (16 lanes read 32 bytes of 4 rows).
+// a row permuted so that the lanes an LDS cycle serves (256 bytes) hit all banks
+// once.  K: 16 lanes read one chunk of 16 rows.  V: 32 lanes read 32 bytes of 4
+// rows of two neighbouring column blocks (wide) or of 8 rows (narrow); the row's
+// low bits move the pair of chunks, and leave the pair's last bit to bit 2.
 template <int D>
-__device__ __forceinline__ int k_chunk(int row, int c) { return c ^ (row & (D / 8 - 1)); }
+__device__ __forceinline__ int k_chunk(int row, int c) {
+    return c ^ (D == 128 ? row & 15 : (row >> 1) & 7);
+}
 template <int D>
-__device__ __forceinline__ int v_chunk(int row, int c) { return c ^ (2 * (row & (D / 16 - 1))); }
-
-// Wave-uniform read of a page id through the scalar cache (the table is read-only
-// for the whole launch).
-__device__ __forceinline__ int32_t ld_uniform(const int32_t* p, int32_t i) {
-    return ((const __attribute__((address_space(4))) int32_t*)p)[i];
+__device__ __forceinline__ int v_chunk(int row, int c) {
+    return c ^ ((D == 128 ? (row & 3) << 2 : (row & 2) << 1) | ((row >> 1) & 2));
 }
 
 // 16 bytes per lane from memory to LDS, past the registers: lane i's go to lds +
@@ -341,113 +363,182 @@ __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint
 __device__ __forceinline__ void copy_to_lds(const char* from, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Until at most N of the wave's loads, the last ones, are under way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Barrier of the workgroup that waits for LDS writes, not for loads.
+__device__ __forceinline__ void barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 __device__ __forceinline__ uint32_t lds_addr(const char* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
 
-// Tokens [t0, t0 + ROWS) of one kv head on their way from the cache to LDS: NT
-// lanes (t of them, waves of 64 from `wave`) move 8 elements each a step, RPS
-// rows.  Tokens past the end of the sequence take its last token's place:
-// nothing sees them.
+// How NW waves move a tile of ROWS tokens: a wave moves RPI rows at a time, 16
+// bytes of bf16 (or 8 of codes) per lane, in STEPS steps.
+template <int D, int NW, int ROWS>
+struct Split {
+    static constexpr int CPR = D / 8, RPI = 64 / CPR, STEPS = ROWS / (RPI * NW);
+    // first row of step s of a wave
+    static __device__ __forceinline__ int row(int s, int wave) { return (s * NW + wave) * RPI; }
+};
+
+// Where a wave's rows of the item's tiles lie in the cache: addresses of their
+// keys.  `Tiles` maps a tile's number to its first token; numbers past the last
+// tile stand for it.  Tokens past the end of the sequence take its last token's
+// place: nothing sees them.
 //
-// UNI: a page holds RPS tokens at least, so a step's rows lie in one page, whose
-// address is scalar, and the strides fit 32 bits; otherwise every lane looks its
-// own page up.
-//
-// DIRECT: bf16 rows go straight to LDS, the permutation of a row's chunks made
-// by the lanes' source addresses.  Otherwise they go through registers, and e4m3
-// codes become bf16 (exactly) on the way.
-template <int D, bool E4M3, bool UNI, bool DIRECT, int ROWS, int NT>
+// UNI: a page holds RPI tokens at least, so a step's rows lie in one page, and the
+// address is that of their first row.  Each lane works out the address of one
+// step of one of the next 64 / STEPS tiles, from a page id fetched a window
+// earlier; a tile then only reads lanes.  (Looked up tile by tile with scalar
+// loads and multiplies, the same took longer than the tile's softmax: a scalar
+// instruction that waits for another takes ten cycles.)  Otherwise every lane
+// looks up the page of its own row, tile by tile.
+template <int D, bool E4M3, bool UNI, int NW, int ROWS, typename Tiles>
+struct Places {
+    typedef Split<D, NW, ROWS> S;
+    typedef typename std::conditional<UNI, uint32_t, int64_t>::type scale_t;
+    static constexpr int STEPS = S::STEPS, WINDOW = 64 / STEPS, ES = E4M3 ? 1 : 2;
+    const Kv& c;
+    const Item& it;
+    const Tiles& tiles;
+    const uint64_t base;  // the head's first key
+    const int wave, lane;
+    int32_t ahead[UNI ? 1 : STEPS];  // page ids looked up
+    uint32_t lo, hi, so, more;  // UNI, a step a lane: address, scale offset, rows after the first (at most RPI - 1)
+    // of the tile last asked for: address and scale offset of the step's first row (UNI) or of the lane's row
+    uint64_t at[STEPS];
+    scale_t sc[STEPS];
+    uint32_t rows[UNI ? STEPS : 1];
+
+    __device__ __forceinline__ Places(const Kv& c_, const Item& it_, const Tiles& tiles_, int head, int wave_)
+        : c(c_), it(it_), tiles(tiles_), base((uint64_t)(uintptr_t)c_.k + ES * head * c_.head_stride), wave(wave_),
+          lane(threadIdx.x & 63) {}
+    __device__ __forceinline__ int window_token(int i) const { return tiles(i + lane / STEPS) + S::row(lane % STEPS, wave); }
+    __device__ __forceinline__ int token(int i, int s) const {
+        return min(tiles(i) + S::row(s, wave) + lane / S::CPR, it.kv - 1);
+    }
+    // UNI: the pages of the window that starts at tile i; else of tile i
+    __device__ __forceinline__ void look_up(int i) {
+        if constexpr (UNI) {
+            ahead[0] = it.table[min(window_token(i), it.kv - 1) >> c.page_shift];
+        } else {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) ahead[s] = it.table[token(i, s) >> c.page_shift];
+        }
+    }
+    // Tile i is the next to be asked for; tiles are asked for in order, from 0,
+    // after look_up(0).
+    __device__ __forceinline__ void open(int i) {
+        if (!UNI || i % WINDOW != 0) return;
+        const int first = window_token(i), tok = min(first, it.kv - 1);
+        const int32_t pg = clamp_page(c, ahead[0]), slot = tok & ((1 << c.page_shift) - 1);
+        const uint64_t x = base + ES * ((uint64_t)(uint32_t)pg * (uint32_t)c.page_stride +
+                                        (uint64_t)(uint32_t)slot * (uint32_t)c.token_stride);
+        lo = (uint32_t)x;
+        hi = (uint32_t)(x >> 32);
+        so = (uint32_t)(((uint32_t)pg * (uint32_t)c.n_kv_heads << c.page_shift) + slot);
+        more = (uint32_t)min(max(it.kv - 1 - first, 0), S::RPI - 1);
+        look_up(i + WINDOW);
+    }
+    __device__ __forceinline__ void read(int i) {
+        if constexpr (UNI) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int l = (i % WINDOW) * STEPS + s;
+                at[s] = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, l) << 32) |
+                        (uint32_t)__builtin_amdgcn_readlane(lo, l);
+                rows[s] = __builtin_amdgcn_readlane(more, l);
+                if constexpr (E4M3) sc[s] = __builtin_amdgcn_readlane(so, l);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int32_t pg = clamp_page(c, ahead[s]), slot = token(i, s) & ((1 << c.page_shift) - 1);
+                at[s] = base + ES * (pg * c.page_stride + slot * c.token_stride);
+                if constexpr (E4M3) sc[s] = scale_off(c, pg, 0, slot);
+            }
+            look_up(i + 1);
+        }
+    }
+};
+
+// Keys (or VALUES) of a tile on their way from the cache to LDS.  DIRECT: bf16
+// rows go straight to LDS, the permutation of a row's chunks made by the lanes'
+// source addresses.  Otherwise they go through registers, and e4m3 codes become
+// bf16 (exactly) on the way.
+template <int D, bool E4M3, bool UNI, bool DIRECT, bool VALUES, int NW, int ROWS>
 struct Stage {
     static_assert(!(E4M3 && DIRECT), "codes are converted on the way");
-    static constexpr int CPR = D / 8, RPS = NT / CPR, STEPS = ROWS / RPS, HELD = DIRECT ? 1 : STEPS, ES = E4M3 ? 1 : 2;
+    typedef Split<D, NW, ROWS> S;
+    static constexpr int STEPS = S::STEPS, ES = E4M3 ? 1 : 2, HELD = DIRECT ? 1 : STEPS;
     typedef typename std::conditional<E4M3, u32x2_t, u32x4_t>::type raw_t;
-    const char *kbase, *vbase;  // the head's first element
-    const int32_t* table;
-    int32_t t, wave, kv;
-    uint32_t row_bytes, page_bytes;
-    int32_t page[STEPS];
-    raw_t k[HELD], v[HELD];
-    uint32_t ke[E4M3 ? STEPS : 1], ve[E4M3 ? STEPS : 1];
+    typedef typename std::conditional<UNI, uint32_t, int64_t>::type scale_t;
+    uint64_t at[STEPS];  // as in Places
+    scale_t sc[STEPS];
+    uint32_t rows[UNI ? STEPS : 1];
+    const uint8_t* scales;  // the head's first scale
+    uint64_t apart;         // values from keys
+    int32_t wave;
+    uint32_t row_bytes;
+    raw_t held[HELD];
+    uint32_t exps[E4M3 ? STEPS : 1];
 
-    __device__ __forceinline__ void init(const Kv& c, const Item& it, int head, int lane, int wave_) {
-        kbase = c.k + head * c.head_stride * ES;
-        vbase = c.v + head * c.head_stride * ES;
-        table = it.table;
-        t = lane;
+    __device__ __forceinline__ void init(const Kv& c, int head, int wave_) {
+        scales = (VALUES ? c.v_scale : c.k_scale) + ((int64_t)head << c.page_shift);
+        apart = VALUES ? (uint64_t)(uintptr_t)c.v - (uint64_t)(uintptr_t)c.k : 0;
         wave = wave_;
-        kv = it.kv;
         row_bytes = (uint32_t)c.token_stride * ES;
-        page_bytes = (uint32_t)c.page_stride * ES;
     }
-    // the pages of a tile, some time before its load
-    __device__ __forceinline__ void look_up(const Kv& c, int t0) {
+    template <typename P>
+    __device__ __forceinline__ void take(const P& p) {
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            if constexpr (UNI) page[s] = ld_uniform(table, min(t0 + s * RPS, kv - 1) >> c.page_shift);
-            else page[s] = table[min(t0 + s * RPS + t / CPR, kv - 1) >> c.page_shift];
+            at[s] = p.at[s] + apart;
+            if constexpr (UNI) rows[s] = p.rows[s];
+            if constexpr (E4M3) sc[s] = p.sc[s];
         }
     }
-    __device__ __forceinline__ void load(const Kv& c, int head, int t0, char* kt, char* vt) {
-        const int mask = (1 << c.page_shift) - 1;
-        const uint32_t lane_row = (t / CPR) * row_bytes;
+    __device__ __forceinline__ int chunk(int row) const {
+        const int c = (threadIdx.x & 63) % S::CPR;
+        return VALUES ? v_chunk<D>(row, c) : k_chunk<D>(row, c);
+    }
+    __device__ __forceinline__ void load(char* tile) {
+        const int lane = threadIdx.x & 63, mine = lane / S::CPR;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            const int row = s * RPS + t / CPR;
-            const int first = min(t0 + s * RPS, kv - 1), tok = min(t0 + row, kv - 1);
-            const int32_t pg = clamp_page(c, page[s]);
-            const int kc = (DIRECT ? k_chunk<D>(row, t % CPR) : t % CPR) * 8 * ES;
-            const int vc = (DIRECT ? v_chunk<D>(row, t % CPR) : t % CPR) * 8 * ES;
-            const uint32_t to = s * RPS * (2 * D) + wave * 1024;
-            if constexpr (UNI) {
-                // scalar: the step's first row; by lane: its row and chunk
-                const uint64_t base = (uint64_t)(uint32_t)pg * page_bytes + (uint64_t)(uint32_t)(first & mask) * row_bytes;
-                uint32_t at = lane_row;
-                if (t0 + (s + 1) * RPS > kv) at = (uint32_t)(tok - first) * row_bytes;
-                if constexpr (DIRECT) {
-                    copy_to_lds(kbase + base, at + kc, lds_addr(kt) + to);
-                    copy_to_lds(vbase + base, at + vc, lds_addr(vt) + to);
-                } else {
-                    k[s] = *reinterpret_cast<const raw_t*>(kbase + base + (at + kc));
-                    v[s] = *reinterpret_cast<const raw_t*>(vbase + base + (at + vc));
-                }
+            const char* from = (const char*)(uintptr_t)at[s];
+            uint32_t off = (DIRECT ? chunk(S::row(s, wave) + mine) : lane % S::CPR) * 8 * ES;
+            if constexpr (UNI) off += min(mine * row_bytes, rows[s] * row_bytes);
+            if constexpr (DIRECT) {
+                const uint32_t to = lds_addr(tile) + S::row(s, wave) * (2 * D);
+                if constexpr (UNI) copy_to_lds(from, off, to);
+                else copy_to_lds(from + off, to);
             } else {
-                const int64_t at = ES * (pg * c.page_stride + (tok & mask) * c.token_stride);
-                if constexpr (DIRECT) {
-                    copy_to_lds(kbase + at + kc, lds_addr(kt) + to);
-                    copy_to_lds(vbase + at + vc, lds_addr(vt) + to);
-                } else {
-                    k[s] = *reinterpret_cast<const raw_t*>(kbase + at + kc);
-                    v[s] = *reinterpret_cast<const raw_t*>(vbase + at + vc);
-                }
+                held[s] = *reinterpret_cast<const raw_t*>(from + off);
             }
             if constexpr (E4M3) {
-                const int64_t so = scale_off(c, pg, head, UNI ? first & mask : tok & mask);
-                ke[s] = (c.k_scale + so)[UNI ? (uint32_t)(tok - first) : 0u];
-                ve[s] = (c.v_scale + so)[UNI ? (uint32_t)(tok - first) : 0u];
+                if constexpr (UNI) exps[s] = scales[sc[s] + min((uint32_t)mine, rows[s])];
+                else exps[s] = scales[sc[s]];
             }
         }
     }
-    // what load() has left in registers, or its end
-    __device__ __forceinline__ void store(char* kt, char* vt) const {
+    // what load() has left in registers
+    __device__ __forceinline__ void store(char* tile) const {
         if constexpr (!DIRECT) {
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                const int row = s * RPS + t / CPR, chunk = t % CPR;
-                u32x4_t kk, vv;
-                if constexpr (E4M3) {
-                    kk = dequant8(k[s], scale_of(ke[s]));
-                    vv = dequant8(v[s], scale_of(ve[s]));
-                } else {
-                    kk = k[s];
-                    vv = v[s];
-                }
-                *reinterpret_cast<u32x4_t*>(kt + row * (2 * D) + 16 * k_chunk<D>(row, chunk)) = kk;
-                *reinterpret_cast<u32x4_t*>(vt + row * (2 * D) + 16 * v_chunk<D>(row, chunk)) = vv;
+                const int row = S::row(s, wave) + (threadIdx.x & 63) / S::CPR;
+                u32x4_t x;
+                if constexpr (E4M3) x = dequant8(held[s], scale_of(exps[s]));
+                else x = held[s];
+                *reinterpret_cast<u32x4_t*>(tile + row * (2 * D) + 16 * chunk(row)) = x;
             }
-        } else {
-            wait_loads();
         }
     }
 };
@@ -457,67 +548,117 @@ __device__ __forceinline__ float v_elem(const char* vt, int row_bytes, int row, 
                            << 16);
 }
 
-// One wave's rows in the wide kernel.
-struct WideRows {
+// One wave's rows in the wide kernel, and what it has of them so far.
+template <int D>
+struct Wide {
     int row, pos, p_lo, p_hi;  // this lane's row and its position; the wave's first and last position
     bool active;
-};
+    int whole0, whole1, whole2;  // every row sees all of tiles i < whole0 and whole1 <= i < whole2
+    u32x4_t qf[D / 16];
+    f32x16_t s[2];       // scores of a tile: S^T, 64 tokens x 32 rows
+    uint32_t pw[16];     // its weights, in pairs
+    f32x16_t acc[D / 32];  // O^T
+    float m;
+    f32x4_t l;  // the sum of the lane's weights, four times
 
-// One wave's 32 rows over one tile in LDS: scores, weights, and their product
-// with v added to acc (rows d of O^T), m and l brought up to date.
-template <int D, bool CAREFUL>
-__device__ __forceinline__ void wide_tile(const AttnArgs& a, const WideRows& wr, const u32x4_t (&qf)[D / 16],
-                                          const char* kt, const char* vt, int t0, f32x16_t (&acc)[D / 32], float& m,
-                                          float& l) {
-    constexpr int RB = 2 * D, DB = D / 32, KS = D / 16;
-    const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
-    f32x16_t s[2] = {f32x16_t{}, f32x16_t{}};
+    __device__ __forceinline__ void find_whole(const AttnArgs& a, const Item& it) {
+        const int behind = at_max(0, (p_lo + 1) >> 6);  // tiles that end before the first row's next token
+        const int list = it.span.sinks - it.span.first - it.it0;  // tile -> number, past the sinks
+        whole0 = a.window ? min(min(a.sinks >> 6, behind), it.span.sinks) - it.it0 : 0;
+        whole1 = a.window ? (at_max(-64, p_hi - a.window) >> 6) + 1 + list : 0;
+        whole1 = max(whole1, it.span.sinks - it.it0);
+        whole2 = behind + list;
+    }
+    __device__ __forceinline__ bool masks(int i) const { return !(i < whole0 || (i >= whole1 && i < whole2)); }
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+        for (int d = 0; d < D / 32; ++d) acc[d] = f32x16_t{};
+        m = -INFINITY;
+        l = f32x4_t{};
+    }
+    // Operands of the multiplications in their order: chunk f / 2 of the keys'
+    // tokens 32 (f % 2) ..., and 32 columns f % (D/32) of 16 tokens of the values.
+    __device__ __forceinline__ static u32x4_t k_part(const char* kt, int f) {
+        const int col = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1, r = 32 * (f & 1) + col;
+        return *reinterpret_cast<const u32x4_t*>(kt + r * (2 * D) + 16 * k_chunk<D>(r, 2 * (f >> 1) + h));
+    }
+    __device__ __forceinline__ static u32x4_t v_part(const char* vt, int f) {
+        const int lane = threadIdx.x & 63, h = lane >> 5, i16 = lane & 15, g = (lane >> 4) & 1;
+        const int r = 16 * (f / (D / 32)) + 4 * h + (i16 >> 2);
+        const int ch = 4 * (f % (D / 32)) + 2 * g + ((i16 & 3) >> 1), by = 8 * (i16 & 1);
+        const u32x2_t lo = ds_tr16(vt + r * (2 * D) + 16 * v_chunk<D>(r, ch) + by);
+        const u32x2_t hi = ds_tr16(vt + (r + 8) * (2 * D) + 16 * v_chunk<D>(r + 8, ch) + by);
+        return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+    }
+    // Scores of one tile (SCORES) and product of another (PRODUCT).  LDS answers
+    // after four MFMAs' time, so the operands are read AHEAD of them.  between(f)
+    // comes after MFMA f: other work, in the matrix unit's time.
+    template <bool SCORES, bool PRODUCT, typename F>
+    __device__ __forceinline__ void multiply(const char* kt, const char* vt, F between) {
+        constexpr int NS = SCORES ? D / 8 : 0, N = NS + (PRODUCT ? D / 8 : 0), AHEAD = 6;
+        u32x4_t part[AHEAD];
+        const auto read = [&](int f) { return f < NS ? k_part(kt, f) : v_part(vt, f - NS); };
+        if (SCORES) s[0] = s[1] = f32x16_t{};
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int r = 32 * b + col;
-            s[b] = mfma32(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 2 * ks + h)), qf[ks], s[b]);
+        for (int f = 0; f < AHEAD; ++f) part[f] = read(f);
+#pragma unroll
+        for (int f = 0; f < N; ++f) {
+            if (f < NS) {
+                s[f & 1] = mfma32(part[f % AHEAD], qf[f >> 1], s[f & 1]);
+            } else {
+                const int c = (f - NS) / (D / 32), d = (f - NS) % (D / 32);
+                const u32x4_t pf = {pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]};
+                acc[d] = mfma32(part[f % AHEAD], pf, acc[d]);
+                if (d < 2) l = add_weights(pf[2 * d], pf[2 * d + 1], l);
+            }
+            if (f + AHEAD < N) part[f % AHEAD] = read(f + AHEAD);
+            between(f);
+            __builtin_amdgcn_sched_barrier(0x6);  // arithmetic may move
         }
-    const bool masked = !all_see(a, wr.p_lo, wr.p_hi, t0, t0 + AT_TILE - 1);
-    if (masked) {
+    }
+    // of tile i
+    template <typename Tiles>
+    __device__ __forceinline__ void weights(const AttnArgs& a, const Tiles& tiles, int i) {
+        const int h = (threadIdx.x >> 5) & 1;
+        if (masks(i)) hide(a, pos, tiles(i) + 4 * h, [&](auto hidden) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (hidden(32 * b + 8 * (r >> 2) + (r & 3))) s[b][r] = -INFINITY;
+        });
+        float top = s[0][0];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (!sees(a, wr.pos, t0 + 32 * b + 8 * (r >> 2) + 4 * h + (r & 3))) s[b][r] = -INFINITY;
-    }
-    float top = s[0][0];
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+        if (__ballot(top * a.sl2 > m + kGrow)) {
+            const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
+            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
+            m = up;
+            l *= f;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
-    if (__ballot(top * a.sl2 > m + kGrow)) {
-        const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
-        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
-        m = up;
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < DB; ++d) acc[d] *= f;
-    }
-    const float off = m == -INFINITY ? 0.f : -m;
-    uint32_t pw[16];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
-            const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
-            const uint32_t pk = pack_bf16(p0, p1);
-            l = add_bf16_pair(pk, l);
-            pw[8 * b + r / 2] = pk;
+            for (int d = 0; d < D / 32; ++d) acc[d] *= f;
         }
-    if (CAREFUL && masked) {
+        const float off = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
+                const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
+                pw[8 * b + r / 2] = pack_bf16(p0, p1);
+            }
+    }
+    // the product of each row's visible tokens alone
+    __device__ __forceinline__ void careful_product(const AttnArgs& a, const char* vt, int t0) {
+        const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
         // one pair of rows' weights after the other, each register moved down
         // to the first: a rolled loop over registers
 #pragma unroll 1
         for (int j = 0; j < 16; ++j) {
             const uint32_t cur = pw[0];
+            l = add_weights(cur, 0, l);
 #pragma unroll
             for (int k = 0; k < 15; ++k) pw[k] = pw[k + 1];
 #pragma unroll 1
@@ -526,194 +667,307 @@ __device__ __forceinline__ void wide_tile(const AttnArgs& a, const WideRows& wr,
                 const float p = x & 1 ? bf16_hi(both) : bf16_lo(both);
                 const int r = 2 * (j & 7) + (x & 1);
                 const int tok = 32 * (j >> 3) + 8 * (r >> 2) + 4 * (x >> 1) + (r & 3);
-                const bool vis = sees(a, wr.pos, t0 + tok);
+                const bool vis = sees(a, pos, t0 + tok);
 #pragma unroll
-                for (int d = 0; d < DB; ++d)
+                for (int d = 0; d < D / 32; ++d)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int el = 32 * d + 8 * (e >> 2) + 4 * h + (e & 3);
-                        const float v = v_elem(vt, RB, tok, v_chunk<D>(tok, el >> 3), el & 7);
+                        const float v = v_elem(vt, 2 * D, tok, v_chunk<D>(tok, el >> 3), el & 7);
                         acc[d][e] = vis ? fmaf(p, v, acc[d][e]) : acc[d][e];
                     }
             }
         }
-        return;
     }
+    // the rows' output, or their partial result
+    __device__ __forceinline__ void finish(const AttnArgs& a, const Item& it, int head, bool mine) const {
+        const int h = (threadIdx.x >> 5) & 1;
+        const float total = l[0] + __shfl_xor(l[0], 32);
+        if (!mine) return;
+        if (it.nsplits == 1) {
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            uint16_t* o = a.out + row_off(a, it, it.row0 + row, head, a.ldo, D) + 4 * h;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const u32x4_t pf = {pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]};
-        const int i16 = lane & 15, g = (lane >> 4) & 1;
-        const int r = 16 * c + 4 * h + (i16 >> 2);
+            for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-            const int ch = 4 * d + 2 * g + ((i16 & 3) >> 1), by = 8 * (i16 & 1);
-            const u32x2_t lo = ds_tr16(vt + r * RB + 16 * v_chunk<D>(r, ch) + by);
-            const u32x2_t hi = ds_tr16(vt + (r + 8) * RB + 16 * v_chunk<D>(r + 8, ch) + by);
-            acc[d] = mfma32(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
+                for (int b = 0; b < 4; ++b)
+                    *reinterpret_cast<u32x2_t*>(o + 32 * d + 8 * b) =
+                        u32x2_t{pack_bf16(acc[d][4 * b] * inv, acc[d][4 * b + 1] * inv),
+                                pack_bf16(acc[d][4 * b + 2] * inv, acc[d][4 * b + 3] * inv)};
+        } else {
+            const int64_t pr = head * a.part_rows + it.part + row;
+            float* o = a.part + pr * D + 4 * h;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    *reinterpret_cast<f32x4_t*>(o + 32 * d + 8 * b) =
+                        f32x4_t{acc[d][4 * b], acc[d][4 * b + 1], acc[d][4 * b + 2], acc[d][4 * b + 3]};
+            if (h == 0) {
+                float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D + 2 * pr;
+                ml[0] = m;
+                ml[1] = total;
+            }
         }
     }
-}
-
-// The item's tiles, the next one on its way to one half of LDS while the other
-// is worked on; true where the result is not finite.
-template <int D, bool E4M3, bool UNI, bool CAREFUL>
-__device__ __forceinline__ bool wide_pass(const AttnArgs& a, const Item& it, const WideRows& wr, int head,
-                                          const u32x4_t (&qf)[D / 16], char (&even)[2][AT_TILE * 2 * D],
-                                          char (&odd)[2][AT_TILE * 2 * D], f32x16_t (&acc)[D / 32], float& m, float& l) {
+    // The compiler may not move the multiplications, or the weights, past here: a
+    // barrier alone orders memory, not registers.
+    __device__ __forceinline__ void multiplied() {
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) acc[d] = f32x16_t{};
-    m = -INFINITY;
-    l = 0.f;
-    Stage<D, E4M3, UNI, !E4M3, AT_TILE, 256> st;
-    st.init(a.kv, it, head, threadIdx.x, wave_id());
-    const int n = it.it1 - it.it0;
-    const auto tile = [&](int i) { return AT_TILE * at_span_tile(it.span, min(it.it0 + i, it.it1 - 1)); };
-    if (n > 0) {
-        st.look_up(a.kv, tile(0));
-        st.load(a.kv, head, tile(0), even[0], even[1]);
-        st.look_up(a.kv, tile(1));
+        for (int b = 0; b < 2; ++b) asm volatile("" : "+v"(s[b]));
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) asm volatile("" : "+v"(acc[d]));
     }
-    const auto step = [&](int i, char (&mine)[2][AT_TILE * 2 * D], char (&next)[2][AT_TILE * 2 * D]) {
-        st.store(mine[0], mine[1]);
-        __syncthreads();
-        const int t0 = tile(i);
-        if (i + 1 < n) {
-            st.load(a.kv, head, tile(i + 1), next[0], next[1]);
-            st.look_up(a.kv, tile(i + 2));
-        }
-        if (wr.active && !none_sees(a, wr.p_lo, wr.p_hi, t0, t0 + AT_TILE - 1))
-            wide_tile<D, CAREFUL>(a, wr, qf, mine[0], mine[1], t0, acc, m, l);
-    };
-    for (int i = 0; i < n; i += 2) {
-        step(i, even, odd);
-        if (i + 1 < n) step(i + 1, odd, even);
+    __device__ __forceinline__ void weighed() {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) asm volatile("" : "+v"(pw[i]));
     }
-    float bad = 0.f;
+    __device__ __forceinline__ bool not_finite() const {
+        float bad = 0.f;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+        for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) bad = fmaf(acc[d][e], 0.f, bad);
-    return wr.active && bad != 0.f;
-}
+            for (int e = 0; e < 16; ++e) bad = fmaf(acc[d][e], 0.f, bad);
+        return active && bad != 0.f;
+    }
+};
 
-// Four waves, 32 rows each; tiles of 64 tokens go through LDS.
+// Tile number -> first token, for a workgroup that takes all of the item's tiles.
+// Numbers past the last one stand for the last.
+struct AllTiles {
+    AtSpan span;
+    int32_t it0, last;
+    __device__ __forceinline__ int operator()(int i) const { return AT_TILE * at_span_tile(span, min(it0 + i, last)); }
+};
+
+// A wave has 32 rows.  A tile of 64 tokens is 32 MFMAs for it (1024 cycles of the
+// matrix unit) and about as many cycles of vector instructions.
+//
+// PAIR: eight waves, 256 rows.  Each SIMD has one wave of either half, and they
+// alternate: between two barriers one half multiplies (the scores of its tile i
+// and the product of tile i - 1) while the other one is at its softmax.  Left to
+// themselves the two waves of a SIMD fell into step and took turns at both units.
+// Otherwise four waves, 128 rows, and two workgroups to a compute unit.
+//
+// Keys and values have NB tiles each in LDS.  Keys i + LEAD and values i + LEAD - 1
+// are sent for between the multiplications of tile i (EARLY) or in its softmax,
+// into the place of tiles that every wave is done with; a wave waits for its own
+// share of keys i + 1 and values i at the barrier before the first half
+// multiplies them.  Past the last tile it is sent for again, which no one reads:
+// without branches the scalar work hides between the multiplications.
 //
 // A value that is infinite or NaN in a place that a row does not see would
 // still reach it through the second product (0 * NaN).  Looking for such values
 // in every masked tile costs more than it is worth, so the item looks at its
 // result: when that is not finite, it is computed again, and the tiles in which
 // some row is masked take each row's visible tokens alone.
-template <int D, bool E4M3, bool UNI>
-__global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a) {
-    constexpr int DB = D / 32;
-    __shared__ __align__(16) char even[2][AT_TILE * 2 * D];
-    __shared__ __align__(16) char odd[2][AT_TILE * 2 * D];
+template <int D, bool E4M3, bool UNI, bool PAIR>
+__global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs a) {
+    constexpr int BYTES = AT_TILE * 2 * D, NW = PAIR ? 8 : 4, NB = PAIR ? 4 : 2, LEAD = PAIR ? 3 : 2;
+    constexpr bool DIRECT = !E4M3, EARLY = DIRECT && PAIR && UNI;
+    typedef Stage<D, E4M3, UNI, DIRECT, false, NW, AT_TILE> KStage;
+    typedef Stage<D, E4M3, UNI, DIRECT, true, NW, AT_TILE> VStage;
+    constexpr int BOTH = KStage::STEPS + VStage::STEPS;  // loads of a wave for a tile's keys and values
+    __shared__ __align__(16) char lds[2][NB][BYTES];
     const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
     const int col = lane & 31, h = lane >> 5;
+    const bool second = PAIR && w >= 4;
     Item it;
-    if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_WIDE_ROWS, it)) return;
+    if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, 32 * NW, it)) return;
 
-    WideRows wr;
-    wr.row = min(32 * w + col, it.nrows - 1);  // lanes past the item's rows repeat its last one
-    wr.active = 32 * w < it.nrows;
-    wr.pos = it.p0 + (it.row0 + wr.row) / a.group;
-    wr.p_lo = it.p0 + (it.row0 + min(32 * w, it.nrows - 1)) / a.group;
-    wr.p_hi = it.p0 + (it.row0 + min(32 * w + 31, it.nrows - 1)) / a.group;
-    u32x4_t qf[D / 16];
+    Wide<D> x;
+    x.row = min(32 * w + col, it.nrows - 1);  // lanes past the item's rows repeat its last one
+    x.active = 32 * w < it.nrows;
+    x.pos = it.p0 + (it.row0 + x.row) / a.group;
+    x.p_lo = it.p0 + (it.row0 + min(32 * w, it.nrows - 1)) / a.group;
+    x.p_hi = it.p0 + (it.row0 + min(32 * w + 31, it.nrows - 1)) / a.group;
     {
-        const uint16_t* q = a.q + row_off(a, it, it.row0 + wr.row, head, a.ldq, D) + 8 * h;
+        const uint16_t* q = a.q + row_off(a, it, it.row0 + x.row, head, a.ldq, D) + 8 * h;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const u32x4_t*>(q + 16 * s);
+        for (int s = 0; s < D / 16; ++s) x.qf[s] = *reinterpret_cast<const u32x4_t*>(q + 16 * s);
         // they arrive here: a wait for them inside the loop over tiles would
         // be one for the copies that are under way there
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(qf[s]));
+        for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(x.qf[s]));
     }
-    f32x16_t acc[DB];
-    float m, l;
-    if (__syncthreads_or(wide_pass<D, E4M3, UNI, false>(a, it, wr, head, qf, even, odd, acc, m, l)))
-        wide_pass<D, E4M3, UNI, true>(a, it, wr, head, qf, even, odd, acc, m, l);
+    const int n = it.it1 - it.it0;
+    if (n <= 0) {  // the rows see nothing
+        x.clear();
+        x.finish(a, it, head, 32 * w + col < it.nrows);
+        return;
+    }
+    const AllTiles tile{it.span, it.it0, it.it1 - 1};
+    const auto keys = [&](int i) { return lds[0][i % NB]; };
+    const auto values = [&](int i) { return lds[1][i % NB]; };
+    KStage ks;
+    VStage vs;
+    ks.init(a.kv, head, w);
+    vs.init(a.kv, head, w);
+    Places<D, E4M3, UNI, NW, AT_TILE, AllTiles> places(a.kv, it, tile, head, w);
+    x.find_whole(a, it);
 
-    if (!wr.active) return;
-    l += __shfl_xor(l, 32);
-    if (32 * w + col >= it.nrows) return;
-    if (it.nsplits == 1) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* o = a.out + row_off(a, it, it.row0 + wr.row, head, a.ldo, D) + 4 * h;
+    // values i + LEAD - 1 lie where keys i + LEAD - 1 did
+    const auto plan = [&](int i) {
+        if (i + LEAD > 0) vs.take(places);
+        places.read(i + LEAD);
+        ks.take(places);
+    };
+    const auto send_values = [&](int i) {
+        if (i + LEAD > 0) vs.load(values(i + LEAD - 1));
+    };
+    const auto send_keys = [&](int i) { ks.load(keys(i + LEAD)); };
+    // codes sent for the last time, into LDS
+    const auto unpack = [&](int i) {
+        if (DIRECT || i == -LEAD) return;
+        if (i + LEAD > 1) vs.store(values(i + LEAD - 2));
+        ks.store(keys(i + LEAD - 1));
+    };
+    places.look_up(0);
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                *reinterpret_cast<u32x2_t*>(o + 32 * d + 8 * b) =
-                    u32x2_t{pack_bf16(acc[d][4 * b] * inv, acc[d][4 * b + 1] * inv),
-                            pack_bf16(acc[d][4 * b + 2] * inv, acc[d][4 * b + 3] * inv)};
-    } else {
-        const int64_t pr = head * a.part_rows + it.part + wr.row;
-        float* o = a.part + pr * D + 4 * h;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                *reinterpret_cast<f32x4_t*>(o + 32 * d + 8 * b) =
-                    f32x4_t{acc[d][4 * b], acc[d][4 * b + 1], acc[d][4 * b + 2], acc[d][4 * b + 3]};
-        if (h == 0) {
-            float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D + 2 * pr;
-            ml[0] = m;
-            ml[1] = l;
-        }
+    for (int i = -LEAD; i < 0; ++i) {
+        places.open(i + LEAD);
+        plan(i);
+        unpack(i);
+        send_values(i);
+        send_keys(i);
     }
+    places.open(LEAD);
+    wait_loads<DIRECT ? (LEAD - 1) * BOTH : 0>();
+    barrier();
+    if (second) barrier();
+    const auto phase = [&](int i) {
+        x.multiplied();
+        __builtin_amdgcn_s_setprio(0);
+        barrier();
+        if (!EARLY) {
+            unpack(i);
+            plan(i);
+            send_values(i);
+            send_keys(i);
+        }
+        places.open(i + 1 + LEAD);
+        x.weights(a, tile, i);
+        x.weighed();
+        if (DIRECT && !second) wait_loads<(LEAD - 1) * BOTH>();
+        barrier();
+        __builtin_amdgcn_s_setprio(1);  // the matrix unit goes first
+    };
+    const auto arrive = [&] {  // without EARLY, this tile's have not been sent for yet
+        if (DIRECT && second) wait_loads<(LEAD - (EARLY ? 1 : 2)) * BOTH>();
+    };
+    const auto among = [&](int i) {
+        return [&, i](int f) {
+            if (EARLY && f == 1) plan(i);
+            if (EARLY && f == D / 32) send_values(i);
+            if (EARLY && f == D / 16 - 1) send_keys(i);
+        };
+    };
+    const auto nothing = [](int) {};
+    x.clear();
+    x.template multiply<true, false>(keys(0), nullptr, among(0));
+    arrive();
+    int i = 0;
+    for (; i < n - 1; ++i) {
+        phase(i);
+        x.template multiply<true, true>(keys(i + 1), values(i), among(i + 1));
+        arrive();
+    }
+    phase(i);
+    x.template multiply<false, true>(nullptr, values(i), nothing);
+    wait_loads<0>();
+    if (PAIR && !second) barrier();
+
+    if (__syncthreads_or(x.not_finite())) {
+        x.clear();
+        places.look_up(0);
+        i = 0;
+        do {
+            places.open(i);
+            places.read(i);
+            ks.take(places);
+            vs.take(places);
+            ks.load(keys(0));
+            vs.load(values(0));
+            ks.store(keys(0));
+            vs.store(values(0));
+            wait_loads<0>();
+            barrier();
+            x.template multiply<true, false>(keys(0), nullptr, nothing);
+            x.weights(a, tile, i);
+            if (x.masks(i)) x.careful_product(a, values(0), tile(i));
+            else x.template multiply<false, true>(nullptr, values(0), nothing);
+            barrier();
+        } while (++i < n);
+    }
+
+    x.finish(a, it, head, 32 * w + col < it.nrows);
 }
 
-// The narrow kernel's tiles of 32 tokens of one wave, every fourth of the item's;
-// true where the result is not finite.
+// Tile number -> first token of the tiles of 32 that one of the narrow kernel's
+// four waves takes.
+struct EveryFourth {
+    AtSpan span;
+    int32_t first, last;
+    __device__ __forceinline__ int operator()(int i) const {
+        const int x = min(first + 4 * i, last);
+        return AT_TILE * at_span_tile(span, x >> 1) + 32 * (x & 1);
+    }
+};
+
+// One wave's tiles in the narrow kernel; true where the result is not finite.
 template <int D, bool E4M3, bool UNI, bool CAREFUL>
 __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, int pos, int p_lo, int p_hi, int head,
                                             int w, const u32x4_t (&qf)[D / 32], char* kt, char* vt,
-                                            f32x4_t (&acc)[D / 16], float& m, float& l) {
+                                            f32x4_t (&acc)[D / 16], float& m, f32x4_t& l) {
     constexpr int RB = 2 * D, DB = D / 16, KS = D / 32, T = 32;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-    const int first = 2 * it.it0 + w, end = 2 * it.it1;
-    const auto tile = [&](int i) {
-        i = min(i, end - 1);
-        return AT_TILE * at_span_tile(it.span, i >> 1) + T * (i & 1);
-    };
+    const int n = max(0, 2 * it.it1 - 2 * it.it0 - w + 3) >> 2;
+    const EveryFourth tile{it.span, 2 * it.it0 + w, 2 * it.it1 - 1};
 #pragma unroll
     for (int d = 0; d < DB; ++d) acc[d] = f32x4_t{};
     m = -INFINITY;
-    l = 0.f;
-    Stage<D, E4M3, UNI, false, T, 64> st;
-    st.init(a.kv, it, head, lane, 0);
-    if (first < end) {
-        st.look_up(a.kv, tile(first));
-        st.load(a.kv, head, tile(first), kt, vt);
-        st.look_up(a.kv, tile(first + 4));
+    l = f32x4_t{};
+    Stage<D, E4M3, UNI, false, false, 1, T> ks;
+    Stage<D, E4M3, UNI, false, true, 1, T> vs;
+    ks.init(a.kv, head, 0);
+    vs.init(a.kv, head, 0);
+    Places<D, E4M3, UNI, 1, T, EveryFourth> places(a.kv, it, tile, head, 0);
+    const auto send = [&](int i) {
+        places.open(i);
+        places.read(i);
+        ks.take(places);
+        vs.take(places);
+        ks.load(kt);
+        vs.load(vt);
+    };
+    if (n > 0) {
+        places.look_up(0);
+        send(0);
     }
-    for (int i = first; i < end; i += 4) {
+    for (int i = 0; i < n; ++i) {
         const int t0 = tile(i);
-        st.store(kt, vt);
-        if (i + 4 < end) {
-            st.load(a.kv, head, tile(i + 4), kt, vt);
-            st.look_up(a.kv, tile(i + 8));
-        }
+        ks.store(kt);
+        vs.store(vt);
+        if (i + 1 < n) send(i + 1);
         if (none_sees(a, p_lo, p_hi, t0, t0 + T - 1)) continue;
 
         f32x4_t s[2] = {f32x4_t{}, f32x4_t{}};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int r = 16 * b + col;
-                s[b] = mfma16(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 4 * ks + g)), qf[ks],
+                s[b] = mfma16(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 4 * k + g)), qf[k],
                               s[b]);
             }
         const bool masked = !all_see(a, p_lo, p_hi, t0, t0 + T - 1);
-        if (masked) {
+        if (masked) hide(a, pos, t0 + 4 * g, [&](auto hidden) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (!sees(a, pos, t0 + 16 * b + 4 * g + r)) s[b][r] = -INFINITY;
-        }
+                    if (hidden(16 * b + r)) s[b][r] = -INFINITY;
+        });
         float top = s[0][0];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -736,10 +990,10 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
             for (int r = 0; r < 4; r += 2) {
                 const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
                 const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
-                const uint32_t pk = pack_bf16(p0, p1);
-                l = add_bf16_pair(pk, l);
-                pw[2 * b + r / 2] = pk;
+                pw[2 * b + r / 2] = pack_bf16(p0, p1);
             }
+        l = add_weights(pw[0], pw[1], l);
+        l = add_weights(pw[2], pw[3], l);
         if (CAREFUL && masked) {
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
@@ -805,12 +1059,13 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
         for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4_t*>(q + 32 * s);
     }
     f32x4_t acc[DB];
-    float m, l;
-    if (narrow_pass<D, E4M3, UNI, false>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w][0], lds[w][1], acc, m, l))
-        narrow_pass<D, E4M3, UNI, true>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w][0], lds[w][1], acc, m, l);
+    float m;
+    f32x4_t sum;
+    if (narrow_pass<D, E4M3, UNI, false>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w][0], lds[w][1], acc, m, sum))
+        narrow_pass<D, E4M3, UNI, true>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w][0], lds[w][1], acc, m, sum);
 
     // join the waves: each leaves its maximum, sum and [row][D] accumulator in LDS
-    l += __shfl_xor(l, 16);
+    float l = sum[0] + __shfl_xor(sum[0], 16);
     l += __shfl_xor(l, 32);
     if (g == 0) {
         s_m[w][col] = m;
@@ -823,7 +1078,7 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
     constexpr int EPT = D / 16;  // elements per thread: 16 threads a row
     const int r = threadIdx.x / 16, e0 = (threadIdx.x % 16) * EPT;
     if (r >= it.nrows) return;
-    float top = s_m[0][r], sum = 0.f, o[EPT];
+    float top = s_m[0][r], total = 0.f, o[EPT];
 #pragma unroll
     for (int x = 1; x < 4; ++x) top = fmaxf(top, s_m[x][r]);
 #pragma unroll
@@ -833,13 +1088,13 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
         const float mx = s_m[x][r];
         if (mx == -INFINITY) continue;
         const float f = __builtin_amdgcn_exp2f(mx - top);
-        sum = fmaf(f, s_l[x][r], sum);
+        total = fmaf(f, s_l[x][r], total);
         const float* p = reinterpret_cast<const float*>(lds[x][0]) + r * D + e0;
 #pragma unroll
         for (int e = 0; e < EPT; ++e) o[e] = fmaf(f, p[e], o[e]);
     }
     if (it.nsplits == 1) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
         uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row_off(a, it, it.row0 + r, head, a.ldo, D) + e0);
 #pragma unroll
         for (int e = 0; e < EPT; e += 2) dst[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
@@ -851,7 +1106,7 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
         if (threadIdx.x % 16 == 0) {
             float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D + 2 * pr;
             ml[0] = top;
-            ml[1] = sum;
+            ml[1] = total;
         }
     }
 }
@@ -859,10 +1114,10 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
 // Joins the splits of one row tile, in their order: D/4 lanes a row.
 template <int D>
 __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
-    constexpr int LPR = D / 4, RPB = 256 / LPR, PARTS = AT_WIDE_ROWS / RPB;  // workgroups per tile and head
+    constexpr int LPR = D / 4, RPB = 256 / LPR, PARTS = AT_PAIR_ROWS / RPB;  // workgroups per tile and head
     const int head = blockIdx.x % a.kv.n_kv_heads, block = blockIdx.x / a.kv.n_kv_heads;
     Item it;
-    if (!load_item(a, block / PARTS, AT_WIDE_ROWS, it)) return;
+    if (!load_item(a, block / PARTS, AT_PAIR_ROWS, it)) return;
     if ((int64_t)it.part + (int64_t)it.nsplits * it.nrows > a.part_rows) return;
     const int r = (block % PARTS) * RPB + threadIdx.x / LPR, e0 = 4 * (threadIdx.x % LPR);
     if (r >= it.nrows) return;
@@ -1024,8 +1279,8 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
         if (workspace_floats < I.workspace_floats) return LORA_ECAPACITY;
         if (!workspace || !aligned16(workspace)) return LORA_EINVAL;
     }
-    const int64_t parts = AT_WIDE_ROWS / (256 / (d / 4));  // merge workgroups per row tile and head
-    for (const int64_t n : {(int64_t)I.n_work[0], (int64_t)I.n_work[1], I.n_merge * parts})
+    const int64_t parts = AT_PAIR_ROWS / (256 / (d / 4));  // merge workgroups per row tile and head
+    for (const int64_t n : {(int64_t)I.n_work[0], (int64_t)I.n_work[1], (int64_t)I.n_work[2], I.n_merge * parts})
         if (n < 0 || n * hk > kMaxBlocks) return LORA_EINVAL;
     AttnArgs a;
     memset(&a, 0, sizeof(a));
@@ -1048,20 +1303,23 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     const hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
     const bool e4m3 = kv->dtype == LORA_KV_E4M3;
     typedef void (*fn_t)(AttnArgs);
-#define AT_FORMS(kernel, d) \
-    {{kernel<d, false, false>, kernel<d, false, true>}, {kernel<d, true, false>, kernel<d, true, true>}}
-    static const fn_t fn[2][2][2][2] = {{AT_FORMS(attn_narrow_kernel, 64), AT_FORMS(attn_narrow_kernel, 128)},
-                                        {AT_FORMS(attn_wide_kernel, 64), AT_FORMS(attn_wide_kernel, 128)}};
+#define AT_FORMS(kernel, d, ...)                                                        \
+    {{kernel<d, false, false, ##__VA_ARGS__>, kernel<d, false, true, ##__VA_ARGS__>},   \
+     {kernel<d, true, false, ##__VA_ARGS__>, kernel<d, true, true, ##__VA_ARGS__>}}
+    static const fn_t fn[LORA_ATTN_KINDS][2][2][2] = {
+        {AT_FORMS(attn_narrow_kernel, 64), AT_FORMS(attn_narrow_kernel, 128)},
+        {AT_FORMS(attn_wide_kernel, 64, false), AT_FORMS(attn_wide_kernel, 128, false)},
+        {AT_FORMS(attn_wide_kernel, 64, true), AT_FORMS(attn_wide_kernel, 128, true)}};
 #undef AT_FORMS
-    // where Stage can work with scalar page addresses: 32-bit strides in bytes, 64 rows' offsets among them
-    const bool small = kv->token_stride <= INT32_MAX / 128 && kv->page_stride <= INT32_MAX / 2;
-    for (int kind = 1; kind >= 0; --kind) {  // the longer items first
+    // where Places can work with scalar page offsets: a step's rows in one page, 32-bit strides and scale offsets
+    const bool uni = kv->page_tokens >= 64 / (d / 8) && kv->token_stride <= INT32_MAX / 64 &&
+                     kv->page_stride <= INT32_MAX && (int64_t)kv->n_pages * kv->page_tokens * hk <= UINT32_MAX;
+    for (int kind = LORA_ATTN_KINDS - 1; kind >= 0; --kind) {  // the longer items first
         if (I.n_work[kind] == 0) continue;
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_work[kind]);
         a.n_work = I.n_work[kind];
-        const bool uni = small && kv->page_tokens >= (kind == LORA_ATTN_WIDE ? 256 : 64) / (d / 8);
-        if (launch(fn[kind][d == 128][e4m3][uni], dim3((unsigned)(a.n_work * hk)), dim3(256), s, a) != hipSuccess)
-            return LORA_EHIP;
+        const dim3 grid((unsigned)(a.n_work * hk)), block(kind == LORA_ATTN_PAIR ? 512 : 256);
+        if (launch(fn[kind][d == 128][e4m3][uni], grid, block, s, a) != hipSuccess) return LORA_EHIP;
     }
     if (I.n_merge > 0) {
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_merge);

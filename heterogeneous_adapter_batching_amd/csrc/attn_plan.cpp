@@ -12,8 +12,8 @@
 
 namespace {
 
-// Workgroups that the chip works on at once: 256 compute units, two each.
-constexpr int64_t kSlots = 512;
+// Workgroups of each kernel that the chip works on at once: 256 compute units.
+constexpr int64_t kSlots[LORA_ATTN_KINDS] = {512, 512, 256};
 // Fewest tiles of one split: below four (256 tokens) a split's partial result
 // costs more than the tiles it takes off the longest workgroup.
 constexpr int64_t kMinTiles = 4;
@@ -32,13 +32,13 @@ int32_t check_shape(const lora_attn_shape_t& s) {
     return LORA_OK;
 }
 
-// Cuts every row tile of `kind` into splits of about equal tiles, so that all
-// heads' splits together fill the chip, and appends items and merges.
-void split(const std::vector<Tile>& tiles, int32_t n_kv_heads, std::vector<lora_attn_work_t>& work,
+// Cuts every row tile of one kernel into splits of about equal tiles, so that all
+// heads' splits together fill the chip's slots, and appends items and merges.
+void split(const std::vector<Tile>& tiles, int64_t slots, int32_t n_kv_heads, std::vector<lora_attn_work_t>& work,
            std::vector<lora_attn_work_t>& merge, int64_t& part_rows) {
     int64_t total = 0;
     for (const Tile& t : tiles) total += t.tiles;
-    const int64_t most = std::max(kMinTiles, (total * n_kv_heads + kSlots - 1) / kSlots);
+    const int64_t most = std::max(kMinTiles, (total * n_kv_heads + slots - 1) / slots);
     for (const Tile& t : tiles) {
         const int32_t n = (int32_t)std::max<int64_t>(1, (t.tiles + most - 1) / most);
         const int32_t first = (int32_t)part_rows;
@@ -80,20 +80,23 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
             if (row[i] < 0 || row[i] >= s.n_pages) return LORA_EPAGE;
     }
 
-    std::vector<Tile> tiles[2];
+    std::vector<Tile> tiles[LORA_ATTN_KINDS];
     for (int32_t b = 0; b < n_seq; ++b) {
         const int32_t rows = q_len[b] * group, p0 = kv_len[b] - q_len[b];
-        const int kind = rows <= AT_NARROW_ROWS ? LORA_ATTN_NARROW : LORA_ATTN_WIDE;
-        const int32_t step = kind == LORA_ATTN_NARROW ? AT_NARROW_ROWS : AT_WIDE_ROWS;
-        for (int32_t r = 0; r < rows; r += step) {
-            const int32_t n = std::min(step, rows - r);
+        for (int32_t r = 0, n = 0; r < rows; r += n) {
+            const int32_t left = rows - r;
+            const int kind = left <= AT_NARROW_ROWS ? LORA_ATTN_NARROW
+                           : left <= AT_WIDE_ROWS   ? LORA_ATTN_WIDE
+                                                    : LORA_ATTN_PAIR;
+            n = std::min(left, (int32_t)AT_PAIR_ROWS);
             const AtSpan sp = at_span(p0 + r / group, p0 + (r + n - 1) / group, s.window, s.sinks);
             tiles[kind].push_back({b, r, n, at_span_tiles(sp)});
         }
     }
-    std::vector<lora_attn_work_t> work[2], merge;
+    std::vector<lora_attn_work_t> work[LORA_ATTN_KINDS], merge;
     int64_t part_rows = 0;
-    for (int kind = 0; kind < 2; ++kind) split(tiles[kind], s.n_kv_heads, work[kind], merge, part_rows);
+    for (int kind = 0; kind < LORA_ATTN_KINDS; ++kind)
+        split(tiles[kind], kSlots[kind], s.n_kv_heads, work[kind], merge, part_rows);
 
     if (part_rows > INT32_MAX) return LORA_EINVAL;
     constexpr int64_t wi = sizeof(lora_attn_work_t) / sizeof(int32_t);
@@ -114,7 +117,7 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
         off += (n + 3) / 4 * 4;
         return at;
     };
-    for (int kind = 0; kind < 2; ++kind) {
+    for (int kind = 0; kind < LORA_ATTN_KINDS; ++kind) {
         out.n_work[kind] = (int32_t)work[kind].size();
         out.off_work[kind] = place(wi * out.n_work[kind]);
     }
@@ -133,7 +136,7 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
     const auto put = [staging](int64_t at, const std::vector<lora_attn_work_t>& v) {
         if (!v.empty()) memcpy(staging + at, v.data(), v.size() * sizeof(lora_attn_work_t));
     };
-    for (int kind = 0; kind < 2; ++kind) put(out.off_work[kind], work[kind]);
+    for (int kind = 0; kind < LORA_ATTN_KINDS; ++kind) put(out.off_work[kind], work[kind]);
     put(out.off_merge, merge);
     int32_t *q_start = staging + out.off_q_start, *kv_start = staging + out.off_kv_start;
     int32_t row = 0, token = 0;

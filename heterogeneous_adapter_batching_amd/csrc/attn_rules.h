@@ -11,8 +11,10 @@
 #endif
 
 #define AT_TILE 64          // cached tokens of one tile
-#define AT_WIDE_ROWS 128    // query rows of one item of the wide kernel
-#define AT_NARROW_ROWS 16   // and of the narrow one
+// query rows of one item of the kernels
+#define AT_NARROW_ROWS 16
+#define AT_WIDE_ROWS 128
+#define AT_PAIR_ROWS 256
 
 // Tiles that queries at positions p_lo .. p_hi may see, as a list: the first
 // `sinks` tiles 0 .. sinks-1, then `first` .. `end`-1.

@@ -720,6 +720,8 @@ typedef struct lora_attn_work {
 
 #define LORA_ATTN_NARROW 0  /* kernels: up to 16 rows, four waves share the tokens */
 #define LORA_ATTN_WIDE 1    /* up to 128 rows, four waves share the rows           */
+#define LORA_ATTN_PAIR 2    /* up to 256 rows, eight waves in two alternating halves */
+#define LORA_ATTN_KINDS 3
 
 /* Host-side summary of an attention plan, and where its parts lie in the
  * staging buffer (off_*, in int32 elements). */
@@ -730,11 +732,11 @@ typedef struct lora_attn_info {
     int32_t n_tokens;           /* rows of lora_kv_read's outputs            */
     int32_t max_kv;             /* longest kv_len                            */
     int32_t ld_table;           /* pages per sequence in the staged table    */
-    int32_t n_work[2];          /* items by kernel (LORA_ATTN_*)             */
+    int32_t n_work[LORA_ATTN_KINDS];  /* items by kernel                     */
     int32_t n_merge;
     int64_t part_rows;          /* rows of partial results per kv head       */
     int64_t workspace_floats;   /* fp32 elements lora_attn needs             */
-    int64_t off_work[2];        /* lora_attn_work_t [n_work[kind]]           */
+    int64_t off_work[LORA_ATTN_KINDS];  /* lora_attn_work_t [n_work[kind]]   */
     int64_t off_merge;          /* lora_attn_work_t [n_merge]                */
     int64_t off_q_start;        /* [n_seq + 1] first row of each sequence    */
     int64_t off_kv_len;         /* [n_seq]                                   */

@@ -13,7 +13,8 @@ import heterogeneous_adapter_batching_amd as hl
 import oracle
 
 REPO = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-TILE, NARROW, WIDE = 64, 16, 128
+TILE = 64
+MOST = {hl.LORA_ATTN_NARROW: 16, hl.LORA_ATTN_WIDE: 128, hl.LORA_ATTN_PAIR: 256}  # rows of an item
 
 
 def shape(heads=8, kv_heads=2, dim=128, page=16, pages=1000, dtype=hl.LORA_KV_BF16, window=0, sinks=0):
@@ -47,7 +48,7 @@ def check_plan(s, q_len, kv_len, tab, staging, info):
     def items(off, n):
         return staging[off:off + 8 * n].reshape(-1, 8)
     tiles, parts = {}, []
-    for kind, most in ((hl.LORA_ATTN_NARROW, NARROW), (hl.LORA_ATTN_WIDE, WIDE)):
+    for kind, most in MOST.items():
         for seq, row0, nrows, it0, it1, split, nsplits, part in items(info.off_work[kind], info.n_work[kind]):
             assert 1 <= nrows <= most and 0 <= split < nsplits
             tiles.setdefault((seq, row0, nrows), []).append((split, it0, it1, nsplits, part))
@@ -99,7 +100,7 @@ def test_plan_covers_random_batches(window, sinks):
         kv_heads, group = int(rng.choice([1, 2, 8])), int(rng.choice([1, 3, 4, 7]))
         page = int(rng.choice([1, 8, 64]))
         n = int(rng.integers(0, 6))
-        q_len = rng.choice([0, 1, 1, 2, 17, 150], n)
+        q_len = rng.choice([0, 1, 1, 2, 17, 150, 300], n)
         kv_len = np.maximum(0, q_len + rng.choice([-3, 0, 1, 63, 64, 500], n))
         s = shape(kv_heads * group, kv_heads, 64, page, 4000, window=window, sinks=sinks)
         tab = make_table(rng, kv_len, page, 4000)
@@ -121,7 +122,7 @@ def test_plan_splits_long_contexts_and_counts_a_window():
 
 def test_plan_of_nothing():
     staging, info = hl.lora_attn_plan(shape(), [], [], None)
-    assert info.n_rows == 0 and info.n_work[0] == info.n_work[1] == 0
+    assert info.n_rows == 0 and list(info.n_work) == [0, 0, 0]
     staging, info = hl.lora_attn_plan(shape(), [2, 0], [0, 0], None)  # rows that see nothing still have an item
     assert info.n_work[0] == 1 and info.max_kv == 0
 
