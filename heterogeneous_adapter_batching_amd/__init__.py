@@ -32,6 +32,7 @@ LORA_KV_BF16, LORA_KV_E4M3 = 0, 1
 LORA_F32, LORA_BF16 = 0, 1
 LORA_ATTN_NARROW, LORA_ATTN_WIDE, LORA_ATTN_PAIR = 0, 1, 2
 LORA_ATTN_KINDS = 3
+ATTN_WORK_INTS = 12  # int32 fields of lora_attn_work_t
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built: run `python __graft_entry__.py` (build()) first")
@@ -128,8 +129,7 @@ class lora_attn_shape_t(ctypes.Structure):
 class lora_attn_info_t(ctypes.Structure):
     _fields_ = [("shape", lora_attn_shape_t), ("n_seq", _i32), ("n_rows", _i32), ("n_tokens", _i32),
                 ("max_kv", _i32), ("ld_table", _i32), ("n_work", _i32 * LORA_ATTN_KINDS), ("n_merge", _i32), ("part_rows", _i64),
-                ("workspace_floats", _i64), ("off_work", _i64 * LORA_ATTN_KINDS), ("off_merge", _i64), ("off_q_start", _i64),
-                ("off_kv_len", _i64), ("off_kv_start", _i64), ("off_row_pos", _i64), ("off_row_slot", _i64),
+                ("workspace_floats", _i64), ("off_work", _i64 * LORA_ATTN_KINDS), ("off_merge", _i64), ("off_kv_start", _i64), ("off_row_pos", _i64), ("off_row_slot", _i64),
                 ("off_table", _i64), ("n_staged", _i64)]
 
 

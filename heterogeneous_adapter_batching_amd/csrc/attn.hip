@@ -263,43 +263,38 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
 struct AttnArgs {
     Kv kv;
     const lora_attn_work_t* work;
-    const int32_t *q_start, *kv_len, *table;
+    const int32_t* table;
     const uint16_t* q;
     uint16_t* out;
     float* part;  // [n_kv_heads][part_rows][D] partial sums, then [n_kv_heads][part_rows][2] of (maximum, sum)
     int64_t ldq, ldo, part_rows;
-    int32_t n_seq, ld_table, n_work, group, window, sinks;
+    int32_t n_seq, n_rows, max_kv, ld_table, group, window, sinks;
     float sl2;  // scale * log2 e
 };
 
 // What every lane of an item needs to know.
-struct Item {
-    int32_t seq, row0, nrows, it0, it1, nsplits, part;
-    int32_t q0, n_new, kv, p0;  // first row, new tokens, cached tokens, position of the first new token
+struct Item : lora_attn_work_t {
+    int32_t p0;  // position of the first new token
     const int32_t* table;
     AtSpan span;
 };
 // Items that do not lie inside the batch are skipped, so a corrupted work list
 // cannot index outside the buffers.
-__device__ __forceinline__ bool load_item(const AttnArgs& a, int i, int max_rows, Item& it) {
-    const lora_attn_work_t w = a.work[i];
-    if (w.seq < 0 || w.seq >= a.n_seq) return false;
-    it.seq = w.seq;
-    it.row0 = w.row0;
-    it.nrows = w.nrows;
-    it.nsplits = w.nsplits;
-    it.part = w.part;
-    it.q0 = a.q_start[w.seq];
-    it.n_new = a.q_start[w.seq + 1] - it.q0;
-    it.kv = a.kv_len[w.seq];
-    it.p0 = it.kv - it.n_new;
-    it.table = a.table + (int64_t)w.seq * a.ld_table;
-    if (w.nrows < 1 || w.nrows > max_rows || w.row0 < 0 || (int64_t)w.row0 + w.nrows > (int64_t)it.n_new * a.group)
+__device__ __forceinline__ bool load_item(const AttnArgs& a, int i, int max_rows, bool merge, Item& it) {
+    static_cast<lora_attn_work_t&>(it) = a.work[i];
+    if (it.seq < 0 || it.seq >= a.n_seq || it.n_new < 0 || it.kv < 0 || it.q0 < 0 || it.q0 + it.n_new > a.n_rows ||
+        it.kv > a.max_kv)
         return false;
-    if (w.nsplits > 1 && (w.part < 0 || (int64_t)w.part + w.nrows > a.part_rows)) return false;
-    it.span = at_span(it.p0 + w.row0 / a.group, it.p0 + (w.row0 + w.nrows - 1) / a.group, a.window, a.sinks);
-    it.it0 = max(w.it0, 0);
-    it.it1 = min(w.it1, at_span_tiles(it.span));
+    if (it.nrows < 1 || it.nrows > max_rows || it.row0 < 0 ||
+        (int64_t)it.row0 + it.nrows > (int64_t)it.n_new * a.group)
+        return false;
+    if (it.nsplits > 1 && (it.part < 0 || it.part + (int64_t)it.nrows * (merge ? it.nsplits : 1) > a.part_rows))
+        return false;
+    it.p0 = it.kv - it.n_new;
+    it.table = a.table + (int64_t)it.seq * a.ld_table;
+    it.span = at_span(it.p0 + it.row0 / a.group, it.p0 + (it.row0 + it.nrows - 1) / a.group, a.window, a.sinks);
+    it.it0 = max(it.it0, 0);
+    it.it1 = min(it.it1, merge ? it.nrows : at_span_tiles(it.span));
     return true;
 }
 // Element offset of row r of the item's sequence (head r % group of kv head h, new token r / group).
@@ -763,7 +758,7 @@ struct AllTiles {
 // some row is masked take each row's visible tokens alone.
 template <int D, bool E4M3, bool UNI, bool PAIR>
 __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs a) {
-    constexpr int BYTES = AT_TILE * 2 * D, NW = PAIR ? 8 : 4, NB = PAIR ? 4 : 2, LEAD = PAIR ? 3 : 2;
+    constexpr int BYTES = AT_TILE * 2 * D, NW = PAIR ? 8 : 4, NB = PAIR ? 4 : 2, LEAD = 3;
     constexpr bool DIRECT = !E4M3, EARLY = DIRECT && PAIR && UNI;
     typedef Stage<D, E4M3, UNI, DIRECT, false, NW, AT_TILE> KStage;
     typedef Stage<D, E4M3, UNI, DIRECT, true, NW, AT_TILE> VStage;
@@ -771,9 +766,9 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
     __shared__ __align__(16) char lds[2][NB][BYTES];
     const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
     const int col = lane & 31, h = lane >> 5;
-    const bool second = PAIR && w >= 4;
+    [[maybe_unused]] const bool second = PAIR && w >= 4;
     Item it;
-    if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, 32 * NW, it)) return;
+    if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, 32 * NW, false, it)) return;
 
     Wide<D> x;
     x.row = min(32 * w + col, it.nrows - 1);  // lanes past the item's rows repeat its last one
@@ -805,82 +800,106 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
     vs.init(a.kv, head, w);
     Places<D, E4M3, UNI, NW, AT_TILE, AllTiles> places(a.kv, it, tile, head, w);
     x.find_whole(a, it);
-
-    // values i + LEAD - 1 lie where keys i + LEAD - 1 did
-    const auto plan = [&](int i) {
-        if (i + LEAD > 0) vs.take(places);
-        places.read(i + LEAD);
-        ks.take(places);
-    };
-    const auto send_values = [&](int i) {
-        if (i + LEAD > 0) vs.load(values(i + LEAD - 1));
-    };
-    const auto send_keys = [&](int i) { ks.load(keys(i + LEAD)); };
-    // codes sent for the last time, into LDS
-    const auto unpack = [&](int i) {
-        if (DIRECT || i == -LEAD) return;
-        if (i + LEAD > 1) vs.store(values(i + LEAD - 2));
-        ks.store(keys(i + LEAD - 1));
-    };
+    const auto nothing = [](int) {};
+    x.clear();
     places.look_up(0);
+    if constexpr (!PAIR) {
+        // Tile i's keys and values arrive together, behind the work on tile i - 1.
+        const auto send = [&](int i) {
+            places.open(i);
+            places.read(i);
+            ks.take(places);
+            vs.take(places);
+            ks.load(keys(i));
+            vs.load(values(i));
+        };
+        send(0);
+        for (int i = 0; i < n; ++i) {
+            ks.store(keys(i));
+            vs.store(values(i));
+            if (DIRECT) wait_loads<0>();
+            barrier();
+            if (i + 1 < n) send(i + 1);
+            const int t0 = tile(i);
+            if (!x.active || none_sees(a, x.p_lo, x.p_hi, t0, t0 + AT_TILE - 1)) continue;
+            x.template multiply<true, false>(keys(i), nullptr, nothing);
+            x.weights(a, tile, i);
+            x.template multiply<false, true>(nullptr, values(i), nothing);
+        }
+    } else {
+        // values i + LEAD - 1 lie where keys i + LEAD - 1 did
+        const auto plan = [&](int i) {
+            if (i + LEAD > 0) vs.take(places);
+            places.read(i + LEAD);
+            ks.take(places);
+        };
+        const auto send_values = [&](int i) {
+            if (i + LEAD > 0) vs.load(values(i + LEAD - 1));
+        };
+        const auto send_keys = [&](int i) { ks.load(keys(i + LEAD)); };
+        // codes sent for the last time, into LDS
+        const auto unpack = [&](int i) {
+            if (DIRECT || i == -LEAD) return;
+            if (i + LEAD > 1) vs.store(values(i + LEAD - 2));
+            ks.store(keys(i + LEAD - 1));
+        };
 #pragma unroll
-    for (int i = -LEAD; i < 0; ++i) {
-        places.open(i + LEAD);
-        plan(i);
-        unpack(i);
-        send_values(i);
-        send_keys(i);
-    }
-    places.open(LEAD);
-    wait_loads<DIRECT ? (LEAD - 1) * BOTH : 0>();
-    barrier();
-    if (second) barrier();
-    const auto phase = [&](int i) {
-        x.multiplied();
-        __builtin_amdgcn_s_setprio(0);
-        barrier();
-        if (!EARLY) {
-            unpack(i);
+        for (int i = -LEAD; i < 0; ++i) {
+            places.open(i + LEAD);
             plan(i);
+            unpack(i);
             send_values(i);
             send_keys(i);
         }
-        places.open(i + 1 + LEAD);
-        x.weights(a, tile, i);
-        x.weighed();
-        if (DIRECT && !second) wait_loads<(LEAD - 1) * BOTH>();
+        places.open(LEAD);
+        wait_loads<DIRECT ? (LEAD - 1) * BOTH : 0>();
         barrier();
-        __builtin_amdgcn_s_setprio(1);  // the matrix unit goes first
-    };
-    const auto arrive = [&] {  // without EARLY, this tile's have not been sent for yet
-        if (DIRECT && second) wait_loads<(LEAD - (EARLY ? 1 : 2)) * BOTH>();
-    };
-    const auto among = [&](int i) {
-        return [&, i](int f) {
-            if (EARLY && f == 1) plan(i);
-            if (EARLY && f == D / 32) send_values(i);
-            if (EARLY && f == D / 16 - 1) send_keys(i);
+        if (second) barrier();
+        const auto phase = [&](int i) {
+            x.multiplied();
+            __builtin_amdgcn_s_setprio(0);
+            barrier();
+            if (!EARLY) {
+                unpack(i);
+                plan(i);
+                send_values(i);
+                send_keys(i);
+            }
+            places.open(i + 1 + LEAD);
+            x.weights(a, tile, i);
+            x.weighed();
+            if (DIRECT && !second) wait_loads<(LEAD - 1) * BOTH>();
+            barrier();
+            __builtin_amdgcn_s_setprio(1);  // the matrix unit goes first
         };
-    };
-    const auto nothing = [](int) {};
-    x.clear();
-    x.template multiply<true, false>(keys(0), nullptr, among(0));
-    arrive();
-    int i = 0;
-    for (; i < n - 1; ++i) {
-        phase(i);
-        x.template multiply<true, true>(keys(i + 1), values(i), among(i + 1));
+        const auto arrive = [&] {  // without EARLY, this tile's have not been sent for yet
+            if (DIRECT && second) wait_loads<(LEAD - (EARLY ? 1 : 2)) * BOTH>();
+        };
+        const auto among = [&](int i) {
+            return [&, i](int f) {
+                if (EARLY && f == 1) plan(i);
+                if (EARLY && f == D / 32) send_values(i);
+                if (EARLY && f == D / 16 - 1) send_keys(i);
+            };
+        };
+        x.template multiply<true, false>(keys(0), nullptr, among(0));
         arrive();
+        int i = 0;
+        for (; i < n - 1; ++i) {
+            phase(i);
+            x.template multiply<true, true>(keys(i + 1), values(i), among(i + 1));
+            arrive();
+        }
+        phase(i);
+        x.template multiply<false, true>(nullptr, values(i), nothing);
+        wait_loads<0>();
+        if (!second) barrier();
     }
-    phase(i);
-    x.template multiply<false, true>(nullptr, values(i), nothing);
-    wait_loads<0>();
-    if (PAIR && !second) barrier();
 
     if (__syncthreads_or(x.not_finite())) {
         x.clear();
         places.look_up(0);
-        i = 0;
+        int i = 0;
         do {
             places.open(i);
             places.read(i);
@@ -1047,7 +1066,7 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
     const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
     const int col = lane & 15, g = lane >> 4;
     Item it;
-    if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_NARROW_ROWS, it)) return;
+    if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_NARROW_ROWS, false, it)) return;
 
     const int row = min(col, it.nrows - 1);
     const int pos = it.p0 + (it.row0 + row) / a.group;
@@ -1114,13 +1133,12 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
 // Joins the splits of one row tile, in their order: D/4 lanes a row.
 template <int D>
 __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
-    constexpr int LPR = D / 4, RPB = 256 / LPR, PARTS = AT_PAIR_ROWS / RPB;  // workgroups per tile and head
-    const int head = blockIdx.x % a.kv.n_kv_heads, block = blockIdx.x / a.kv.n_kv_heads;
+    constexpr int LPR = D / 4;
+    const int head = blockIdx.x % a.kv.n_kv_heads;
     Item it;
-    if (!load_item(a, block / PARTS, AT_PAIR_ROWS, it)) return;
-    if ((int64_t)it.part + (int64_t)it.nsplits * it.nrows > a.part_rows) return;
-    const int r = (block % PARTS) * RPB + threadIdx.x / LPR, e0 = 4 * (threadIdx.x % LPR);
-    if (r >= it.nrows) return;
+    if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_PAIR_ROWS, true, it)) return;
+    const int r = it.it0 + threadIdx.x / LPR, e0 = 4 * (threadIdx.x % LPR);
+    if (r >= it.it1) return;
     const int64_t first = head * a.part_rows + it.part + r;
     const float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D;
     float top = -INFINITY;
@@ -1279,14 +1297,11 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
         if (workspace_floats < I.workspace_floats) return LORA_ECAPACITY;
         if (!workspace || !aligned16(workspace)) return LORA_EINVAL;
     }
-    const int64_t parts = AT_PAIR_ROWS / (256 / (d / 4));  // merge workgroups per row tile and head
-    for (const int64_t n : {(int64_t)I.n_work[0], (int64_t)I.n_work[1], (int64_t)I.n_work[2], I.n_merge * parts})
+    for (const int64_t n : {I.n_work[0], I.n_work[1], I.n_work[2], I.n_merge})
         if (n < 0 || n * hk > kMaxBlocks) return LORA_EINVAL;
     AttnArgs a;
     memset(&a, 0, sizeof(a));
     a.kv = to_kv(*kv);
-    a.q_start = L->meta + I.off_q_start;
-    a.kv_len = L->meta + I.off_kv_len;
     a.table = L->meta + I.off_table;
     a.q = q;
     a.out = out;
@@ -1295,6 +1310,8 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     a.ldo = ldo;
     a.part_rows = I.part_rows;
     a.n_seq = I.n_seq;
+    a.n_rows = I.n_rows;
+    a.max_kv = I.max_kv;
     a.ld_table = I.ld_table;
     a.group = I.shape.n_heads / hk;
     a.window = I.shape.window;
@@ -1317,14 +1334,12 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     for (int kind = LORA_ATTN_KINDS - 1; kind >= 0; --kind) {  // the longer items first
         if (I.n_work[kind] == 0) continue;
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_work[kind]);
-        a.n_work = I.n_work[kind];
-        const dim3 grid((unsigned)(a.n_work * hk)), block(kind == LORA_ATTN_PAIR ? 512 : 256);
+        const dim3 grid((unsigned)(I.n_work[kind] * hk)), block(kind == LORA_ATTN_PAIR ? 512 : 256);
         if (launch(fn[kind][d == 128][e4m3][uni], grid, block, s, a) != hipSuccess) return LORA_EHIP;
     }
     if (I.n_merge > 0) {
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_merge);
-        a.n_work = I.n_merge;
-        const dim3 grid((unsigned)((int64_t)hk * I.n_merge * parts));
+        const dim3 grid((unsigned)(I.n_merge * hk));
         if (launch(d == 128 ? attn_merge_kernel<128> : attn_merge_kernel<64>, grid, dim3(256), s, a) != hipSuccess)
             return LORA_EHIP;
     }

@@ -17,9 +17,15 @@ constexpr int64_t kSlots[LORA_ATTN_KINDS] = {512, 512, 256};
 // Fewest tiles of one split: below four (256 tokens) a split's partial result
 // costs more than the tiles it takes off the longest workgroup.
 constexpr int64_t kMinTiles = 4;
+// Fewest tiles of a pair item.  It has one workgroup to a compute unit, whose
+// start nothing else covers, and 256 rows end later than 128 on a causal mask:
+// 16 prompts of up to 2048 tokens (32 heads) took 154 us on pair items and 124
+// on wide ones, 2 x 1024 tokens over 33k 1.90 and 1.98 ms.
+constexpr int32_t kPairTiles = 32;
 
 struct Tile {  // one row tile of one sequence before it is split
-    int32_t seq, row0, nrows, tiles;
+    lora_attn_work_t work;
+    int32_t tiles;
 };
 
 int32_t check_shape(const lora_attn_shape_t& s) {
@@ -32,22 +38,34 @@ int32_t check_shape(const lora_attn_shape_t& s) {
     return LORA_OK;
 }
 
-// Cuts every row tile of one kernel into splits of about equal tiles, so that all
-// heads' splits together fill the chip's slots, and appends items and merges.
-void split(const std::vector<Tile>& tiles, int64_t slots, int32_t n_kv_heads, std::vector<lora_attn_work_t>& work,
-           std::vector<lora_attn_work_t>& merge, int64_t& part_rows) {
+// Cuts the row tiles of one kernel that take much longer than the chip's share
+// of the whole into splits of about that, so that all heads' splits together
+// fill the chip's slots, and appends items and merges.
+void split(const std::vector<Tile>& tiles, int64_t slots, const lora_attn_shape_t& s,
+           std::vector<lora_attn_work_t>& work, std::vector<lora_attn_work_t>& merge, int64_t& part_rows) {
     int64_t total = 0;
     for (const Tile& t : tiles) total += t.tiles;
-    const int64_t most = std::max(kMinTiles, (total * n_kv_heads + slots - 1) / slots);
+    const int64_t share = std::max(kMinTiles, (total * s.n_kv_heads + slots - 1) / slots);
     for (const Tile& t : tiles) {
-        const int32_t n = (int32_t)std::max<int64_t>(1, (t.tiles + most - 1) / most);
-        const int32_t first = (int32_t)part_rows;
-        for (int32_t s = 0; s < n; ++s) {
-            const int32_t it0 = (int32_t)((int64_t)t.tiles * s / n), it1 = (int32_t)((int64_t)t.tiles * (s + 1) / n);
-            work.push_back({t.seq, t.row0, t.nrows, it0, it1, s, n, n > 1 ? (int32_t)part_rows : -1});
-            if (n > 1) part_rows += t.nrows;
+        const int32_t n = (int32_t)std::max<int64_t>(1, (t.tiles + share / 2) / share);
+        lora_attn_work_t w = t.work;
+        w.nsplits = n;
+        const int64_t first = part_rows;
+        for (int32_t i = 0; i < n; ++i) {
+            w.it0 = (int32_t)((int64_t)t.tiles * i / n);
+            w.it1 = (int32_t)((int64_t)t.tiles * (i + 1) / n);
+            w.part = n > 1 ? (int32_t)part_rows : -1;
+            work.push_back(w);
+            if (n > 1) part_rows += w.nrows;
         }
-        if (n > 1) merge.push_back({t.seq, t.row0, t.nrows, 0, 0, 0, n, first});
+        if (n == 1) continue;
+        const int32_t step = AT_MERGE_ROWS(s.head_dim);
+        w.part = (int32_t)first;
+        for (int32_t r = 0; r < w.nrows; r += step) {
+            w.it0 = r;
+            w.it1 = std::min(r + step, w.nrows);
+            merge.push_back(w);
+        }
     }
     // longest first, so that the last workgroups to start are short
     std::stable_sort(work.begin(), work.end(), [](const lora_attn_work_t& a, const lora_attn_work_t& b) {
@@ -81,22 +99,30 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
     }
 
     std::vector<Tile> tiles[LORA_ATTN_KINDS];
+    int32_t q0 = 0;
     for (int32_t b = 0; b < n_seq; ++b) {
         const int32_t rows = q_len[b] * group, p0 = kv_len[b] - q_len[b];
         for (int32_t r = 0, n = 0; r < rows; r += n) {
             const int32_t left = rows - r;
-            const int kind = left <= AT_NARROW_ROWS ? LORA_ATTN_NARROW
-                           : left <= AT_WIDE_ROWS   ? LORA_ATTN_WIDE
-                                                    : LORA_ATTN_PAIR;
-            n = std::min(left, (int32_t)AT_PAIR_ROWS);
-            const AtSpan sp = at_span(p0 + r / group, p0 + (r + n - 1) / group, s.window, s.sinks);
-            tiles[kind].push_back({b, r, n, at_span_tiles(sp)});
+            const auto tiles_of = [&](int32_t m) {
+                return at_span_tiles(at_span(p0 + r / group, p0 + (r + m - 1) / group, s.window, s.sinks));
+            };
+            // the last rows of a chunk stay with the others: a launch of their
+            // own would follow the wide one and take longer than they do in it
+            int kind = rows <= AT_NARROW_ROWS ? LORA_ATTN_NARROW : LORA_ATTN_WIDE;
+            n = std::min(left, (int32_t)AT_WIDE_ROWS);
+            if (left > AT_WIDE_ROWS && tiles_of(n) >= kPairTiles) {
+                kind = LORA_ATTN_PAIR;
+                n = std::min(left, (int32_t)AT_PAIR_ROWS);
+            }
+            tiles[kind].push_back({{b, r, n, 0, 0, 1, -1, q0, q_len[b], kv_len[b], {0, 0}}, tiles_of(n)});
         }
+        q0 += q_len[b];
     }
     std::vector<lora_attn_work_t> work[LORA_ATTN_KINDS], merge;
     int64_t part_rows = 0;
     for (int kind = 0; kind < LORA_ATTN_KINDS; ++kind)
-        split(tiles[kind], kSlots[kind], s.n_kv_heads, work[kind], merge, part_rows);
+        split(tiles[kind], kSlots[kind], s, work[kind], merge, part_rows);
 
     if (part_rows > INT32_MAX) return LORA_EINVAL;
     constexpr int64_t wi = sizeof(lora_attn_work_t) / sizeof(int32_t);
@@ -122,8 +148,6 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
         out.off_work[kind] = place(wi * out.n_work[kind]);
     }
     out.off_merge = place(wi * out.n_merge);
-    out.off_q_start = place(n_seq + 1);
-    out.off_kv_len = place(n_seq);
     out.off_kv_start = place(n_seq + 1);
     out.off_row_pos = place(n_rows);
     out.off_row_slot = place(n_rows);
@@ -138,12 +162,10 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
     };
     for (int kind = 0; kind < LORA_ATTN_KINDS; ++kind) put(out.off_work[kind], work[kind]);
     put(out.off_merge, merge);
-    int32_t *q_start = staging + out.off_q_start, *kv_start = staging + out.off_kv_start;
+    int32_t* kv_start = staging + out.off_kv_start;
     int32_t row = 0, token = 0;
     for (int32_t b = 0; b < n_seq; ++b) {
-        q_start[b] = row;
         kv_start[b] = token;
-        staging[out.off_kv_len + b] = kv_len[b];
         const int32_t* src = table + (pages ? b * ld_table : 0);
         for (int32_t i = 0; i < q_len[b]; ++i, ++row) {
             const int32_t p = kv_len[b] - q_len[b] + i;
@@ -157,7 +179,6 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
         if (need) memcpy(dst, src, sizeof(int32_t) * (size_t)need);
         std::fill(dst + need, dst + pages, 0);
     }
-    q_start[n_seq] = row;
     kv_start[n_seq] = token;
     return LORA_OK;
 }

@@ -15,6 +15,8 @@
 #define AT_NARROW_ROWS 16
 #define AT_WIDE_ROWS 128
 #define AT_PAIR_ROWS 256
+// rows of one merge entry: 256 threads, four elements each
+#define AT_MERGE_ROWS(head_dim) (1024 / (head_dim))
 
 // Tiles that queries at positions p_lo .. p_hi may see, as a list: the first
 // `sinks` tiles 0 .. sinks-1, then `first` .. `end`-1.

@@ -705,17 +705,21 @@ typedef struct lora_attn_shape {
  * sequence `seq`, where row r is query head r % group of the kv head's group
  * at new token r / group, over the tiles [it0, it1) of 64 tokens in the list
  * of tiles that these rows may see.  With nsplits > 1 the partial result goes
- * to rows part.. of the workspace; a merge entry (it0 = it1 = 0, part = the
- * first split's) joins the splits of one row tile. */
+ * to rows part.. of the workspace; merge entries join the splits of a row tile,
+ * a few of its rows each: there nrows is the tile's, it0 .. it1 are the entry's
+ * rows in it and part is the first split's. */
 typedef struct lora_attn_work {
     int32_t seq;
     int32_t row0;
     int32_t nrows;
     int32_t it0;
     int32_t it1;
-    int32_t split;
     int32_t nsplits;
     int32_t part;
+    int32_t q0;                 /* the sequence's first row, new tokens and  */
+    int32_t n_new;              /* cached tokens                             */
+    int32_t kv;
+    int32_t reserved[2];
 } lora_attn_work_t;
 
 #define LORA_ATTN_NARROW 0  /* kernels: up to 16 rows, four waves share the tokens */
@@ -738,8 +742,6 @@ typedef struct lora_attn_info {
     int64_t workspace_floats;   /* fp32 elements lora_attn needs             */
     int64_t off_work[LORA_ATTN_KINDS];  /* lora_attn_work_t [n_work[kind]]   */
     int64_t off_merge;          /* lora_attn_work_t [n_merge]                */
-    int64_t off_q_start;        /* [n_seq + 1] first row of each sequence    */
-    int64_t off_kv_len;         /* [n_seq]                                   */
     int64_t off_kv_start;       /* [n_seq + 1] first output row of the read  */
     int64_t off_row_pos;        /* [n_rows] token each row is                */
     int64_t off_row_slot;       /* [n_rows] page * page_tokens + place, or -1 */

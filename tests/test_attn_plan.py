@@ -46,39 +46,41 @@ def check_plan(s, q_len, kv_len, tab, staging, info):
     group = s.n_heads // s.n_kv_heads
 
     def items(off, n):
-        return staging[off:off + 8 * n].reshape(-1, 8)
+        return staging[off:off + hl.ATTN_WORK_INTS * n].reshape(-1, hl.ATTN_WORK_INTS)
+    starts = np.concatenate([[0], np.cumsum(q_len)])
     tiles, parts = {}, []
     for kind, most in MOST.items():
-        for seq, row0, nrows, it0, it1, split, nsplits, part in items(info.off_work[kind], info.n_work[kind]):
-            assert 1 <= nrows <= most and 0 <= split < nsplits
-            tiles.setdefault((seq, row0, nrows), []).append((split, it0, it1, nsplits, part))
+        for seq, row0, nrows, it0, it1, nsplits, part, q0, n_new, kv, *_ in items(info.off_work[kind], info.n_work[kind]):
+            assert 1 <= nrows <= most and nsplits >= 1
+            assert (q0, n_new, kv) == (starts[seq], q_len[seq], kv_len[seq])
+            tiles.setdefault((seq, row0, nrows), []).append((it0, it1, nsplits, part))
             if nsplits > 1:
                 parts.append((part, part + nrows))
     for a, b in zip(sorted(parts), sorted(parts)[1:]):
         assert a[1] <= b[0]
     assert all(0 <= a and b <= info.part_rows for a, b in parts)
     assert info.workspace_floats == info.part_rows * s.n_kv_heads * (s.head_dim + 2)
-    merges = {tuple(m[:3]): m for m in items(info.off_merge, info.n_merge)}
+    merges = {}
+    for m in items(info.off_merge, info.n_merge):
+        merges.setdefault(tuple(m[:3]), []).append(m)
     rows = {}
     for (seq, row0, nrows), got in tiles.items():
         rows.setdefault(seq, []).extend(range(row0, row0 + nrows))
         got.sort()
-        n = got[0][3]
-        assert [g[0] for g in got] == list(range(n)) and all(g[3] == n for g in got)
-        assert got[0][1] == 0 and all(a[2] == b[1] for a, b in zip(got, got[1:]))
+        n = got[0][2]
+        assert len(got) == n and all(g[2] == n for g in got)
+        assert got[0][0] == 0 and all(a[1] == b[0] for a, b in zip(got, got[1:]))
         p0 = int(kv_len[seq]) - int(q_len[seq])
         want = span(p0 + row0 // group, p0 + (row0 + nrows - 1) // group, s.window, s.sinks)
-        assert got[-1][2] >= len(want)  # the list of tiles holds every visible one
+        assert got[-1][1] >= len(want)  # the list of tiles holds every visible one
         if n > 1:
-            m = merges.pop((seq, row0, nrows))
-            assert [g[4] for g in got] == [got[0][4] + i * nrows for i in range(n)]
-            assert m[6] == n and m[7] == got[0][4]
+            assert [g[3] for g in got] == [got[0][3] + i * nrows for i in range(n)]
+            ms = merges.pop((seq, row0, nrows))
+            assert all(m[5] == n and m[6] == got[0][3] for m in ms)
+            assert sorted(r for m in ms for r in range(m[3], m[4])) == list(range(nrows))
     assert not merges
     for b, n in enumerate(q_len):
         assert sorted(rows.get(b, [])) == list(range(int(n) * group))
-    starts = np.concatenate([[0], np.cumsum(q_len)])
-    assert np.array_equal(staging[info.off_q_start:info.off_q_start + len(q_len) + 1], starts)
-    assert np.array_equal(staging[info.off_kv_len:info.off_kv_len + len(q_len)], kv_len)
     assert np.array_equal(staging[info.off_kv_start:info.off_kv_start + len(q_len) + 1],
                           np.concatenate([[0], np.cumsum(kv_len)]))
     row = 0
@@ -116,7 +118,7 @@ def test_plan_splits_long_contexts_and_counts_a_window():
     _, full = hl.lora_attn_plan(shape(page=64, pages=2000), [1], [100000], tab)
     assert full.n_merge == 1 and full.n_work[hl.LORA_ATTN_NARROW] >= 64
     staging, few = hl.lora_attn_plan(shape(page=64, pages=2000, window=1000, sinks=4), [1], [100000], tab)
-    it = staging[few.off_work[0]:few.off_work[0] + 8 * few.n_work[0]].reshape(-1, 8)
+    it = staging[few.off_work[0]:few.off_work[0] + hl.ATTN_WORK_INTS * few.n_work[0]].reshape(-1, hl.ATTN_WORK_INTS)
     assert (it[:, 4] - it[:, 3]).sum() <= 1000 // TILE + 3  # the window's tiles and one of sinks
 
 
