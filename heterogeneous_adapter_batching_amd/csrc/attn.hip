@@ -226,36 +226,56 @@ struct ReadArgs {
     int32_t n_seq, n_tokens, ld_table;
 };
 
-// D/8 lanes take one (token, head): 8 elements of k and 8 of v each.
+// D/8 lanes take one token and several heads: 8 elements of k and 8 of v of each.
+// A workgroup finds the sequence of its first token by bisection, a lane goes on
+// from there, and every head's loads are under way before the first is stored.
+constexpr int kReadHeads = 4;
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
-    constexpr int LPV = D / 8, VPB = 256 / LPV;
-    const int c = 8 * (threadIdx.x % LPV), hk = a.kv.n_kv_heads;
-    const int64_t n_vec = (int64_t)a.n_tokens * hk;
-    for (int64_t vec = (int64_t)blockIdx.x * VPB + threadIdx.x / LPV; vec < n_vec; vec += (int64_t)gridDim.x * VPB) {
-        const int token = (int)(vec / hk), head = (int)(vec % hk);
-        int lo = 0, hi = a.n_seq;  // the sequence: kv_start[lo] <= token < kv_start[lo + 1]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.kv_start[mid] <= token) lo = mid;
-            else hi = mid;
-        }
-        const int t = token - a.kv_start[lo];
-        const int32_t page = clamp_page(a.kv, a.table[(int64_t)lo * a.ld_table + (t >> a.kv.page_shift)]);
-        const int32_t place = t & ((1 << a.kv.page_shift) - 1);
-        const int64_t off = kv_off(a.kv, page, head, place) + c, out = (int64_t)token * a.ld + (int64_t)head * D + c;
-        u32x4_t k, v;
+    constexpr int LPV = D / 8, VPB = 256 / LPV, HEADS = kReadHeads;
+    typedef typename std::conditional<E4M3, u32x2_t, u32x4_t>::type raw_t;
+    const int hk = a.kv.n_kv_heads, groups = (hk + HEADS - 1) / HEADS;
+    const int first = (int)(blockIdx.x / groups) * VPB, head0 = (int)(blockIdx.x % groups) * HEADS;
+    const int token = first + (int)threadIdx.x / LPV, c = 8 * (threadIdx.x % LPV);
+    if (token >= a.n_tokens) return;
+    int seq = 0, hi = a.n_seq;  // kv_start[seq] <= first < kv_start[seq + 1]
+    while (hi - seq > 1) {
+        const int mid = (seq + hi) >> 1;
+        if (a.kv_start[mid] <= first) seq = mid;
+        else hi = mid;
+    }
+    while (seq + 1 < a.n_seq && a.kv_start[seq + 1] <= token) ++seq;
+    const int t = token - a.kv_start[seq];
+    const int32_t page = clamp_page(a.kv, a.table[(int64_t)seq * a.ld_table + (t >> a.kv.page_shift)]);
+    const int32_t place = t & ((1 << a.kv.page_shift) - 1);
+    raw_t k[HEADS], v[HEADS];
+    uint32_t ks[HEADS], vs[HEADS];
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h) {
+        const int head = min(head0 + h, hk - 1);
+        const int64_t off = (kv_off(a.kv, page, head, place) + c) * (E4M3 ? 1 : 2);
         if constexpr (E4M3) {
             const int64_t so = scale_off(a.kv, page, head, place);
-            const float ks = scale_of(a.kv.k_scale[so]), vs = scale_of(a.kv.v_scale[so]);
-            k = dequant8(*reinterpret_cast<const u32x2_t*>(a.kv.k + off), ks);
-            v = dequant8(*reinterpret_cast<const u32x2_t*>(a.kv.v + off), vs);
-        } else {
-            k = *reinterpret_cast<const u32x4_t*>(a.kv.k + 2 * off);
-            v = *reinterpret_cast<const u32x4_t*>(a.kv.v + 2 * off);
+            ks[h] = a.kv.k_scale[so];
+            vs[h] = a.kv.v_scale[so];
         }
-        *reinterpret_cast<u32x4_t*>(a.k_out + out) = k;
-        *reinterpret_cast<u32x4_t*>(a.v_out + out) = v;
+        k[h] = *reinterpret_cast<const raw_t*>(a.kv.k + off);
+        v[h] = *reinterpret_cast<const raw_t*>(a.kv.v + off);
+    }
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h) {
+        if (head0 + h >= hk) return;
+        const int64_t out = (int64_t)token * a.ld + (int64_t)(head0 + h) * D + c;
+        u32x4_t x, y;
+        if constexpr (E4M3) {
+            x = dequant8(k[h], scale_of(ks[h]));
+            y = dequant8(v[h], scale_of(vs[h]));
+        } else {
+            x = k[h];
+            y = v[h];
+        }
+        __builtin_nontemporal_store(x, reinterpret_cast<u32x4_t*>(a.k_out + out));
+        __builtin_nontemporal_store(y, reinterpret_cast<u32x4_t*>(a.v_out + out));
     }
 }
 
@@ -933,12 +953,81 @@ struct EveryFourth {
     }
 };
 
+// The narrow kernel's V tiles: v_chunk's order, and bit 3 of the row turns a
+// pair's chunks, so that 16 lanes that write one chunk of 16 rows hit all banks.
+template <int D>
+__device__ __forceinline__ int n_chunk(int row, int c) {
+    return v_chunk<D>(row, c) ^ ((row >> 3) & 1);
+}
+
 // One wave's tiles in the narrow kernel; true where the result is not finite.
-template <int D, bool E4M3, bool UNI, bool CAREFUL>
+//
+// Lane (col, g) = (lane % 16, lane / 16) loads parts of tokens col and 16 + col,
+// of keys and values alike, at the addresses that it works out itself: 64 bytes
+// of a token go to the 4 lanes of one load.  The keys are the first product's
+// operand as they are loaded, with EPL elements in a row for each lane; q is
+// loaded in the same order (q_part).  Only the values pass through LDS, which
+// transposes them.
+template <int D, bool E4M3>
+struct NarrowTile {
+    static constexpr int ES = E4M3 ? 1 : 2, EPL = 16 / ES, J = D / (4 * EPL), H = EPL / 8;
+    // first element of operand k of lanes g
+    static __device__ __forceinline__ int q_part(int k, int g) { return 4 * EPL * (k / H) + EPL * g + 8 * (k % H); }
+    // operand k from a token's loads
+    static __device__ __forceinline__ u32x4_t part(const u32x4_t (&raw)[J], uint32_t exp, int k) {
+        const u32x4_t x = raw[k / H];
+        if constexpr (E4M3) return dequant8(u32x2_t{x[2 * (k % H)], x[2 * (k % H) + 1]}, scale_of(exp));
+        else return x;
+    }
+    u32x4_t k[2][J], v[2][J];
+    uint32_t k_exp[2], v_exp[2];
+    int32_t page[2];
+    int64_t at[2], sc[2];  // bytes from the head's first token; scale
+
+    __device__ __forceinline__ static int token(const Item& it, int t0, int b) {
+        return min(t0 + 16 * b + (int)(threadIdx.x & 15), it.kv - 1);
+    }
+    __device__ __forceinline__ void look_up(const Kv& c, const Item& it, int t0) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) page[b] = it.table[token(it, t0, b) >> c.page_shift];
+    }
+    // of the tile that look_up() was last called for
+    __device__ __forceinline__ void place(const Kv& c, const Item& it, int t0, int head) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int32_t pg = clamp_page(c, page[b]), slot = token(it, t0, b) & ((1 << c.page_shift) - 1);
+            at[b] = ES * (pg * c.page_stride + slot * c.token_stride) + 16 * ((threadIdx.x >> 4) & 3);
+            if constexpr (E4M3) sc[b] = scale_off(c, pg, head, slot);
+        }
+    }
+    __device__ __forceinline__ static void load(u32x4_t (&to)[2][J], uint32_t (&exp)[2], const char* from,
+                                                const uint8_t* scales, const int64_t (&at)[2], const int64_t (&sc)[2]) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) to[b][j] = *reinterpret_cast<const u32x4_t*>(from + at[b] + 64 * j);
+            if constexpr (E4M3) exp[b] = scales[sc[b]];
+        }
+    }
+    __device__ __forceinline__ void load_k(const Kv& c, int head) { load(k, k_exp, c.k + ES * head * c.head_stride, c.k_scale, at, sc); }
+    __device__ __forceinline__ void load_v(const Kv& c, int head) { load(v, v_exp, c.v + ES * head * c.head_stride, c.v_scale, at, sc); }
+    __device__ __forceinline__ void store_v(char* vt) const {
+        const int col = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                *reinterpret_cast<u32x4_t*>(vt + (16 * b + col) * (2 * D) + 16 * n_chunk<D>(col, q_part(i, g) / 8)) =
+                    part(v[b], v_exp[b], i);
+    }
+};
+
+template <int D, bool E4M3, bool CAREFUL>
 __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, int pos, int p_lo, int p_hi, int head,
-                                            int w, const u32x4_t (&qf)[D / 32], char* kt, char* vt,
-                                            f32x4_t (&acc)[D / 16], float& m, f32x4_t& l) {
+                                            int w, const u32x4_t (&qf)[D / 32], char* vt, f32x4_t (&acc)[D / 16],
+                                            float& m, f32x4_t& l) {
     constexpr int RB = 2 * D, DB = D / 16, KS = D / 32, T = 32;
+    typedef NarrowTile<D, E4M3> Tile;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int n = max(0, 2 * it.it1 - 2 * it.it0 - w + 3) >> 2;
     const EveryFourth tile{it.span, 2 * it.it0 + w, 2 * it.it1 - 1};
@@ -946,39 +1035,30 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
     for (int d = 0; d < DB; ++d) acc[d] = f32x4_t{};
     m = -INFINITY;
     l = f32x4_t{};
-    Stage<D, E4M3, UNI, false, false, 1, T> ks;
-    Stage<D, E4M3, UNI, false, true, 1, T> vs;
-    ks.init(a.kv, head, 0);
-    vs.init(a.kv, head, 0);
-    Places<D, E4M3, UNI, 1, T, EveryFourth> places(a.kv, it, tile, head, 0);
-    const auto send = [&](int i) {
-        places.open(i);
-        places.read(i);
-        ks.take(places);
-        vs.take(places);
-        ks.load(kt);
-        vs.load(vt);
-    };
+    Tile x;
     if (n > 0) {
-        places.look_up(0);
-        send(0);
+        x.look_up(a.kv, it, tile(0));
+        x.place(a.kv, it, tile(0), head);
+        x.look_up(a.kv, it, tile(1));
+        x.load_k(a.kv, head);
+        x.load_v(a.kv, head);
     }
     for (int i = 0; i < n; ++i) {
         const int t0 = tile(i);
-        ks.store(kt);
-        vs.store(vt);
-        if (i + 1 < n) send(i + 1);
-        if (none_sees(a, p_lo, p_hi, t0, t0 + T - 1)) continue;
-
         f32x4_t s[2] = {f32x4_t{}, f32x4_t{}};
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int r = 16 * b + col;
-                s[b] = mfma16(*reinterpret_cast<const u32x4_t*>(kt + r * RB + 16 * k_chunk<D>(r, 4 * k + g)), qf[k],
-                              s[b]);
-            }
+            for (int b = 0; b < 2; ++b) s[b] = mfma16(Tile::part(x.k[b], x.k_exp[b], k), qf[k], s[b]);
+        x.store_v(vt);
+        if (i + 1 < n) {
+            x.place(a.kv, it, tile(i + 1), head);
+            x.look_up(a.kv, it, tile(i + 2));
+            x.load_k(a.kv, head);
+            x.load_v(a.kv, head);
+        }
+        if (none_sees(a, p_lo, p_hi, t0, t0 + T - 1)) continue;
+
         const bool masked = !all_see(a, p_lo, p_hi, t0, t0 + T - 1);
         if (masked) hide(a, pos, t0 + 4 * g, [&](auto hidden) {
 #pragma unroll
@@ -1030,7 +1110,7 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int el = 16 * d + 4 * g + e;
-                            const float v = v_elem(vt, RB, tok, v_chunk<D>(tok, el >> 3), el & 7);
+                            const float v = v_elem(vt, RB, tok, n_chunk<D>(tok, el >> 3), el & 7);
                             acc[d][e] = vis ? fmaf(p, v, acc[d][e]) : acc[d][e];
                         }
                 }
@@ -1042,8 +1122,8 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
             const int ch = 2 * d + ((col & 3) >> 1), by = 8 * (col & 1);
-            const u32x2_t lo = ds_tr16(vt + r * RB + 16 * v_chunk<D>(r, ch) + by);
-            const u32x2_t hi = ds_tr16(vt + (r + 16) * RB + 16 * v_chunk<D>(r + 16, ch) + by);
+            const u32x2_t lo = ds_tr16(vt + r * RB + 16 * n_chunk<D>(r, ch) + by);
+            const u32x2_t hi = ds_tr16(vt + (r + 16) * RB + 16 * n_chunk<D>(r, ch) + by);
             acc[d] = mfma16(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
         }
     }
@@ -1058,10 +1138,10 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
 // Up to 16 rows (the query heads of a kv head, for a few new tokens): the four
 // waves take tiles of 32 tokens in turn, each through LDS of its own, so that
 // no barrier stands between the loads, and join their results at the end.
-template <int D, bool E4M3, bool UNI>
-__global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_kernel(AttnArgs a) {
     constexpr int DB = D / 16, KS = D / 32, T = 32;
-    __shared__ __align__(16) char lds[4][2][T * 2 * D];
+    __shared__ __align__(16) char lds[4][T * 2 * D];
     __shared__ float s_m[4][16], s_l[4][16];
     const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
     const int col = lane & 15, g = lane >> 4;
@@ -1073,15 +1153,16 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
     const int p_lo = it.p0 + it.row0 / a.group, p_hi = it.p0 + (it.row0 + it.nrows - 1) / a.group;
     u32x4_t qf[KS];
     {
-        const uint16_t* q = a.q + row_off(a, it, it.row0 + row, head, a.ldq, D) + 8 * g;
+        const uint16_t* q = a.q + row_off(a, it, it.row0 + row, head, a.ldq, D);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4_t*>(q + 32 * s);
+        for (int k = 0; k < KS; ++k)
+            qf[k] = *reinterpret_cast<const u32x4_t*>(q + NarrowTile<D, E4M3>::q_part(k, g));
     }
     f32x4_t acc[DB];
     float m;
     f32x4_t sum;
-    if (narrow_pass<D, E4M3, UNI, false>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w][0], lds[w][1], acc, m, sum))
-        narrow_pass<D, E4M3, UNI, true>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w][0], lds[w][1], acc, m, sum);
+    if (narrow_pass<D, E4M3, false>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w], acc, m, sum))
+        narrow_pass<D, E4M3, true>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w], acc, m, sum);
 
     // join the waves: each leaves its maximum, sum and [row][D] accumulator in LDS
     float l = sum[0] + __shfl_xor(sum[0], 16);
@@ -1090,7 +1171,7 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
         s_m[w][col] = m;
         s_l[w][col] = l;
     }
-    float* mine = reinterpret_cast<float*>(lds[w][0]);
+    float* mine = reinterpret_cast<float*>(lds[w]);
 #pragma unroll
     for (int d = 0; d < DB; ++d) *reinterpret_cast<f32x4_t*>(mine + col * D + 16 * d + 4 * g) = acc[d];
     __syncthreads();
@@ -1108,7 +1189,7 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
         if (mx == -INFINITY) continue;
         const float f = __builtin_amdgcn_exp2f(mx - top);
         total = fmaf(f, s_l[x][r], total);
-        const float* p = reinterpret_cast<const float*>(lds[x][0]) + r * D + e0;
+        const float* p = reinterpret_cast<const float*>(lds[x]) + r * D + e0;
 #pragma unroll
         for (int e = 0; e < EPT; ++e) o[e] = fmaf(f, p[e], o[e]);
     }
@@ -1133,27 +1214,41 @@ __global__ __launch_bounds__(256, 2) void attn_narrow_kernel(AttnArgs a) {
 // Joins the splits of one row tile, in their order: D/4 lanes a row.
 template <int D>
 __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
-    constexpr int LPR = D / 4;
+    constexpr int LPR = D / 4, AHEAD = 4;
     const int head = blockIdx.x % a.kv.n_kv_heads;
     Item it;
     if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_PAIR_ROWS, true, it)) return;
     const int r = it.it0 + threadIdx.x / LPR, e0 = 4 * (threadIdx.x % LPR);
     if (r >= it.it1) return;
     const int64_t first = head * a.part_rows + it.part + r;
-    const float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D;
-    float top = -INFINITY;
-    for (int s = 0; s < it.nsplits; ++s) top = fmaxf(top, ml[2 * (first + (int64_t)s * it.nrows)]);
-    float sum = 0.f;
+    const u32x2_t* ml = reinterpret_cast<const u32x2_t*>(a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D);
+    float top = -INFINITY, sum = 0.f;
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < it.nsplits; ++s) {
-        const int64_t pr = first + (int64_t)s * it.nrows;
-        const float mx = ml[2 * pr], lx = ml[2 * pr + 1];
-        const f32x4_t p = *reinterpret_cast<const f32x4_t*>(a.part + pr * D + e0);
-        if (mx == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f(mx - top);
-        sum = fmaf(f, lx, sum);
+    for (int s = 0; s < it.nsplits; s += AHEAD) {  // AHEAD splits' loads at once
+        u32x2_t x[AHEAD];
+        f32x4_t p[AHEAD];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = fmaf(f, p[e], o[e]);
+        for (int i = 0; i < AHEAD; ++i) {
+            const int64_t pr = first + (int64_t)min(s + i, it.nsplits - 1) * it.nrows;
+            x[i] = ml[pr];
+            p[i] = *reinterpret_cast<const f32x4_t*>(a.part + pr * D + e0);
+        }
+        float up = top;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) up = fmaxf(up, __uint_as_float(x[i][0]));
+        const float old = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - up);
+        top = up;
+        sum *= old;
+        o *= old;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const float mx = __uint_as_float(x[i][0]);
+            if (s + i >= it.nsplits || mx == -INFINITY) continue;
+            const float f = __builtin_amdgcn_exp2f(mx - top);
+            sum = fmaf(f, __uint_as_float(x[i][1]), sum);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(f, p[i][e], o[e]);
+        }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<u32x2_t*>(a.out + row_off(a, it, it.row0 + r, head, a.ldo, D) + e0) =
@@ -1275,9 +1370,10 @@ extern "C" int32_t lora_kv_read(const lora_attn_launch_t* L, const lora_kv_t* kv
     typedef void (*fn_t)(ReadArgs);
     static const fn_t fn[2][2] = {{kv_read_kernel<64, false>, kv_read_kernel<64, true>},
                                   {kv_read_kernel<128, false>, kv_read_kernel<128, true>}};
-    const int64_t vpb = 256 / (d / 8), blocks = ((int64_t)I.n_tokens * hk + vpb - 1) / vpb;
-    const hipError_t e = launch(fn[d == 128][kv->dtype == LORA_KV_E4M3],
-                                dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256),
+    const int64_t vpb = 256 / (d / 8);
+    const int64_t blocks = (I.n_tokens + vpb - 1) / vpb * ((hk + kReadHeads - 1) / kReadHeads);
+    if (blocks > kMaxBlocks) return LORA_EINVAL;
+    const hipError_t e = launch(fn[d == 128][kv->dtype == LORA_KV_E4M3], dim3((unsigned)blocks), dim3(256),
                                 reinterpret_cast<hipStream_t>(hip_stream), a);
     return e == hipSuccess ? LORA_OK : LORA_EHIP;
 }
@@ -1323,10 +1419,11 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
 #define AT_FORMS(kernel, d, ...)                                                        \
     {{kernel<d, false, false, ##__VA_ARGS__>, kernel<d, false, true, ##__VA_ARGS__>},   \
      {kernel<d, true, false, ##__VA_ARGS__>, kernel<d, true, true, ##__VA_ARGS__>}}
-    static const fn_t fn[LORA_ATTN_KINDS][2][2][2] = {
-        {AT_FORMS(attn_narrow_kernel, 64), AT_FORMS(attn_narrow_kernel, 128)},
+    static const fn_t wide[2][2][2][2] = {
         {AT_FORMS(attn_wide_kernel, 64, false), AT_FORMS(attn_wide_kernel, 128, false)},
         {AT_FORMS(attn_wide_kernel, 64, true), AT_FORMS(attn_wide_kernel, 128, true)}};
+    static const fn_t narrow[2][2] = {{attn_narrow_kernel<64, false>, attn_narrow_kernel<64, true>},
+                                      {attn_narrow_kernel<128, false>, attn_narrow_kernel<128, true>}};
 #undef AT_FORMS
     // where Places can work with scalar page offsets: a step's rows in one page, 32-bit strides and scale offsets
     const bool uni = kv->page_tokens >= 64 / (d / 8) && kv->token_stride <= INT32_MAX / 64 &&
@@ -1335,7 +1432,9 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
         if (I.n_work[kind] == 0) continue;
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_work[kind]);
         const dim3 grid((unsigned)(I.n_work[kind] * hk)), block(kind == LORA_ATTN_PAIR ? 512 : 256);
-        if (launch(fn[kind][d == 128][e4m3][uni], grid, block, s, a) != hipSuccess) return LORA_EHIP;
+        const fn_t fn = kind == LORA_ATTN_NARROW ? narrow[d == 128][e4m3]
+                                                 : wide[kind == LORA_ATTN_PAIR][d == 128][e4m3][uni];
+        if (launch(fn, grid, block, s, a) != hipSuccess) return LORA_EHIP;
     }
     if (I.n_merge > 0) {
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_merge);

@@ -12,11 +12,26 @@
 
 namespace {
 
-// Workgroups of each kernel that the chip works on at once: 256 compute units.
-constexpr int64_t kSlots[LORA_ATTN_KINDS] = {512, 512, 256};
-// Fewest tiles of one split: below four (256 tokens) a split's partial result
-// costs more than the tiles it takes off the longest workgroup.
-constexpr int64_t kMinTiles = 4;
+constexpr int64_t kUnits = 256;  // compute units
+// Workgroups of each kernel that a compute unit holds, by registers.
+int64_t resident(int kind, const lora_attn_shape_t& s) {
+    if (kind != LORA_ATTN_NARROW) return kind == LORA_ATTN_WIDE ? 2 : 1;
+    return s.head_dim == 64 ? 4 : s.kv_dtype == LORA_KV_E4M3 ? 3 : 2;
+}
+// Tiles of one split, for `tiles` tiles of all heads together: what fills the
+// chip's places once where that is kFullTiles at least, else up to kFullTiles
+// with one workgroup to a compute unit, and never under kMinTiles.  A split's
+// partial result and its part of the merge cost as much as a few tiles do: one
+// token over each of 8 windows of 4096 (8 kv heads) took 34.9 us in splits of 8
+// tiles and 32.4 in splits of 16; over a single context of 776, where most
+// compute units are idle, 14.7 us whole, 12.0 in splits of 8 and 10.6 in 4.
+// One token over each of 32 e4m3 contexts of up to 32768 took 126 us on three
+// places to a unit, 143 on two, 134 on four.
+constexpr int64_t kMinTiles = 4, kFullTiles = 16;
+int64_t tiles_per_split(int64_t tiles, int64_t places) {
+    const int64_t once = (tiles + places - 1) / places, spread = (tiles + kUnits - 1) / kUnits;
+    return once >= kFullTiles ? once : std::max(kMinTiles, std::min(kFullTiles, spread));
+}
 // Fewest tiles of a pair item.  It has one workgroup to a compute unit, whose
 // start nothing else covers, and 256 rows end later than 128 on a causal mask:
 // 16 prompts of up to 2048 tokens (32 heads) took 154 us on pair items and 124
@@ -38,14 +53,12 @@ int32_t check_shape(const lora_attn_shape_t& s) {
     return LORA_OK;
 }
 
-// Cuts the row tiles of one kernel that take much longer than the chip's share
-// of the whole into splits of about that, so that all heads' splits together
-// fill the chip's slots, and appends items and merges.
-void split(const std::vector<Tile>& tiles, int64_t slots, const lora_attn_shape_t& s,
+// Cuts the row tiles of one kernel into splits and appends items and merges.
+void split(const std::vector<Tile>& tiles, int64_t places, const lora_attn_shape_t& s,
            std::vector<lora_attn_work_t>& work, std::vector<lora_attn_work_t>& merge, int64_t& part_rows) {
     int64_t total = 0;
     for (const Tile& t : tiles) total += t.tiles;
-    const int64_t share = std::max(kMinTiles, (total * s.n_kv_heads + slots - 1) / slots);
+    const int64_t share = tiles_per_split(total * s.n_kv_heads, places);
     for (const Tile& t : tiles) {
         const int32_t n = (int32_t)std::max<int64_t>(1, (t.tiles + share / 2) / share);
         lora_attn_work_t w = t.work;
@@ -122,7 +135,7 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
     std::vector<lora_attn_work_t> work[LORA_ATTN_KINDS], merge;
     int64_t part_rows = 0;
     for (int kind = 0; kind < LORA_ATTN_KINDS; ++kind)
-        split(tiles[kind], kSlots[kind], s, work[kind], merge, part_rows);
+        split(tiles[kind], kUnits * resident(kind, s), s, work[kind], merge, part_rows);
 
     if (part_rows > INT32_MAX) return LORA_EINVAL;
     constexpr int64_t wi = sizeof(lora_attn_work_t) / sizeof(int32_t);
