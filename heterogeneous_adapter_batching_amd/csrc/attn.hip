@@ -289,12 +289,16 @@ struct AttnArgs {
     float* part;  // [n_kv_heads][part_rows][D] partial sums, then [n_kv_heads][part_rows][2] of (maximum, sum)
     int64_t ldq, ldo, part_rows;
     int32_t n_seq, n_rows, max_kv, ld_table, group, window, sinks;
+    uint32_t inv_group;  // 2^31 / group, rounded up
     float sl2;  // scale * log2 e
 };
 
+// i / group for i < group + 256 (group up to AT_MAX_GROUP): the rounded-up
+// reciprocal is less than 2^-31 too large, and i * group stays below 2^31.
+__device__ __forceinline__ int token_of(const AttnArgs& a, int i) { return (int)__umulhi(2 * (uint32_t)i, a.inv_group); }
 // What every lane of an item needs to know.
 struct Item : lora_attn_work_t {
-    int32_t p0;  // position of the first new token
+    int32_t p0;  // position of the first row's token
     const int32_t* table;
     AtSpan span;
 };
@@ -305,21 +309,24 @@ __device__ __forceinline__ bool load_item(const AttnArgs& a, int i, int max_rows
     if (it.seq < 0 || it.seq >= a.n_seq || it.n_new < 0 || it.kv < 0 || it.q0 < 0 || it.q0 + it.n_new > a.n_rows ||
         it.kv > a.max_kv)
         return false;
-    if (it.nrows < 1 || it.nrows > max_rows || it.row0 < 0 ||
-        (int64_t)it.row0 + it.nrows > (int64_t)it.n_new * a.group)
+    if (it.nrows < 1 || it.nrows > max_rows || it.tok0 < 0 || it.lead < 0 || it.lead >= a.group ||
+        it.tok0 + (int64_t)token_of(a, it.lead + it.nrows - 1) >= it.n_new)
         return false;
     if (it.nsplits > 1 && (it.part < 0 || it.part + (int64_t)it.nrows * (merge ? it.nsplits : 1) > a.part_rows))
         return false;
-    it.p0 = it.kv - it.n_new;
+    it.p0 = it.kv - it.n_new + it.tok0;
     it.table = a.table + (int64_t)it.seq * a.ld_table;
-    it.span = at_span(it.p0 + it.row0 / a.group, it.p0 + (it.row0 + it.nrows - 1) / a.group, a.window, a.sinks);
+    it.span = at_span(it.p0, it.p0 + token_of(a, it.lead + it.nrows - 1), a.window, a.sinks);
     it.it0 = max(it.it0, 0);
     it.it1 = min(it.it1, merge ? it.nrows : at_span_tiles(it.span));
     return true;
 }
-// Element offset of row r of the item's sequence (head r % group of kv head h, new token r / group).
+// Position of the item's row r, and the element offset of its query or result
+// (query head lead + r of the group, tokens on end, of kv head h).
+__device__ __forceinline__ int row_pos(const AttnArgs& a, const Item& it, int r) { return it.p0 + token_of(a, it.lead + r); }
 __device__ __forceinline__ int64_t row_off(const AttnArgs& a, const Item& it, int r, int h, int64_t ld, int D) {
-    return (int64_t)(it.q0 + r / a.group) * ld + (int64_t)(h * a.group + r % a.group) * D;
+    const int t = token_of(a, it.lead + r);
+    return (int64_t)(it.q0 + it.tok0 + t) * ld + (int64_t)(h * a.group + it.lead + r - t * a.group) * D;
 }
 __device__ __forceinline__ bool sees(const AttnArgs& a, int pos, int token) {
     return token <= pos && (a.window == 0 || token > pos - a.window || token < a.sinks);
@@ -701,14 +708,24 @@ struct Wide {
         if (!mine) return;
         if (it.nsplits == 1) {
             const float inv = total == 0.f ? 0.f : 1.f / total;
-            uint16_t* o = a.out + row_off(a, it, it.row0 + row, head, a.ldo, D) + 4 * h;
+            // a lane's 4 elements and those of the other half's lane make 16 bytes
+            uint16_t* o = a.out + row_off(a, it, row, head, a.ldo, D) + 8 * h;
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    *reinterpret_cast<u32x2_t*>(o + 32 * d + 8 * b) =
-                        u32x2_t{pack_bf16(acc[d][4 * b] * inv, acc[d][4 * b + 1] * inv),
-                                pack_bf16(acc[d][4 * b + 2] * inv, acc[d][4 * b + 3] * inv)};
+                for (int b = 0; b < 4; b += 2) {
+                    u32x4_t out;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const f32x16_t& x = acc[d];
+                        const auto both = __builtin_amdgcn_permlane32_swap(
+                            pack_bf16(x[4 * b + 2 * e] * inv, x[4 * b + 2 * e + 1] * inv),
+                            pack_bf16(x[4 * b + 2 * e + 4] * inv, x[4 * b + 2 * e + 5] * inv), false, false);
+                        out[e] = both[0];
+                        out[2 + e] = both[1];
+                    }
+                    *reinterpret_cast<u32x4_t*>(o + 32 * d + 8 * b) = out;
+                }
         } else {
             const int64_t pr = head * a.part_rows + it.part + row;
             float* o = a.part + pr * D + 4 * h;
@@ -793,17 +810,13 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
     Wide<D> x;
     x.row = min(32 * w + col, it.nrows - 1);  // lanes past the item's rows repeat its last one
     x.active = 32 * w < it.nrows;
-    x.pos = it.p0 + (it.row0 + x.row) / a.group;
-    x.p_lo = it.p0 + (it.row0 + min(32 * w, it.nrows - 1)) / a.group;
-    x.p_hi = it.p0 + (it.row0 + min(32 * w + 31, it.nrows - 1)) / a.group;
+    x.pos = row_pos(a, it, x.row);
+    x.p_lo = row_pos(a, it, min(32 * w, it.nrows - 1));
+    x.p_hi = row_pos(a, it, min(32 * w + 31, it.nrows - 1));
     {
-        const uint16_t* q = a.q + row_off(a, it, it.row0 + x.row, head, a.ldq, D) + 8 * h;
+        const uint16_t* q = a.q + row_off(a, it, x.row, head, a.ldq, D) + 8 * h;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) x.qf[s] = *reinterpret_cast<const u32x4_t*>(q + 16 * s);
-        // they arrive here: a wait for them inside the loop over tiles would
-        // be one for the copies that are under way there
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(x.qf[s]));
     }
     const int n = it.it1 - it.it0;
     if (n <= 0) {  // the rows see nothing
@@ -823,6 +836,10 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
     const auto nothing = [](int) {};
     x.clear();
     places.look_up(0);
+    // the queries arrive here: a wait for them inside the loop over tiles would
+    // be one for the copies that are under way there
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(x.qf[s]));
     if constexpr (!PAIR) {
         // Tile i's keys and values arrive together, behind the work on tile i - 1.
         const auto send = [&](int i) {
@@ -1149,11 +1166,10 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
     if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_NARROW_ROWS, false, it)) return;
 
     const int row = min(col, it.nrows - 1);
-    const int pos = it.p0 + (it.row0 + row) / a.group;
-    const int p_lo = it.p0 + it.row0 / a.group, p_hi = it.p0 + (it.row0 + it.nrows - 1) / a.group;
+    const int pos = row_pos(a, it, row), p_lo = it.p0, p_hi = row_pos(a, it, it.nrows - 1);
     u32x4_t qf[KS];
     {
-        const uint16_t* q = a.q + row_off(a, it, it.row0 + row, head, a.ldq, D);
+        const uint16_t* q = a.q + row_off(a, it, row, head, a.ldq, D);
 #pragma unroll
         for (int k = 0; k < KS; ++k)
             qf[k] = *reinterpret_cast<const u32x4_t*>(q + NarrowTile<D, E4M3>::q_part(k, g));
@@ -1195,7 +1211,7 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
     }
     if (it.nsplits == 1) {
         const float inv = total == 0.f ? 0.f : 1.f / total;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row_off(a, it, it.row0 + r, head, a.ldo, D) + e0);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row_off(a, it, r, head, a.ldo, D) + e0);
 #pragma unroll
         for (int e = 0; e < EPT; e += 2) dst[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
     } else {
@@ -1251,7 +1267,7 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<u32x2_t*>(a.out + row_off(a, it, it.row0 + r, head, a.ldo, D) + e0) =
+    *reinterpret_cast<u32x2_t*>(a.out + row_off(a, it, r, head, a.ldo, D) + e0) =
         u32x2_t{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 
@@ -1410,6 +1426,8 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     a.max_kv = I.max_kv;
     a.ld_table = I.ld_table;
     a.group = I.shape.n_heads / hk;
+    if (a.group > AT_MAX_GROUP) return LORA_ESHAPE;
+    a.inv_group = (uint32_t)((((int64_t)1 << 31) + a.group - 1) / a.group);
     a.window = I.shape.window;
     a.sinks = I.shape.sinks;
     a.sl2 = scale * kLog2e;

@@ -46,7 +46,8 @@ struct Tile {  // one row tile of one sequence before it is split
 int32_t check_shape(const lora_attn_shape_t& s) {
     if (s.n_heads < 1 || s.n_kv_heads < 1 || s.n_pages < 1 || s.window < 0 || s.sinks < 0) return LORA_EINVAL;
     if (s.kv_dtype != LORA_KV_BF16 && s.kv_dtype != LORA_KV_E4M3) return LORA_EINVAL;
-    if ((s.head_dim != 64 && s.head_dim != 128) || s.n_heads % s.n_kv_heads != 0 || s.n_kv_heads > 65535)
+    if ((s.head_dim != 64 && s.head_dim != 128) || s.n_heads % s.n_kv_heads != 0 || s.n_kv_heads > 65535 ||
+        s.n_heads / s.n_kv_heads > AT_MAX_GROUP)
         return LORA_ESHAPE;
     if (s.page_tokens < 1 || s.page_tokens > 1024 || (s.page_tokens & (s.page_tokens - 1)) != 0) return LORA_ESHAPE;
     if ((int64_t)s.n_pages * s.page_tokens > INT32_MAX) return LORA_EINVAL;
@@ -128,7 +129,7 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
                 kind = LORA_ATTN_PAIR;
                 n = std::min(left, (int32_t)AT_PAIR_ROWS);
             }
-            tiles[kind].push_back({{b, r, n, 0, 0, 1, -1, q0, q_len[b], kv_len[b], {0, 0}}, tiles_of(n)});
+            tiles[kind].push_back({{b, r, n, 0, 0, 1, -1, q0, q_len[b], kv_len[b], r / group, r % group}, tiles_of(n)});
         }
         q0 += q_len[b];
     }

@@ -15,6 +15,8 @@
 #define AT_NARROW_ROWS 16
 #define AT_WIDE_ROWS 128
 #define AT_PAIR_ROWS 256
+// most query heads of a kv head: the kernels divide numbers below this and 256 by it
+#define AT_MAX_GROUP 4096
 // rows of one merge entry: 256 threads, four elements each
 #define AT_MERGE_ROWS(head_dim) (1024 / (head_dim))
 

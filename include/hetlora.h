@@ -719,7 +719,8 @@ typedef struct lora_attn_work {
     int32_t q0;                 /* the sequence's first row, new tokens and  */
     int32_t n_new;              /* cached tokens                             */
     int32_t kv;
-    int32_t reserved[2];
+    int32_t tok0;               /* row0 / group                              */
+    int32_t lead;               /* row0 % group                              */
 } lora_attn_work_t;
 
 #define LORA_ATTN_NARROW 0  /* kernels: up to 16 rows, four waves share the tokens */

@@ -50,9 +50,10 @@ def check_plan(s, q_len, kv_len, tab, staging, info):
     starts = np.concatenate([[0], np.cumsum(q_len)])
     tiles, parts = {}, []
     for kind, most in MOST.items():
-        for seq, row0, nrows, it0, it1, nsplits, part, q0, n_new, kv, *_ in items(info.off_work[kind], info.n_work[kind]):
+        for seq, row0, nrows, it0, it1, nsplits, part, q0, n_new, kv, tok0, lead in items(info.off_work[kind], info.n_work[kind]):
             assert 1 <= nrows <= most and nsplits >= 1
             assert (q0, n_new, kv) == (starts[seq], q_len[seq], kv_len[seq])
+            assert (tok0, lead) == divmod(row0, group)
             tiles.setdefault((seq, row0, nrows), []).append((it0, it1, nsplits, part))
             if nsplits > 1:
                 parts.append((part, part + nrows))
