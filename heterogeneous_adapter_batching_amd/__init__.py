@@ -128,8 +128,9 @@ class lora_attn_shape_t(ctypes.Structure):
 
 class lora_attn_info_t(ctypes.Structure):
     _fields_ = [("shape", lora_attn_shape_t), ("n_seq", _i32), ("n_rows", _i32), ("n_tokens", _i32),
-                ("max_kv", _i32), ("ld_table", _i32), ("n_work", _i32 * LORA_ATTN_KINDS), ("n_merge", _i32), ("part_rows", _i64),
-                ("workspace_floats", _i64), ("off_work", _i64 * LORA_ATTN_KINDS), ("off_merge", _i64), ("off_kv_start", _i64), ("off_row_pos", _i64), ("off_row_slot", _i64),
+                ("max_kv", _i32), ("ld_table", _i32), ("n_work", _i32 * LORA_ATTN_KINDS), ("n_merge", _i32),
+                ("part_rows", _i64), ("workspace_floats", _i64), ("off_work", _i64 * LORA_ATTN_KINDS),
+                ("off_merge", _i64), ("off_kv_start", _i64), ("off_row_pos", _i64), ("off_row_slot", _i64),
                 ("off_table", _i64), ("n_staged", _i64)]
 
 

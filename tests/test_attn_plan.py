@@ -135,7 +135,7 @@ def test_plan_of_nothing():
     (dict(heads=7), hl.LORA_ESHAPE), (dict(heads=0), hl.LORA_EINVAL), (dict(kv_heads=0), hl.LORA_EINVAL),
     (dict(page=0), hl.LORA_ESHAPE), (dict(page=24), hl.LORA_ESHAPE), (dict(page=2048), hl.LORA_ESHAPE),
     (dict(pages=0), hl.LORA_EINVAL), (dict(pages=2 ** 31 - 1), hl.LORA_EINVAL), (dict(dtype=2), hl.LORA_EINVAL),
-    (dict(window=-1), hl.LORA_EINVAL), (dict(sinks=-1), hl.LORA_EINVAL)])
+    (dict(heads=4097, kv_heads=1), hl.LORA_ESHAPE), (dict(window=-1), hl.LORA_EINVAL), (dict(sinks=-1), hl.LORA_EINVAL)])
 def test_plan_refuses_shapes(change, code):
     st, _, _ = hl.lora_attn_plan(shape(**change), [1], [1], np.zeros((1, 1), np.int32), raw=True)
     assert st == code

@@ -146,6 +146,66 @@ def test_groups(heads, kv_heads):
     run_case([(1, 77), (3, 100), (2, 2)], heads, kv_heads, 64, 16, "bf16")
 
 
+def test_many_heads_to_a_kv_head():
+    run_case([(1, 77), (2, 100), (1, 2100)], 300, 1, 64, 16, "bf16")
+
+
+# row tiles over 32 tiles of tokens and more
+OVER = [(70, 2300), (300, 2433), (1, 40), (33, 33)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page,window,sinks", [(1, 0, 0), (16, 0, 0), (64, 2200, 5), (4, 2050, 130)])
+def test_chunks_over_long_contexts(page, window, sinks, dim, dtype):
+    batch, cache, table, q, out = run_case(OVER, 4, 1, dim, page, dtype, window, sinks)
+    assert batch.info.n_work[hl.LORA_ATTN_PAIR] > 0
+    again = torch.zeros_like(out)
+    for _ in range(2):
+        batch.attn(q, again, dim ** -0.5)
+        torch.cuda.synchronize()
+        assert torch.equal(out, again)
+
+
+def test_long_contexts_of_a_token_major_cache():
+    batch, *_ = run_case(OVER, 6, 2, 128, 32, "bf16", token_major=True)
+    assert batch.info.n_work[hl.LORA_ATTN_PAIR] > 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [1, 16])
+def test_values_that_no_row_sees_over_long_contexts(page, dtype):
+    """As the test of masked values below, for row tiles of the kernel for long contexts."""
+    rng = np.random.default_rng([page, 4])
+    n, kv, window, sinks, dim, heads = 100, 2600, 2100, 70, 128, 4
+    pages = -(-kv // page) + 2
+    cache = make_cache(rng, pages, 1, page, dim, dtype)
+    table = make_table(rng, [kv], page, pages)
+    kvs = [tokens(cache, table, 0, kv)]
+    hidden = np.arange(sinks, kv - n - window + 1)
+    assert len(hidden) > 300
+    for t in (cache.k, cache.v):
+        at = (torch.from_numpy(table[0][hidden // page].astype(np.int64)).cuda(), 0,
+              torch.from_numpy(hidden % page).cuda())
+        if dtype == "e4m3":
+            t.view(torch.uint8)[at] = 0x7F
+        else:
+            t[at] = float("nan")
+    q = torch.from_numpy(rng.standard_normal((n, heads * dim)).astype(np.float32)).bfloat16().cuda()
+    out = torch.zeros_like(q)
+    batch = AttnBatch(cache, heads, window, sinks).refresh([n], [kv], table)
+    assert batch.info.n_work[hl.LORA_ATTN_PAIR] > 0
+    batch.attn(q, out, 0.09)
+    torch.cuda.synchronize()
+    check(out, *expected(cache, table, q, [n], [kv], heads, window, sinks, 0.09, kvs))
+    last = cache.v[int(table[0, (kv - 1) // page]), :, (kv - 1) % page]  # only the last new token sees it
+    (last.view(torch.uint8) if dtype == "e4m3" else last).fill_(0x7F if dtype == "e4m3" else float("nan"))
+    batch.attn(q, out, 0.09)
+    torch.cuda.synchronize()
+    check(out[:n - 1], *(x[:n - 1] for x in expected(cache, table, q, [n], [kv], heads, window, sinks, 0.09, kvs)))
+    assert torch.isnan(out[n - 1]).all()
+
+
 def test_token_major_cache_and_strided_rows():
     run_case(CHUNKS, 4, 2, 128, 16, "bf16", token_major=True)
     rng = np.random.default_rng(9)
@@ -507,3 +567,22 @@ def test_read_gives_every_code_at_every_scale():
     want = oracle.e4m3_values()[None] * 2.0 ** (np.arange(27, 247)[:, None] - 127.0)
     for got in (ko, vo):
         assert np.array_equal(got.double().cpu().numpy().reshape(220, 256), want, equal_nan=True)
+
+
+# ---------------------------------------------------------------- all of it together
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attention_layer_example(dtype):
+    """The example's layer against its plain form.  bf16: the base projections,
+    the cache, the turned q, the weights and the attention's output are rounded
+    once each, by 2^-9 rms at most, and the errors add up over two projections in
+    a row: 8 * 2^-9.  An e4m3 value is off by half of 2^-3 of it at most, 2^-4."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_layer.py")
+    spec = importlib.util.spec_from_file_location("attention_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    out, held = mod.run(torch.float8_e4m3fn if dtype == "e4m3" else torch.bfloat16, 8)
+    cache_off = 2.0 ** -4 if dtype == "e4m3" else 2 * 2.0 ** -9
+    assert held <= cache_off + 2 * 2.0 ** -9
+    assert out <= (2 * cache_off if dtype == "e4m3" else 0) + 8 * 2.0 ** -9
