@@ -613,10 +613,9 @@ struct Wide {
         return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
     }
     // Scores of one tile (SCORES) and product of another (PRODUCT).  LDS answers
-    // after four MFMAs' time, so the operands are read AHEAD of them.  between(f)
-    // comes after MFMA f: other work, in the matrix unit's time.
-    template <bool SCORES, bool PRODUCT, typename F>
-    __device__ __forceinline__ void multiply(const char* kt, const char* vt, F between) {
+    // after four MFMAs' time, so the operands are read AHEAD of them.
+    template <bool SCORES, bool PRODUCT>
+    __device__ __forceinline__ void multiply(const char* kt, const char* vt) {
         constexpr int NS = SCORES ? D / 8 : 0, N = NS + (PRODUCT ? D / 8 : 0), AHEAD = 6;
         u32x4_t part[AHEAD];
         const auto read = [&](int f) { return f < NS ? k_part(kt, f) : v_part(vt, f - NS); };
@@ -634,7 +633,6 @@ struct Wide {
                 if (d < 2) l = add_weights(pf[2 * d], pf[2 * d + 1], l);
             }
             if (f + AHEAD < N) part[f % AHEAD] = read(f + AHEAD);
-            between(f);
             __builtin_amdgcn_sched_barrier(0x6);  // arithmetic may move
         }
     }
@@ -782,11 +780,10 @@ struct AllTiles {
 // Otherwise four waves, 128 rows, and two workgroups to a compute unit.
 //
 // Keys and values have NB tiles each in LDS.  Keys i + LEAD and values i + LEAD - 1
-// are sent for between the multiplications of tile i (EARLY) or in its softmax,
-// into the place of tiles that every wave is done with; a wave waits for its own
-// share of keys i + 1 and values i at the barrier before the first half
-// multiplies them.  Past the last tile it is sent for again, which no one reads:
-// without branches the scalar work hides between the multiplications.
+// are sent for in the softmax of tile i, into the place of tiles that every wave
+// is done with; a wave waits for its own share of keys i + 1 and values i at the
+// barrier before the first half multiplies them.  Past the last tile it is sent
+// for again, which no one reads: a wave's loads in flight are then always as many.
 //
 // A value that is infinite or NaN in a place that a row does not see would
 // still reach it through the second product (0 * NaN).  Looking for such values
@@ -796,7 +793,7 @@ struct AllTiles {
 template <int D, bool E4M3, bool UNI, bool PAIR>
 __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs a) {
     constexpr int BYTES = AT_TILE * 2 * D, NW = PAIR ? 8 : 4, NB = PAIR ? 4 : 2, LEAD = 3;
-    constexpr bool DIRECT = !E4M3, EARLY = DIRECT && PAIR && UNI;
+    constexpr bool DIRECT = !E4M3;
     typedef Stage<D, E4M3, UNI, DIRECT, false, NW, AT_TILE> KStage;
     typedef Stage<D, E4M3, UNI, DIRECT, true, NW, AT_TILE> VStage;
     constexpr int BOTH = KStage::STEPS + VStage::STEPS;  // loads of a wave for a tile's keys and values
@@ -833,7 +830,6 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
     vs.init(a.kv, head, w);
     Places<D, E4M3, UNI, NW, AT_TILE, AllTiles> places(a.kv, it, tile, head, w);
     x.find_whole(a, it);
-    const auto nothing = [](int) {};
     x.clear();
     places.look_up(0);
     // the queries arrive here: a wait for them inside the loop over tiles would
@@ -859,9 +855,9 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
             if (i + 1 < n) send(i + 1);
             const int t0 = tile(i);
             if (!x.active || none_sees(a, x.p_lo, x.p_hi, t0, t0 + AT_TILE - 1)) continue;
-            x.template multiply<true, false>(keys(i), nullptr, nothing);
+            x.template multiply<true, false>(keys(i), nullptr);
             x.weights(a, tile, i);
-            x.template multiply<false, true>(nullptr, values(i), nothing);
+            x.template multiply<false, true>(nullptr, values(i));
         }
     } else {
         // values i + LEAD - 1 lie where keys i + LEAD - 1 did
@@ -896,12 +892,10 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
             x.multiplied();
             __builtin_amdgcn_s_setprio(0);
             barrier();
-            if (!EARLY) {
-                unpack(i);
-                plan(i);
-                send_values(i);
-                send_keys(i);
-            }
+            unpack(i);
+            plan(i);
+            send_values(i);
+            send_keys(i);
             places.open(i + 1 + LEAD);
             x.weights(a, tile, i);
             x.weighed();
@@ -909,26 +903,19 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
             barrier();
             __builtin_amdgcn_s_setprio(1);  // the matrix unit goes first
         };
-        const auto arrive = [&] {  // without EARLY, this tile's have not been sent for yet
-            if (DIRECT && second) wait_loads<(LEAD - (EARLY ? 1 : 2)) * BOTH>();
+        const auto arrive = [&] {  // this half has not sent for the next tile's yet
+            if (DIRECT && second) wait_loads<(LEAD - 2) * BOTH>();
         };
-        const auto among = [&](int i) {
-            return [&, i](int f) {
-                if (EARLY && f == 1) plan(i);
-                if (EARLY && f == D / 32) send_values(i);
-                if (EARLY && f == D / 16 - 1) send_keys(i);
-            };
-        };
-        x.template multiply<true, false>(keys(0), nullptr, among(0));
+        x.template multiply<true, false>(keys(0), nullptr);
         arrive();
         int i = 0;
         for (; i < n - 1; ++i) {
             phase(i);
-            x.template multiply<true, true>(keys(i + 1), values(i), among(i + 1));
+            x.template multiply<true, true>(keys(i + 1), values(i));
             arrive();
         }
         phase(i);
-        x.template multiply<false, true>(nullptr, values(i), nothing);
+        x.template multiply<false, true>(nullptr, values(i));
         wait_loads<0>();
         if (!second) barrier();
     }
@@ -948,10 +935,10 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
             vs.store(values(0));
             wait_loads<0>();
             barrier();
-            x.template multiply<true, false>(keys(0), nullptr, nothing);
+            x.template multiply<true, false>(keys(0), nullptr);
             x.weights(a, tile, i);
             if (x.masks(i)) x.careful_product(a, values(0), tile(i));
-            else x.template multiply<false, true>(nullptr, values(0), nothing);
+            else x.template multiply<false, true>(nullptr, values(0));
             barrier();
         } while (++i < n);
     }

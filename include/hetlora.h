@@ -691,7 +691,7 @@ typedef struct lora_kv {
 
 /* What a plan is made for. */
 typedef struct lora_attn_shape {
-    int32_t n_heads;            /* a multiple of n_kv_heads                  */
+    int32_t n_heads;            /* a multiple of n_kv_heads, at most 4096 of them */
     int32_t n_kv_heads;
     int32_t head_dim;
     int32_t page_tokens;
@@ -757,8 +757,8 @@ typedef struct lora_attn_launch {
 } lora_attn_launch_t;
 
 /* Attention plan of a batch (host only): validates the batch, lists the work
- * items (row tiles, split over their tokens where there are too few of them
- * to fill the chip, so that all splits take about as long) and lays out
+ * items (row tiles, split over their tokens where they are too few or too
+ * unequal to fill the chip) and lays out
  * everything the kernels read in one buffer.
  *   q_len, kv_len  host int32 [n_seq], 0 .. 2^30
  *   block_table    host int32 [n_seq][ld_table]: page of tokens
@@ -767,8 +767,8 @@ typedef struct lora_attn_launch {
  *                  every kv_len is 0
  *   staging        host int32 [staging_capacity]
  * Errors: LORA_EINVAL (null pointer, negative or too large count, a kv_len
- * that the table does not hold), LORA_ESHAPE (head_dim, page_tokens, or
- * n_heads not a multiple of n_kv_heads), LORA_EPAGE, LORA_ECAPACITY (info is
+ * that the table does not hold), LORA_ESHAPE (head_dim, page_tokens, n_heads not
+ * a multiple of n_kv_heads or over 4096 times it), LORA_EPAGE, LORA_ECAPACITY (info is
  * written: n_staged holds the size needed), LORA_ENOMEM. */
 int32_t lora_attn_plan(const lora_attn_shape_t* shape, int32_t n_seq,
                        const int32_t* q_len, const int32_t* kv_len,
