@@ -240,48 +240,51 @@ template <int D, bool E4M3>
 __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
     constexpr int LPV = D / 8, VPB = 256 / LPV, HEADS = kReadHeads;
     typedef typename std::conditional<E4M3, u32x2_t, u32x4_t>::type raw_t;
-    const int hk = a.kv.n_kv_heads, groups = (hk + HEADS - 1) / HEADS;
-    const int first = (int)(blockIdx.x / groups) * VPB, head0 = (int)(blockIdx.x % groups) * HEADS;
-    const int token = first + (int)threadIdx.x / LPV, c = 8 * (threadIdx.x % LPV);
-    if (token >= a.n_tokens) return;
-    int seq = 0, hi = a.n_seq;  // kv_start[seq] <= first < kv_start[seq + 1]
-    while (hi - seq > 1) {
-        const int mid = (seq + hi) >> 1;
-        if (a.kv_start[mid] <= first) seq = mid;
-        else hi = mid;
-    }
-    while (seq + 1 < a.n_seq && a.kv_start[seq + 1] <= token) ++seq;
-    const int t = token - a.kv_start[seq];
-    const int32_t page = clamp_page(a.kv, a.table[(int64_t)seq * a.ld_table + (t >> a.kv.page_shift)]);
-    const int32_t place = t & ((1 << a.kv.page_shift) - 1);
-    raw_t k[HEADS], v[HEADS];
-    uint32_t ks[HEADS], vs[HEADS];
-#pragma unroll
-    for (int h = 0; h < HEADS; ++h) {
-        const int head = min(head0 + h, hk - 1);
-        const int64_t off = (kv_off(a.kv, page, head, place) + c) * (E4M3 ? 1 : 2);
-        if constexpr (E4M3) {
-            const int64_t so = scale_off(a.kv, page, head, place);
-            ks[h] = a.kv.k_scale[so];
-            vs[h] = a.kv.v_scale[so];
+    const int hk = a.kv.n_kv_heads, groups = (hk + HEADS - 1) / HEADS, c = 8 * (threadIdx.x % LPV);
+    const int64_t n_blocks = ((int64_t)a.n_tokens + VPB - 1) / VPB * groups;
+    for (int64_t block = blockIdx.x; block < n_blocks; block += gridDim.x) {
+        const int first = (int)(block / groups) * VPB, head0 = (int)(block % groups) * HEADS;
+        const int token = first + (int)threadIdx.x / LPV;
+        if (token >= a.n_tokens) continue;
+        int seq = 0, hi = a.n_seq;  // kv_start[seq] <= first < kv_start[seq + 1]
+        while (hi - seq > 1) {
+            const int mid = (seq + hi) >> 1;
+            if (a.kv_start[mid] <= first) seq = mid;
+            else hi = mid;
         }
-        k[h] = *reinterpret_cast<const raw_t*>(a.kv.k + off);
-        v[h] = *reinterpret_cast<const raw_t*>(a.kv.v + off);
-    }
+        while (seq + 1 < a.n_seq && a.kv_start[seq + 1] <= token) ++seq;
+        const int t = token - a.kv_start[seq];
+        const int32_t page = clamp_page(a.kv, a.table[(int64_t)seq * a.ld_table + (t >> a.kv.page_shift)]);
+        const int32_t place = t & ((1 << a.kv.page_shift) - 1);
+        raw_t k[HEADS], v[HEADS];
+        uint32_t ks[HEADS], vs[HEADS];
 #pragma unroll
-    for (int h = 0; h < HEADS; ++h) {
-        if (head0 + h >= hk) return;
-        const int64_t out = (int64_t)token * a.ld + (int64_t)(head0 + h) * D + c;
-        u32x4_t x, y;
-        if constexpr (E4M3) {
-            x = dequant8(k[h], scale_of(ks[h]));
-            y = dequant8(v[h], scale_of(vs[h]));
-        } else {
-            x = k[h];
-            y = v[h];
+        for (int h = 0; h < HEADS; ++h) {
+            const int head = min(head0 + h, hk - 1);
+            const int64_t off = (kv_off(a.kv, page, head, place) + c) * (E4M3 ? 1 : 2);
+            if constexpr (E4M3) {
+                const int64_t so = scale_off(a.kv, page, head, place);
+                ks[h] = a.kv.k_scale[so];
+                vs[h] = a.kv.v_scale[so];
+            }
+            k[h] = *reinterpret_cast<const raw_t*>(a.kv.k + off);
+            v[h] = *reinterpret_cast<const raw_t*>(a.kv.v + off);
         }
-        __builtin_nontemporal_store(x, reinterpret_cast<u32x4_t*>(a.k_out + out));
-        __builtin_nontemporal_store(y, reinterpret_cast<u32x4_t*>(a.v_out + out));
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            if (head0 + h >= hk) break;
+            const int64_t out = (int64_t)token * a.ld + (int64_t)(head0 + h) * D + c;
+            u32x4_t x, y;
+            if constexpr (E4M3) {
+                x = dequant8(k[h], scale_of(ks[h]));
+                y = dequant8(v[h], scale_of(vs[h]));
+            } else {
+                x = k[h];
+                y = v[h];
+            }
+            __builtin_nontemporal_store(x, reinterpret_cast<u32x4_t*>(a.k_out + out));
+            __builtin_nontemporal_store(y, reinterpret_cast<u32x4_t*>(a.v_out + out));
+        }
     }
 }
 
@@ -1398,8 +1401,8 @@ extern "C" int32_t lora_kv_read(const lora_attn_launch_t* L, const lora_kv_t* kv
                                   {kv_read_kernel<128, false>, kv_read_kernel<128, true>}};
     const int64_t vpb = 256 / (d / 8);
     const int64_t blocks = (I.n_tokens + vpb - 1) / vpb * ((hk + kReadHeads - 1) / kReadHeads);
-    if (blocks > kMaxBlocks) return LORA_EINVAL;
-    const hipError_t e = launch(fn[d == 128][kv->dtype == LORA_KV_E4M3], dim3((unsigned)blocks), dim3(256),
+    const hipError_t e = launch(fn[d == 128][kv->dtype == LORA_KV_E4M3],
+                                dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256),
                                 reinterpret_cast<hipStream_t>(hip_stream), a);
     return e == hipSuccess ? LORA_OK : LORA_EHIP;
 }
