@@ -73,6 +73,12 @@ __device__ __forceinline__ f32x4_t add_weights(uint32_t w0, uint32_t w1, f32x4_t
     return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4_t, ones), __builtin_bit_cast(s16x4_t, w), l, 0,
                                                   0, 0);
 }
+// Factor of a part of a row (a wave's or a split's) whose maximum is m, where
+// the row's is top.  A part with no maximum adds what it has: zeros where it saw
+// nothing, NaN where every score that it saw was NaN.
+__device__ __forceinline__ float part_weight(float m, float top) {
+    return m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top);
+}
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // Transposing LDS read: within each 16 lanes, lane i reads 8 bytes (4 bf16) and
@@ -1213,9 +1219,7 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
     for (int e = 0; e < EPT; ++e) o[e] = 0.f;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-        const float mx = s_m[x][r];
-        if (mx == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f(mx - top);
+        const float f = part_weight(s_m[x][r], top);
         total = fmaf(f, s_l[x][r], total);
         const float* p = reinterpret_cast<const float*>(lds[x]) + r * D + e0;
 #pragma unroll
@@ -1271,9 +1275,8 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
         o *= old;
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const float mx = __uint_as_float(x[i][0]);
-            if (s + i >= it.nsplits || mx == -INFINITY) continue;
-            const float f = __builtin_amdgcn_exp2f(mx - top);
+            if (s + i >= it.nsplits) continue;
+            const float f = part_weight(__uint_as_float(x[i][0]), top);
             sum = fmaf(f, __uint_as_float(x[i][1]), sum);
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = fmaf(f, p[i][e], o[e]);

@@ -1,0 +1,75 @@
+"""Attention on the GPU at the edges of its numbers: NaN scores, against what
+the formula gives."""
+import numpy as np
+import pytest
+import torch
+
+from heterogeneous_adapter_batching_amd.attention import AttnBatch
+from test_gpu_attn import check, expected, make_cache, make_table, tokens
+
+pytestmark = pytest.mark.gpu
+
+# (new tokens, cached tokens with them): narrow items of one and of several splits, wide ones, pair ones
+SIZES = [(1, 40), (1, 3000), (70, 90), (33, 2000), (300, 2433)]
+
+
+def case(n, kv, dtype, seed, heads=4, kv_heads=1, dim=64, page=16, **more):
+    rng = np.random.default_rng([seed, n, kv])
+    pages = -(-kv // page) + 2
+    cache = make_cache(rng, pages, kv_heads, page, dim, dtype, **more)
+    table = make_table(rng, [kv], page, pages)
+    q = torch.from_numpy(rng.standard_normal((n, heads * dim)).astype(np.float32)).bfloat16().cuda()
+    print(f"case {n} over {kv} {dtype}", flush=True)
+    return cache, table, q
+
+
+def attend(cache, table, q, kv, scale, heads=4):
+    out = torch.zeros_like(q)
+    AttnBatch(cache, heads).refresh([q.shape[0]], [kv], table).attn(q, out, scale)
+    torch.cuda.synchronize()
+    return out
+
+
+def set_tokens(t, table, which, value):
+    """Every element of tokens `which` of the one sequence becomes `value` (NaN in e4m3: its code)."""
+    page = t.shape[2]
+    at = (torch.from_numpy(table[0][which // page].astype(np.int64)).cuda(), slice(None),
+          torch.from_numpy(which % page).cuda())
+    if t.dtype == torch.float8_e4m3fn:
+        assert np.isnan(value)
+        t.view(torch.uint8)[at] = 0x7F
+    else:
+        t[at] = value
+
+
+@pytest.mark.parametrize("n,kv", SIZES)
+def test_a_query_that_is_nan_gives_nan(n, kv):
+    cache, table, q = case(n, kv, "bf16", 1)
+    kvs = [tokens(cache, table, 0, kv)]
+    q[n // 2, 64:128] = float("nan")  # one head of one row
+    out = attend(cache, table, q, kv, 0.125)
+    assert torch.isnan(out[n // 2, 64:128]).all()
+    out[n // 2, 64:128] = q[n // 2, 64:128] = 0
+    want, tol = expected(cache, table, q, [n], [kv], 4, 0, 0, 0.125, kvs)
+    want[n // 2, 1] = 0
+    check(out, want, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kv", [1, 33, 34, 65, 97, 129])
+def test_a_newest_key_that_is_nan_gives_nan(kv, dtype):
+    """One token over kv: the newest key may be all that a wave sees."""
+    cache, table, q = case(1, kv, dtype, 2)
+    set_tokens(cache.k, table, np.array([kv - 1]), float("nan"))
+    assert torch.isnan(attend(cache, table, q, kv, 0.125)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,kv", SIZES)
+@pytest.mark.parametrize("late", [False, True])
+def test_keys_that_are_nan_give_nan(n, kv, late, dtype):
+    """Half of the keys that every row sees: some parts of a split row see nothing else."""
+    cache, table, q = case(n, kv, dtype, 3)
+    seen = kv - n + 1
+    set_tokens(cache.k, table, np.arange(seen // 2, seen) if late else np.arange((seen + 1) // 2), float("nan"))
+    assert torch.isnan(attend(cache, table, q, kv, 0.125)).all()
