@@ -359,7 +359,7 @@ __device__ __forceinline__ void hide(const AttnArgs& a, int pos, int first, F ea
         return e > left;
     });
     if (a.window) {
-        const uint32_t from = (uint32_t)first - (uint32_t)a.sinks, count = (uint32_t)max(0, pos - a.window + 1 - a.sinks);
+        const uint32_t from = (uint32_t)first - (uint32_t)a.sinks, count = (uint32_t)max(0, max(0, pos - a.window + 1) - a.sinks);
         each([&](int e) {
             __builtin_amdgcn_sched_barrier(0);
             return from + (uint32_t)e < count;
@@ -1311,6 +1311,7 @@ int32_t check_kv(const lora_attn_launch_t* L, const lora_kv_t* c) {
     if (s.n_kv_heads < 1 || s.n_heads < 1 || s.n_heads % s.n_kv_heads || s.page_tokens < 1 ||
         (s.page_tokens & (s.page_tokens - 1)) || s.n_pages < 1)
         return LORA_ESHAPE;
+    if (s.window < 0 || s.window > AT_MAX_TOKENS || s.sinks < 0 || s.sinks > AT_MAX_TOKENS) return LORA_EINVAL;
     if (s.kv_dtype != LORA_KV_BF16 && s.kv_dtype != LORA_KV_E4M3) return LORA_EINVAL;
     const int64_t per = s.kv_dtype == LORA_KV_E4M3 ? 16 : 8;
     if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0 || c->page_stride % per ||

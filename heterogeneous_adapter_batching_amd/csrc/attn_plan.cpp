@@ -94,7 +94,7 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
     int64_t n_rows = 0, n_tokens = 0;
     int32_t pages = 0, max_kv = 0;
     for (int32_t b = 0; b < n_seq; ++b) {
-        if (q_len[b] < 0 || kv_len[b] < 0 || kv_len[b] > (1 << 30) || q_len[b] > (1 << 30)) return LORA_EINVAL;
+        if (q_len[b] < 0 || kv_len[b] < 0 || kv_len[b] > AT_MAX_TOKENS || q_len[b] > AT_MAX_TOKENS) return LORA_EINVAL;
         n_rows += q_len[b];
         n_tokens += kv_len[b];
         if ((int64_t)q_len[b] * group > INT32_MAX / 2) return LORA_EINVAL;
@@ -206,8 +206,11 @@ extern "C" int32_t lora_attn_plan(const lora_attn_shape_t* shape, int32_t n_seq,
         return LORA_EINVAL;
     const int32_t st = check_shape(*shape);
     if (st != LORA_OK) return st;
+    lora_attn_shape_t s = *shape;
+    s.window = std::min(s.window, AT_MAX_TOKENS);
+    s.sinks = std::min(s.sinks, AT_MAX_TOKENS);
     try {
-        return plan_impl(*shape, n_seq, q_len, kv_len, block_table, ld_table, staging, staging_capacity, info);
+        return plan_impl(s, n_seq, q_len, kv_len, block_table, ld_table, staging, staging_capacity, info);
     } catch (const std::bad_alloc&) {
         return LORA_ENOMEM;
     }

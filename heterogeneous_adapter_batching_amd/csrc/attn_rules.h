@@ -11,6 +11,10 @@
 #endif
 
 #define AT_TILE 64          // cached tokens of one tile
+// Most new and cached tokens of a sequence: positions are in [-AT_MAX_TOKENS,
+// AT_MAX_TOKENS), so a longer window hides nothing and more sinks are all there
+// are.  The plan takes the smaller, and a position minus a window fits 32 bits.
+#define AT_MAX_TOKENS (1 << 30)
 // query rows of one item of the kernels
 #define AT_NARROW_ROWS 16
 #define AT_WIDE_ROWS 128

@@ -698,7 +698,8 @@ typedef struct lora_attn_shape {
     int32_t n_pages;
     int32_t kv_dtype;
     int32_t window;             /* tokens a row sees, itself among them; 0: all */
-    int32_t sinks;              /* first tokens that stay visible with a window */
+    int32_t sinks;              /* first tokens that stay visible with a window;
+                                   a plan's info has 2^30 for more of either */
 } lora_attn_shape_t;
 
 /* One unit of attention work, for every kv head: rows [row0, row0 + nrows) of

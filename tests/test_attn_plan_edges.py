@@ -1,0 +1,32 @@
+"""CPU tests of the attention plan at the ends of its ranges."""
+import numpy as np
+import pytest
+
+import heterogeneous_adapter_batching_amd as hl
+from test_attn_plan import check_plan, make_table, shape
+
+LAST = 2 ** 31 - 1
+# new tokens and cached tokens with them, rows before the first token among them
+MIXED = ([40, 1, 3, 300, 5], [35, 70, 0, 290, 5])
+
+
+@pytest.mark.parametrize("window", [2 ** 30 - 1, 2 ** 30, 2 ** 30 + 1, LAST - 40, LAST])
+@pytest.mark.parametrize("sinks", [0, 5, 2 ** 30 + 1, LAST])
+def test_a_window_longer_than_any_sequence_is_none(window, sinks):
+    """Such a window hides nothing: the plan is that of no window."""
+    q_len, kv_len = MIXED
+    tab = make_table(np.random.default_rng(3), kv_len, 16, 1000)
+    staging, info = hl.lora_attn_plan(shape(window=window, sinks=sinks), q_len, kv_len, tab)
+    check_plan(shape(), q_len, kv_len, tab, staging, info)
+    assert np.array_equal(staging, hl.lora_attn_plan(shape(), q_len, kv_len, tab)[0])
+    # what the kernels subtract from positions of -2^30 and more
+    assert info.shape.window == min(window, 2 ** 30) and info.shape.sinks == min(sinks, 2 ** 30)
+
+
+@pytest.mark.parametrize("sinks", [64, 2 ** 30, LAST - 63, LAST])
+@pytest.mark.parametrize("window", [1, 100])
+def test_more_sinks_than_any_sequence_has_tokens(window, sinks):
+    q_len, kv_len = MIXED
+    tab = make_table(np.random.default_rng(4), kv_len, 16, 1000)
+    staging, info = hl.lora_attn_plan(shape(window=window, sinks=sinks), q_len, kv_len, tab)
+    check_plan(shape(window=window, sinks=sinks), q_len, kv_len, tab, staging, info)

@@ -1,11 +1,11 @@
-"""Attention on the GPU at the edges of its numbers: NaN scores, against what
-the formula gives."""
+"""Attention on the GPU at the edges of its numbers, against what the formula
+gives: NaN scores, windows longer than any sequence."""
 import numpy as np
 import pytest
 import torch
 
 from heterogeneous_adapter_batching_amd.attention import AttnBatch
-from test_gpu_attn import check, expected, make_cache, make_table, tokens
+from test_gpu_attn import check, expected, make_cache, make_table, run_case, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,9 @@ def test_keys_that_are_nan_give_nan(n, kv, late, dtype):
     seen = kv - n + 1
     set_tokens(cache.k, table, np.arange(seen // 2, seen) if late else np.arange((seen + 1) // 2), float("nan"))
     assert torch.isnan(attend(cache, table, q, kv, 0.125)).all()
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 5), (2 ** 30, 2 ** 31 - 1), (20, 2 ** 31 - 1)])
+def test_windows_and_sinks_longer_than_any_sequence(window, sinks):
+    """Rows before the first token among them, which see nothing."""
+    run_case([(40, 35), (1, 70), (3, 0), (150, 140), (1, 2000)], 4, 2, 64, 16, "bf16", window, sinks)
