@@ -51,6 +51,11 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.0f;  // growth of a maximum (in powers of two) that is let pass
+// A maximum m that is kept in base 2 is off by up to half a step from the score
+// that it stands for, and all the row's weights by that power of two: 2^32 at
+// most up to here.  Beyond, items are computed again from the scores' own
+// differences (where a step of the scores is more than the weights can tell).
+constexpr float kFar = 1073741824.0f;  // 2^30
 
 __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
@@ -652,8 +657,8 @@ struct Wide {
             __builtin_amdgcn_sched_barrier(0x6);  // arithmetic may move
         }
     }
-    // of tile i
-    template <typename Tiles>
+    // of tile i; CAREFUL: m is a score, not yet in base 2
+    template <bool CAREFUL, typename Tiles>
     __device__ __forceinline__ void weights(const AttnArgs& a, const Tiles& tiles, int i) {
         const int h = (threadIdx.x >> 5) & 1;
         if (masks(i)) hide(a, pos, tiles(i) + 4 * h, [&](auto hidden) {
@@ -668,23 +673,23 @@ struct Wide {
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
-        if (__ballot(top * a.sl2 > m + kGrow)) {
-            const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
-            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
+        const float unit = CAREFUL ? 1.f : a.sl2;  // of m
+        if (__ballot(top * unit > m + (CAREFUL ? 0.f : kGrow))) {
+            const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * unit);
+            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(CAREFUL ? (m - up) * a.sl2 : m - up);
             m = up;
             l *= f;
 #pragma unroll
             for (int d = 0; d < D / 32; ++d) acc[d] *= f;
         }
         const float off = m == -INFINITY ? 0.f : -m;
+        const auto weight = [&](float x) {
+            return __builtin_amdgcn_exp2f(CAREFUL ? (x + off) * a.sl2 : fmaf(x, a.sl2, off));
+        };
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int r = 0; r < 16; r += 2) {
-                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
-                const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
-                pw[8 * b + r / 2] = pack_bf16(p0, p1);
-            }
+            for (int r = 0; r < 16; r += 2) pw[8 * b + r / 2] = pack_bf16(weight(s[b][r]), weight(s[b][r + 1]));
     }
     // the product of each row's visible tokens alone
     __device__ __forceinline__ void careful_product(const AttnArgs& a, const char* vt, int t0) {
@@ -768,8 +773,9 @@ struct Wide {
 #pragma unroll
         for (int i = 0; i < 16; ++i) asm volatile("" : "+v"(pw[i]));
     }
-    __device__ __forceinline__ bool not_finite() const {
-        float bad = 0.f;
+    // The result is not finite, or its maximum is too far from zero: compute it with care.
+    __device__ __forceinline__ bool needs_care() const {
+        float bad = fabsf(m) >= kFar && m != -INFINITY ? 1.f : 0.f;
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -813,7 +819,8 @@ struct AllTiles {
 // still reach it through the second product (0 * NaN).  Looking for such values
 // in every masked tile costs more than it is worth, so the item looks at its
 // result: when that is not finite, it is computed again, and the tiles in which
-// some row is masked take each row's visible tokens alone.
+// some row is masked take each row's visible tokens alone.  So are items whose
+// maximum is kFar or more from zero.
 template <int D, bool E4M3, bool UNI, bool PAIR>
 __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs a) {
     constexpr int BYTES = AT_TILE * 2 * D, NW = PAIR ? 8 : 4, NB = PAIR ? 4 : 2, LEAD = 3;
@@ -880,7 +887,7 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
             const int t0 = tile(i);
             if (!x.active || none_sees(a, x.p_lo, x.p_hi, t0, t0 + AT_TILE - 1)) continue;
             x.template multiply<true, false>(keys(i), nullptr);
-            x.weights(a, tile, i);
+            x.template weights<false>(a, tile, i);
             x.template multiply<false, true>(nullptr, values(i));
         }
     } else {
@@ -921,7 +928,7 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
             send_values(i);
             send_keys(i);
             places.open(i + 1 + LEAD);
-            x.weights(a, tile, i);
+            x.template weights<false>(a, tile, i);
             x.weighed();
             if (DIRECT && !second) wait_loads<(LEAD - 1) * BOTH>();
             barrier();
@@ -944,7 +951,7 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
         if (!second) barrier();
     }
 
-    if (__syncthreads_or(x.not_finite())) {
+    if (__syncthreads_or(x.needs_care())) {
         x.clear();
         places.look_up(0);
         int i = 0;
@@ -960,11 +967,12 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
             wait_loads<0>();
             barrier();
             x.template multiply<true, false>(keys(0), nullptr);
-            x.weights(a, tile, i);
+            x.template weights<true>(a, tile, i);
             if (x.masks(i)) x.careful_product(a, values(0), tile(i));
             else x.template multiply<false, true>(nullptr, values(0));
             barrier();
         } while (++i < n);
+        x.m *= a.sl2;
     }
 
     x.finish(a, it, head, 32 * w + col < it.nrows);
@@ -988,7 +996,7 @@ __device__ __forceinline__ int n_chunk(int row, int c) {
     return v_chunk<D>(row, c) ^ ((row >> 3) & 1);
 }
 
-// One wave's tiles in the narrow kernel; true where the result is not finite.
+// One wave's tiles in the narrow kernel; true where the result needs care, as in Wide.
 //
 // Lane (col, g) = (lane % 16, lane / 16) loads parts of tokens col and 16 + col,
 // of keys and values alike, at the addresses that it works out itself: 64 bytes
@@ -1100,25 +1108,25 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
-        if (__ballot(top * a.sl2 > m + kGrow)) {
+        const float unit = CAREFUL ? 1.f : a.sl2;  // of m
+        if (__ballot(top * unit > m + (CAREFUL ? 0.f : kGrow))) {
             top = fmaxf(top, __shfl_xor(top, 16));
-            const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * a.sl2);
-            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - up);
+            const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) * unit);
+            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(CAREFUL ? (m - up) * a.sl2 : m - up);
             m = up;
             l *= f;
 #pragma unroll
             for (int d = 0; d < DB; ++d) acc[d] *= f;
         }
         const float off = m == -INFINITY ? 0.f : -m;
+        const auto weight = [&](float x) {
+            return __builtin_amdgcn_exp2f(CAREFUL ? (x + off) * a.sl2 : fmaf(x, a.sl2, off));
+        };
         uint32_t pw[4];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int r = 0; r < 4; r += 2) {
-                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.sl2, off));
-                const float p1 = __builtin_amdgcn_exp2f(fmaf(s[b][r + 1], a.sl2, off));
-                pw[2 * b + r / 2] = pack_bf16(p0, p1);
-            }
+            for (int r = 0; r < 4; r += 2) pw[2 * b + r / 2] = pack_bf16(weight(s[b][r]), weight(s[b][r + 1]));
         l = add_weights(pw[0], pw[1], l);
         l = add_weights(pw[2], pw[3], l);
         if (CAREFUL && masked) {
@@ -1155,7 +1163,8 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
             acc[d] = mfma16(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
         }
     }
-    float bad = 0.f;
+    if (CAREFUL) m *= a.sl2;
+    float bad = fabsf(m) >= kFar && m != -INFINITY ? 1.f : 0.f;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll

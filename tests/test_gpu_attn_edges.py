@@ -1,11 +1,11 @@
 """Attention on the GPU at the edges of its numbers, against what the formula
-gives: NaN scores, windows longer than any sequence."""
+gives: NaN scores, windows longer than any sequence, scores far from zero."""
 import numpy as np
 import pytest
 import torch
 
 from heterogeneous_adapter_batching_amd.attention import AttnBatch
-from test_gpu_attn import check, expected, make_cache, make_table, run_case, tokens
+from test_gpu_attn import U, check, expected, make_cache, make_table, run_case, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -31,13 +31,12 @@ def attend(cache, table, q, kv, scale, heads=4):
 
 
 def set_tokens(t, table, which, value):
-    """Every element of tokens `which` of the one sequence becomes `value` (NaN in e4m3: its code)."""
+    """Every element of tokens `which` of the one sequence becomes `value` (e4m3: its code)."""
     page = t.shape[2]
     at = (torch.from_numpy(table[0][which // page].astype(np.int64)).cuda(), slice(None),
           torch.from_numpy(which % page).cuda())
     if t.dtype == torch.float8_e4m3fn:
-        assert np.isnan(value)
-        t.view(torch.uint8)[at] = 0x7F
+        t.view(torch.uint8)[at] = torch.tensor([value]).to(t.dtype).view(torch.uint8).item()
     else:
         t[at] = value
 
@@ -79,3 +78,28 @@ def test_keys_that_are_nan_give_nan(n, kv, late, dtype):
 def test_windows_and_sinks_longer_than_any_sequence(window, sinks):
     """Rows before the first token among them, which see nothing."""
     run_case([(40, 35), (1, 70), (3, 0), (150, 140), (1, 2000)], 4, 2, 64, 16, "bf16", window, sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,kv", SIZES)
+@pytest.mark.parametrize("query", [1e7, -1e7, 3.1e7, 1e9, -1e12, 1e25])
+def test_scores_far_from_zero(n, kv, query, dtype):
+    """Scores of 1e11 and more, where a step of fp32 is thousands: rows average
+    the values of the tokens with the largest score, however far from zero it
+    is.  Odd tokens have half of the even ones' score.  The weights are equal, so
+    what is left is the sum's rounding and the output's."""
+    cache, table, q = case(n, kv, dtype, 4)
+    set_tokens(cache.k, table, np.arange(kv), -104.0)
+    set_tokens(cache.k, table, np.arange(1, kv, 2), -52.0)
+    if dtype == "e4m3":
+        cache.k_scale.fill_(127)
+    _, v = tokens(cache, table, 0, kv)
+    q.fill_(query)
+    got = attend(cache, table, q, kv, 0.125).double().cpu().numpy().reshape(n, 4, 64)
+    assert np.isfinite(got).all()
+    for i in range(n):
+        seen = np.arange(kv - n + i + 1)
+        best = seen[seen % 2 == (0 if query < 0 or len(seen) == 1 else 1)]
+        want = v[best, 0].mean(0)
+        err = (len(best) + 8) * 2.0 ** -23 * np.abs(v[best, 0]).mean(0)
+        assert np.all(np.abs(got[i] - want) <= err + U * (np.abs(want) + err)), i
