@@ -56,6 +56,10 @@ constexpr float kGrow = 8.0f;  // growth of a maximum (in powers of two) that is
 // most up to here.  Beyond, items are computed again from the scores' own
 // differences (where a step of the scores is more than the weights can tell).
 constexpr float kFar = 1073741824.0f;  // 2^30
+// Weights of an item that is computed again are this much smaller, so that not
+// even 2^30 of the largest values add up to infinity.  (Weights under 2^-90 of
+// the row's largest are lost by it.)
+constexpr float kCare = 2.3283064365386963e-10f;  // 2^-32
 
 __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
@@ -78,12 +82,14 @@ __device__ __forceinline__ f32x4_t add_weights(uint32_t w0, uint32_t w1, f32x4_t
     return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4_t, ones), __builtin_bit_cast(s16x4_t, w), l, 0,
                                                   0, 0);
 }
-// Factor of a part of a row (a wave's or a split's) whose maximum is m, where
-// the row's is top.  A part with no maximum adds what it has: zeros where it saw
-// nothing, NaN where every score that it saw was NaN.
-__device__ __forceinline__ float part_weight(float m, float top) {
-    return m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top);
+// What a part of a row (a wave's or a split's: its output, maximum m and sum l)
+// weighs where the row's maximum is top.  Outputs are joined as a weighted mean,
+// which is no larger than they are.  A part with no maximum adds what it has:
+// zeros where it saw nothing, NaN where every score that it saw was NaN.
+__device__ __forceinline__ float part_weight(float m, float l, float top) {
+    return m == -INFINITY ? l : l * __builtin_amdgcn_exp2f(m - top);
 }
+__device__ __forceinline__ float reciprocal(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // Transposing LDS read: within each 16 lanes, lane i reads 8 bytes (4 bf16) and
@@ -306,7 +312,7 @@ struct AttnArgs {
     const int32_t* table;
     const uint16_t* q;
     uint16_t* out;
-    float* part;  // [n_kv_heads][part_rows][D] partial sums, then [n_kv_heads][part_rows][2] of (maximum, sum)
+    float* part;  // [n_kv_heads][part_rows][D] splits' outputs, then [n_kv_heads][part_rows][2] of (maximum, sum)
     int64_t ldq, ldo, part_rows;
     int32_t n_seq, n_rows, max_kv, ld_table, group, window, sinks;
     uint32_t inv_group;  // 2^31 / group, rounded up
@@ -684,7 +690,8 @@ struct Wide {
         }
         const float off = m == -INFINITY ? 0.f : -m;
         const auto weight = [&](float x) {
-            return __builtin_amdgcn_exp2f(CAREFUL ? (x + off) * a.sl2 : fmaf(x, a.sl2, off));
+            if (CAREFUL) return kCare * __builtin_amdgcn_exp2f((x + off) * a.sl2);
+            return __builtin_amdgcn_exp2f(fmaf(x, a.sl2, off));
         };
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -720,13 +727,13 @@ struct Wide {
             }
         }
     }
-    // the rows' output, or their partial result
-    __device__ __forceinline__ void finish(const AttnArgs& a, const Item& it, int head, bool mine) const {
+    // the rows' output; of a split with its maximum and sum (l is `unit` of it)
+    __device__ __forceinline__ void finish(const AttnArgs& a, const Item& it, int head, bool mine, float unit) const {
         const int h = (threadIdx.x >> 5) & 1;
         const float total = l[0] + __shfl_xor(l[0], 32);
         if (!mine) return;
+        const float inv = reciprocal(total);
         if (it.nsplits == 1) {
-            const float inv = total == 0.f ? 0.f : 1.f / total;
             // a lane's 4 elements and those of the other half's lane make 16 bytes
             uint16_t* o = a.out + row_off(a, it, row, head, a.ldo, D) + 8 * h;
 #pragma unroll
@@ -753,11 +760,11 @@ struct Wide {
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
                     *reinterpret_cast<f32x4_t*>(o + 32 * d + 8 * b) =
-                        f32x4_t{acc[d][4 * b], acc[d][4 * b + 1], acc[d][4 * b + 2], acc[d][4 * b + 3]};
+                        f32x4_t{acc[d][4 * b] * inv, acc[d][4 * b + 1] * inv, acc[d][4 * b + 2] * inv, acc[d][4 * b + 3] * inv};
             if (h == 0) {
                 float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D + 2 * pr;
                 ml[0] = m;
-                ml[1] = total;
+                ml[1] = total / unit;
             }
         }
     }
@@ -849,7 +856,7 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
     const int n = it.it1 - it.it0;
     if (n <= 0) {  // the rows see nothing
         x.clear();
-        x.finish(a, it, head, 32 * w + col < it.nrows);
+        x.finish(a, it, head, 32 * w + col < it.nrows, 1.f);
         return;
     }
     const AllTiles tile{it.span, it.it0, it.it1 - 1};
@@ -951,7 +958,9 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
         if (!second) barrier();
     }
 
+    float unit = 1.f;
     if (__syncthreads_or(x.needs_care())) {
+        unit = kCare;
         x.clear();
         places.look_up(0);
         int i = 0;
@@ -975,7 +984,7 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
         x.m *= a.sl2;
     }
 
-    x.finish(a, it, head, 32 * w + col < it.nrows);
+    x.finish(a, it, head, 32 * w + col < it.nrows, unit);
 }
 
 // Tile number -> first token of the tiles of 32 that one of the narrow kernel's
@@ -1120,7 +1129,8 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
         }
         const float off = m == -INFINITY ? 0.f : -m;
         const auto weight = [&](float x) {
-            return __builtin_amdgcn_exp2f(CAREFUL ? (x + off) * a.sl2 : fmaf(x, a.sl2, off));
+            if (CAREFUL) return kCare * __builtin_amdgcn_exp2f((x + off) * a.sl2);
+            return __builtin_amdgcn_exp2f(fmaf(x, a.sl2, off));
         };
         uint32_t pw[4];
 #pragma unroll
@@ -1204,41 +1214,45 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
     f32x4_t acc[DB];
     float m;
     f32x4_t sum;
-    if (narrow_pass<D, E4M3, false>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w], acc, m, sum))
+    float unit = 1.f;  // of the sum
+    if (narrow_pass<D, E4M3, false>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w], acc, m, sum)) {
+        unit = kCare;
         narrow_pass<D, E4M3, true>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w], acc, m, sum);
+    }
 
-    // join the waves: each leaves its maximum, sum and [row][D] accumulator in LDS
+    // join the waves: each leaves its maximum, sum and [row][D] output in LDS
     float l = sum[0] + __shfl_xor(sum[0], 16);
     l += __shfl_xor(l, 32);
+    const float own = reciprocal(l);
     if (g == 0) {
         s_m[w][col] = m;
-        s_l[w][col] = l;
+        s_l[w][col] = l / unit;
     }
     float* mine = reinterpret_cast<float*>(lds[w]);
 #pragma unroll
-    for (int d = 0; d < DB; ++d) *reinterpret_cast<f32x4_t*>(mine + col * D + 16 * d + 4 * g) = acc[d];
+    for (int d = 0; d < DB; ++d) *reinterpret_cast<f32x4_t*>(mine + col * D + 16 * d + 4 * g) = acc[d] * own;
     __syncthreads();
     constexpr int EPT = D / 16;  // elements per thread: 16 threads a row
     const int r = threadIdx.x / 16, e0 = (threadIdx.x % 16) * EPT;
     if (r >= it.nrows) return;
-    float top = s_m[0][r], total = 0.f, o[EPT];
+    float top = s_m[0][r], total = 0.f, part[4], o[EPT];
 #pragma unroll
     for (int x = 1; x < 4; ++x) top = fmaxf(top, s_m[x][r]);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) total += part[x] = part_weight(s_m[x][r], s_l[x][r], top);
+    const float inv = reciprocal(total);
 #pragma unroll
     for (int e = 0; e < EPT; ++e) o[e] = 0.f;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-        const float f = part_weight(s_m[x][r], top);
-        total = fmaf(f, s_l[x][r], total);
         const float* p = reinterpret_cast<const float*>(lds[x]) + r * D + e0;
 #pragma unroll
-        for (int e = 0; e < EPT; ++e) o[e] = fmaf(f, p[e], o[e]);
+        for (int e = 0; e < EPT; ++e) o[e] = fmaf(part[x] * inv, p[e], o[e]);
     }
     if (it.nsplits == 1) {
-        const float inv = total == 0.f ? 0.f : 1.f / total;
         uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row_off(a, it, r, head, a.ldo, D) + e0);
 #pragma unroll
-        for (int e = 0; e < EPT; e += 2) dst[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
+        for (int e = 0; e < EPT; e += 2) dst[e / 2] = pack_bf16(o[e], o[e + 1]);
     } else {
         const int64_t pr = head * a.part_rows + it.part + r;
         float* dst = a.part + pr * D + e0;
@@ -1278,22 +1292,26 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
         float up = top;
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) up = fmaxf(up, __uint_as_float(x[i][0]));
-        const float old = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - up);
+        float all = part_weight(top, sum, up), part[AHEAD];
+        const float old = all;
         top = up;
-        sum *= old;
-        o *= old;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            part[i] = s + i < it.nsplits ? part_weight(__uint_as_float(x[i][0]), __uint_as_float(x[i][1]), top) : 0.f;
+            all += part[i];
+        }
+        sum = all;
+        const float inv = reciprocal(sum);
+        o *= old * inv;
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             if (s + i >= it.nsplits) continue;
-            const float f = part_weight(__uint_as_float(x[i][0]), top);
-            sum = fmaf(f, __uint_as_float(x[i][1]), sum);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = fmaf(f, p[i][e], o[e]);
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(part[i] * inv, p[i][e], o[e]);
         }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<u32x2_t*>(a.out + row_off(a, it, r, head, a.ldo, D) + e0) =
-        u32x2_t{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+        u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
 }
 
 // ------------------------------------------------------------------ launchers

@@ -1,5 +1,6 @@
 """Attention on the GPU at the edges of its numbers, against what the formula
-gives: NaN scores, windows longer than any sequence, scores far from zero."""
+gives: NaN scores, windows longer than any sequence, scores far from zero, values
+near the largest."""
 import numpy as np
 import pytest
 import torch
@@ -103,3 +104,39 @@ def test_scores_far_from_zero(n, kv, query, dtype):
         want = v[best, 0].mean(0)
         err = (len(best) + 8) * 2.0 ** -23 * np.abs(v[best, 0]).mean(0)
         assert np.all(np.abs(got[i] - want) <= err + U * (np.abs(want) + err)), i
+
+
+HUGE = 3.3e38  # near the largest bf16 value; an e4m3 cache goes to 448 * 2^119
+
+
+def huge_values(cache, rng):
+    """Values near the largest that the cache holds, of one sign in most elements."""
+    x = rng.uniform(0.3, 1.0, cache.v.shape) * np.where(np.arange(cache.v.shape[3]) % 4 == 3, -1, 1)
+    if cache.v_scale is None:
+        cache.v.copy_(torch.from_numpy((HUGE * x).astype(np.float32)))
+    else:
+        cache.v.copy_(torch.from_numpy((448 * x).astype(np.float32)).to(torch.float8_e4m3fn))
+        cache.v_scale.fill_(127 + 119)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,kv", SIZES + [(1, 2), (2, 130), (40, 400)])
+@pytest.mark.parametrize("scale", [1e-6, 0.125, 2.0])
+def test_values_near_the_largest(n, kv, scale, dtype):
+    """A weighted mean is no larger than its largest value, whatever its sum is."""
+    cache, table, q = case(n, kv, dtype, 5)
+    huge_values(cache, np.random.default_rng(6))
+    out = attend(cache, table, q, kv, scale)
+    check(out, *expected(cache, table, q, [n], [kv], 4, 0, 0, scale))
+
+
+@pytest.mark.parametrize("n,kv,every", [(1, 128, 32), (1, 3000, 32), (1, 3000, 256), (33, 2000, 64), (300, 2433, 128)])
+def test_values_near_the_largest_in_every_part(n, kv, every):
+    """Equal weights, one token in each wave's or split's part and none beside it."""
+    cache, table, q = case(n, kv, "bf16", 7)
+    huge_values(cache, np.random.default_rng(8))
+    set_tokens(cache.k, table, np.arange(kv), -8.0)
+    set_tokens(cache.k, table, np.arange(0, kv, every), 8.0)
+    q.fill_(1.0)
+    out = attend(cache, table, q, kv, 0.125)
+    check(out, *expected(cache, table, q, [n], [kv], 4, 0, 0, 0.125))
