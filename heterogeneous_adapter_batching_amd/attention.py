@@ -74,7 +74,10 @@ class AttnBatch:
     ``refresh(q_len, kv_len, block_table)`` plans a new batch with one library
     call (lora_attn_prepare), reusing the host and device buffers, which grow
     when a batch needs more; callables from ``prepare_*`` stay valid, with
-    tensors that have rows enough for the new batch.  One plan serves every
+    tensors that have rows enough for the new batch (a captured graph holds the
+    buffers of its own time, and has to be captured again once they have grown).
+    The buffers belong to the stream of the refresh that made them: work on the
+    batch from other streams has to be ordered after it by events.  One plan serves every
     layer whose cache has the same shape, mask and type: the calls take another
     ``cache`` than the one the batch was made with."""
 
@@ -91,13 +94,19 @@ class AttnBatch:
         self._dev = torch.empty(0, dtype=torch.int32, device=self.device)
         self._planned = False
         self._streams = {}           # streams that work on the batch's buffers was put on
-        self._alloc(1 << 12)
+        self._host = torch.empty(0, dtype=torch.int32)
 
     def _use(self, stream):
-        """The stream's raw handle; remembers the stream."""
+        """The stream that is meant; remembers it."""
         s = torch.cuda.current_stream(self.device) if stream is None else stream
         self._streams[s.cuda_stream] = s
-        return s.cuda_stream
+        return s
+
+    def _empty(self, n, dtype, stream):
+        """Device memory that was free on the stream when it was asked for: the
+        allocator hands out blocks that its current stream may still be using."""
+        with torch.cuda.stream(stream):
+            return torch.empty(n, dtype=dtype, device=self.device)
 
     def _drop(self, t):
         """A device buffer is let go: its memory is not handed out again before
@@ -105,10 +114,10 @@ class AttnBatch:
         for s in self._streams.values():
             t.record_stream(s)
 
-    def _alloc(self, cap):
+    def _alloc(self, cap, stream):
         self._drop(self._dev)
         self._host = torch.empty(cap, dtype=torch.int32, pin_memory=True)
-        self._dev = torch.empty(cap, dtype=torch.int32, device=self.device)
+        self._dev = self._empty(cap, torch.int32, stream)
 
     def refresh(self, q_len, kv_len, block_table, stream=None):
         """q_len, kv_len: int [n_seq], new tokens and cached tokens with them;
@@ -123,7 +132,10 @@ class AttnBatch:
             self._copied.synchronize()   # the staging buffer may still be in flight
             self._pending = False
         self._planned = False
-        h = self._use(stream)
+        s = self._use(stream)
+        h = s.cuda_stream
+        if not self._host.shape[0]:
+            self._alloc(1 << 12, s)
         while True:
             st = _lib.lora_attn_prepare(ctypes.byref(self.shape), ql.shape[0], ql.ctypes.data, kl.ctypes.data,
                                         None if tab is None else tab.ctypes.data, 0 if tab is None else tab.shape[1],
@@ -131,14 +143,14 @@ class AttnBatch:
                                         self._ref)
             if st != LORA_ECAPACITY or self._launch.info.n_staged <= self._host.shape[0]:
                 break
-            self._alloc(int(self._launch.info.n_staged) * 2)
+            self._alloc(int(self._launch.info.n_staged) * 2, s)
         check_status(st, "lora_attn_prepare")
         if self.info.n_staged:
             self._copied.record(h)
             self._pending = True
         if self.info.workspace_floats > self._workspace.shape[0]:
             self._drop(self._workspace)
-            self._workspace = torch.empty(int(self.info.workspace_floats), dtype=torch.float32, device=self.device)
+            self._workspace = self._empty(int(self.info.workspace_floats), torch.float32, s)
         self._planned = True
         return self
 
@@ -188,7 +200,7 @@ class AttnBatch:
             if rope.dim() != 2 or rope.dtype != torch.float32 or not rope.is_contiguous() or rope.device != self.device:
                 raise ValueError("rope: contiguous float32 [positions, rope_dim]")
             args.rope, args.rope_len, args.rope_dim = rope.data_ptr(), rope.shape[0], rope.shape[1]
-        h, L, rows = self._use(stream), self._launch, min(have)
+        h, L, rows = self._use(stream).cuda_stream, self._launch, min(have)
         kv_ref, arg_ref, ref, call = ctypes.byref(cache.c()), ctypes.byref(args), self._ref, _lib.lora_kv_write
 
         def run():
@@ -208,7 +220,7 @@ class AttnBatch:
         rows = min(self._rows(k_out, hk, torch.bfloat16, "k_out"), self._rows(v_out, hk, torch.bfloat16, "v_out"))
         if k_out.stride(0) != v_out.stride(0):
             raise ValueError("k_out and v_out have rows of one stride")
-        h, L, ref, kv_ref = self._use(stream), self._launch, self._ref, ctypes.byref(cache.c())
+        h, L, ref, kv_ref = self._use(stream).cuda_stream, self._launch, self._ref, ctypes.byref(cache.c())
         kp, vp, ld, call = k_out.data_ptr(), v_out.data_ptr(), k_out.stride(0), _lib.lora_kv_read
 
         def run():
@@ -226,7 +238,7 @@ class AttnBatch:
         ordered (one stream, or events)."""
         cache = self._check_cache(cache)
         rows = min(self._rows(q, self.n_heads, torch.bfloat16, "q"), self._rows(out, self.n_heads, torch.bfloat16, "out"))
-        h, L, ref, kv_ref = self._use(stream), self._launch, self._ref, ctypes.byref(cache.c())
+        h, L, ref, kv_ref = self._use(stream).cuda_stream, self._launch, self._ref, ctypes.byref(cache.c())
         qp, ldq, op, ldo, scale, call = q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), float(scale), _lib.lora_attn
 
         def run():
