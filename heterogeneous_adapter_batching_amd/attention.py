@@ -8,7 +8,9 @@ attention of their queries, and the read of whole sequences.  As in session.py,
 a callable that only issues the library call; PyTorch only provides memory and
 streams.
 """
+import collections
 import ctypes
+import sys
 
 import numpy as np
 import torch
@@ -16,6 +18,20 @@ import torch
 from . import (LORA_BF16, LORA_ECAPACITY, LORA_F32, LORA_KV_BF16, LORA_KV_E4M3, LORA_OK, _lib, check_status,
                lora_attn_launch_t, lora_attn_shape_t, lora_kv_t, lora_kv_write_args_t)
 from .session import HipEvent
+
+# staging buffers of batches let go, with the event of the copy that may be reading each
+_held = collections.deque()
+
+
+def _release():
+    """Lets the staging buffers go whose copies have ended."""
+    for _ in range(len(_held)):
+        try:
+            held = _held.popleft()
+        except IndexError:  # another thread's
+            return
+        if not held[1].query():
+            _held.append(held)
 
 
 class KvCache:
@@ -94,6 +110,7 @@ class AttnBatch:
         self._dev = torch.empty(0, dtype=torch.int32, device=self.device)
         self._planned = False
         self._streams = {}           # streams that work on the batch's buffers was put on
+        # pinned; the library's copies out of it are unknown to its allocator
         self._host = torch.empty(0, dtype=torch.int32)
 
     def _use(self, stream):
@@ -114,7 +131,16 @@ class AttnBatch:
         for s in self._streams.values():
             t.record_stream(s)
 
+    def __del__(self):
+        if sys.is_finalizing() or not hasattr(self, "_host"):
+            return
+        if self._pending:
+            _held.append((self._host, self._copied))
+        self._drop(self._dev)
+        self._drop(self._workspace)
+
     def _alloc(self, cap, stream):
+        _release()
         self._drop(self._dev)
         self._host = torch.empty(cap, dtype=torch.int32, pin_memory=True)
         self._dev = self._empty(cap, torch.int32, stream)

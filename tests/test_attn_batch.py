@@ -99,7 +99,9 @@ def cache(pages=5000, device=DEVICE, dtype=hl.LORA_KV_BF16):
 
 @pytest.fixture
 def world(monkeypatch):
-    return World(monkeypatch)
+    yield World(monkeypatch)
+    gc.collect()
+    attention._held.clear()
 
 
 def test_buffers_belong_to_the_stream_that_uses_them(world):
@@ -128,3 +130,23 @@ def test_a_buffer_that_grows_is_held_for_the_streams_that_use_it(world):
     old = world.used()
     batch.refresh(*LONG, stream=one)
     assert all({s.cuda_stream for s in b.recorded} >= {1, 2} for b in old)
+
+
+def test_a_batch_let_go_leaves_its_buffers_to_the_work_under_way(world):
+    """The staging buffer is read by a copy that the allocator knows nothing of, the
+    others by work on any of the batch's streams."""
+    side = Stream(7)
+    batch = attention.AttnBatch(cache(), 4)
+    batch.refresh(*LONG, stream=side)
+    assert batch._pending and not batch._copied.done
+    copied, staging, buffers = batch._copied, batch._host.data_ptr(), world.used()
+    del batch
+    gc.collect()
+    assert not copied.done  # nobody waited
+    assert [h.data_ptr() for h, _ in attention._held] == [staging]
+    assert all(side in b.recorded for b in buffers[-2:])
+    copied.done = True
+    attention.AttnBatch(cache(), 4).refresh(*LONG, stream=side)  # asks for a staging buffer
+    gc.collect()
+    assert all(h.data_ptr() != staging or not e.done for h, e in attention._held)
+    assert len(attention._held) == 1  # that of the batch just made
