@@ -100,6 +100,8 @@ class AttnBatch:
     def __init__(self, cache, n_heads, window=0, sinks=0):
         self.cache, self.n_heads = cache, int(n_heads)
         self.device = cache.k.device
+        if self.device.type != "cuda":
+            raise ValueError("the cache is not on the GPU")
         self.shape = lora_attn_shape_t(self.n_heads, cache.n_kv_heads, cache.head_dim, cache.page_tokens,
                                        cache.n_pages, cache.dtype, int(window), int(sinks))
         self._launch = lora_attn_launch_t()
@@ -190,6 +192,8 @@ class AttnBatch:
         if (cache.n_pages, cache.n_kv_heads, cache.page_tokens, cache.head_dim, cache.dtype) != (
                 s.n_pages, s.n_kv_heads, s.page_tokens, s.head_dim, s.kv_dtype):
             raise ValueError("the cache has another shape or type than the plan's")
+        if cache.k.device != self.device:
+            raise ValueError(f"the cache is not on {self.device}")
         return cache
 
     def _rows(self, t, heads, dtype, name):

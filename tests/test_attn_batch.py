@@ -150,3 +150,22 @@ def test_a_batch_let_go_leaves_its_buffers_to_the_work_under_way(world):
     gc.collect()
     assert all(h.data_ptr() != staging or not e.done for h, e in attention._held)
     assert len(attention._held) == 1  # that of the batch just made
+
+
+def test_refuses_a_cache_that_is_not_on_the_device(world):
+    cpu, other = torch.device("cpu"), torch.device("cuda", 1)
+    with pytest.raises(ValueError):
+        attention.AttnBatch(cache(device=cpu), 4)
+    batch = attention.AttnBatch(cache(), 4).refresh([1], [20], np.array([[1, 2]], np.int32))
+    q = types.SimpleNamespace(dim=lambda: 2, shape=(1, 256), stride=lambda i: (256, 1)[i], dtype=torch.bfloat16,
+                              device=DEVICE, data_ptr=lambda: 0x1000)
+    kv = types.SimpleNamespace(dim=lambda: 2, shape=(20, 128), stride=lambda i: (128, 1)[i], dtype=torch.bfloat16,
+                               device=DEVICE, data_ptr=lambda: 0x1000)
+    batch.prepare_attn(q, q, 0.1, cache=cache())
+    for device in (cpu, other):
+        with pytest.raises(ValueError):
+            batch.prepare_attn(q, q, 0.1, cache=cache(device=device))
+        with pytest.raises(ValueError):
+            batch.prepare_write(kv, kv, cache=cache(device=device))
+        with pytest.raises(ValueError):
+            batch.prepare_read(kv, kv, cache=cache(device=device))
