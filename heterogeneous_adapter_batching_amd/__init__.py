@@ -328,14 +328,25 @@ def lora_pool_scatter(src_ptr, pool_ptr, n, src_off_ptr, dst_off_ptr, len_ptr, s
            "lora_pool_scatter")
 
 
+def as_int32(x, name):
+    """x as a contiguous int32 array; ValueError where that changes a number."""
+    a = np.asarray(x)
+    if a.dtype != np.int32:
+        with np.errstate(invalid="ignore"):
+            narrow = a.astype(np.int32)
+        if not np.array_equal(narrow, a):
+            raise ValueError(f"{name}: not whole numbers of 32 bits")
+        a = narrow
+    return np.ascontiguousarray(a)
+
+
 def lora_attn_plan(shape, q_len, kv_len, block_table=None, staging_capacity=None, raw=False):
     """Attention plan of a batch (host).  block_table: int32 [n_seq, pages], or
     None when nothing is cached.  Returns (staging int32 [n_staged], info), or
     (status, staging, info) with raw=True."""
-    ql = np.ascontiguousarray(q_len, dtype=np.int32)
-    kl = np.ascontiguousarray(kv_len, dtype=np.int32)
+    ql, kl = as_int32(q_len, "q_len"), as_int32(kv_len, "kv_len")
     assert ql.shape == kl.shape and ql.ndim == 1
-    tab = None if block_table is None else np.ascontiguousarray(block_table, dtype=np.int32)
+    tab = None if block_table is None else as_int32(block_table, "block_table")
     assert tab is None or (tab.ndim == 2 and tab.shape[0] == ql.shape[0])
     info = lora_attn_info_t()
     args = (ctypes.byref(shape), ql.shape[0], ql.ctypes.data, kl.ctypes.data, _ptr(tab),

@@ -15,7 +15,7 @@ import sys
 import numpy as np
 import torch
 
-from . import (LORA_BF16, LORA_ECAPACITY, LORA_F32, LORA_KV_BF16, LORA_KV_E4M3, LORA_OK, _lib, check_status,
+from . import (LORA_BF16, LORA_ECAPACITY, LORA_F32, LORA_KV_BF16, LORA_KV_E4M3, LORA_OK, _lib, as_int32, check_status,
                lora_attn_launch_t, lora_attn_shape_t, lora_kv_t, lora_kv_write_args_t)
 from .session import HipEvent
 
@@ -98,12 +98,14 @@ class AttnBatch:
     ``cache`` than the one the batch was made with."""
 
     def __init__(self, cache, n_heads, window=0, sinks=0):
-        self.cache, self.n_heads = cache, int(n_heads)
+        n_heads, window, sinks = (int(as_int32(x, name)[0]) for x, name in
+                                  ((n_heads, "n_heads"), (window, "window"), (sinks, "sinks")))
+        self.cache, self.n_heads = cache, n_heads
         self.device = cache.k.device
         if self.device.type != "cuda":
             raise ValueError("the cache is not on the GPU")
         self.shape = lora_attn_shape_t(self.n_heads, cache.n_kv_heads, cache.head_dim, cache.page_tokens,
-                                       cache.n_pages, cache.dtype, int(window), int(sinks))
+                                       cache.n_pages, cache.dtype, window, sinks)
         self._launch = lora_attn_launch_t()
         self._ref = ctypes.byref(self._launch)
         self._copied = HipEvent()    # the last staging copy
@@ -151,9 +153,8 @@ class AttnBatch:
         """q_len, kv_len: int [n_seq], new tokens and cached tokens with them;
         block_table: int32 [n_seq, pages] page ids (host), or None when nothing
         is cached."""
-        ql = np.ascontiguousarray(q_len, dtype=np.int32)
-        kl = np.ascontiguousarray(kv_len, dtype=np.int32)
-        tab = None if block_table is None else np.ascontiguousarray(block_table, dtype=np.int32)
+        ql, kl = as_int32(q_len, "q_len"), as_int32(kv_len, "kv_len")
+        tab = None if block_table is None else as_int32(block_table, "block_table")
         if ql.ndim != 1 or ql.shape != kl.shape or (tab is not None and (tab.ndim != 2 or tab.shape[0] != ql.shape[0])):
             raise ValueError("q_len [n_seq], kv_len [n_seq], block_table [n_seq, pages]")
         if self._pending:

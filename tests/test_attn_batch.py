@@ -12,6 +12,7 @@ import torch
 
 import heterogeneous_adapter_batching_amd as hl
 from heterogeneous_adapter_batching_amd import attention
+from test_attn_plan import check_plan
 
 DEVICE = torch.device("cuda", 0)
 LONG = ([1] * 8, [9000] * 8, np.arange(8 * 600, dtype=np.int32).reshape(8, 600))  # splits, and a large table
@@ -169,3 +170,37 @@ def test_refuses_a_cache_that_is_not_on_the_device(world):
             batch.prepare_write(kv, kv, cache=cache(device=device))
         with pytest.raises(ValueError):
             batch.prepare_read(kv, kv, cache=cache(device=device))
+
+
+WRAPS = 2 ** 32  # to 0 in 32 bits
+
+
+@pytest.mark.parametrize("q_len,kv_len,table", [
+    ([WRAPS + 1], [20], [[1, 2]]), ([1], [WRAPS + 20], [[1, 2]]), ([1], [20], [[1, WRAPS + 2]]),
+    ([1], [20], [[1, -WRAPS + 2]]), ([1], [20.5], [[1, 2]]), ([float("nan")], [20], [[1, 2]])])
+def test_refuses_numbers_that_32_bits_do_not_hold(world, q_len, kv_len, table):
+    """Wrapped round they are lengths and pages of another batch."""
+    batch = attention.AttnBatch(cache(), 4)
+    args = [np.array(x) for x in (q_len, kv_len, table)]
+    with pytest.raises(ValueError):
+        batch.refresh(*args)
+    with pytest.raises(ValueError):
+        hl.lora_attn_plan(batch.shape, *args)
+
+
+@pytest.mark.parametrize("args", [dict(n_heads=WRAPS + 4), dict(n_heads=4, window=WRAPS), dict(n_heads=4, window=-WRAPS + 9),
+                                  dict(n_heads=4, window=9, sinks=WRAPS)])
+def test_refuses_a_shape_that_32_bits_do_not_hold(world, args):
+    with pytest.raises(ValueError):
+        attention.AttnBatch(cache(), **args)
+
+
+def test_takes_whole_numbers_of_any_type(world):
+    table = np.array([[1, 2]])
+    for kind in (np.int64, np.uint64, np.int16, np.float64):
+        for args in (([1], [20], table), (np.array([1], kind), np.array([20], kind), table.astype(kind)),
+                     (torch.tensor([1]), torch.tensor([20]), torch.from_numpy(table))):
+            batch = attention.AttnBatch(cache(), 4).refresh(*args)
+            check_plan(batch.shape, [1], [20], table, batch._host.numpy()[:batch.info.n_staged], batch.info)
+    batch = attention.AttnBatch(cache(), 4).refresh([], [], None)
+    assert batch.info.n_rows == 0
