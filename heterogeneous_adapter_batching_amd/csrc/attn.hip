@@ -1359,15 +1359,17 @@ extern "C" int32_t lora_attn_prepare(const lora_attn_shape_t* shape, int32_t n_s
                                      const int32_t* kv_len, const int32_t* block_table, int64_t ld_table,
                                      int32_t* staging, int64_t staging_capacity, void* dev_staging, void* hip_stream,
                                      lora_attn_launch_t* out) {
-    if (!out || !dev_staging || !aligned16(dev_staging)) return LORA_EINVAL;
+    if (!out) return LORA_EINVAL;
+    out->meta = nullptr;  // info may change with an error, and the calls would take it for the old plan's
+    if (!dev_staging || !aligned16(dev_staging)) return LORA_EINVAL;
     const int32_t st = lora_attn_plan(shape, n_seq, q_len, kv_len, block_table, ld_table, staging, staging_capacity,
                                       &out->info);
     if (st != LORA_OK) return st;
-    out->meta = static_cast<const int32_t*>(dev_staging);
-    if (out->info.n_staged == 0) return LORA_OK;
     const hipError_t e = hipMemcpyAsync(dev_staging, staging, (size_t)out->info.n_staged * sizeof(int32_t),
                                         hipMemcpyHostToDevice, reinterpret_cast<hipStream_t>(hip_stream));
-    return e == hipSuccess ? LORA_OK : LORA_EHIP;
+    if (e != hipSuccess) return LORA_EHIP;
+    out->meta = static_cast<const int32_t*>(dev_staging);
+    return LORA_OK;
 }
 
 extern "C" int32_t lora_kv_write(const lora_attn_launch_t* L, const lora_kv_t* kv, const lora_kv_write_args_t* w,

@@ -780,8 +780,8 @@ int32_t lora_attn_plan(const lora_attn_shape_t* shape, int32_t n_seq,
 /* lora_attn_plan, and the staging buffer's copy to dev_staging (device,
  * 16-byte aligned, as large) enqueued on hip_stream; `staging` is as in
  * lora_batch_prepare.  out is ready for the calls below; one plan serves every
- * layer of a step whose caches have the same shape.  Errors: as
- * lora_attn_plan, LORA_EHIP. */
+ * layer of a step whose caches have the same shape.  After an error out holds
+ * no plan, and the calls below refuse it.  Errors: as lora_attn_plan, LORA_EHIP. */
 int32_t lora_attn_prepare(const lora_attn_shape_t* shape, int32_t n_seq,
                           const int32_t* q_len, const int32_t* kv_len,
                           const int32_t* block_table, int64_t ld_table,

@@ -1,9 +1,11 @@
 """CPU tests of the attention plan at the ends of its ranges."""
+import ctypes
+
 import numpy as np
 import pytest
 
 import heterogeneous_adapter_batching_amd as hl
-from test_attn_plan import check_plan, make_table, shape
+from test_attn_plan import _attn, _kv, _launch, _read, _write, check_plan, make_table, shape
 
 LAST = 2 ** 31 - 1
 # new tokens and cached tokens with them, rows before the first token among them
@@ -30,3 +32,19 @@ def test_more_sinks_than_any_sequence_has_tokens(window, sinks):
     tab = make_table(np.random.default_rng(4), kv_len, 16, 1000)
     staging, info = hl.lora_attn_plan(shape(window=window, sinks=sinks), q_len, kv_len, tab)
     check_plan(shape(window=window, sinks=sinks), q_len, kv_len, tab, staging, info)
+
+
+@pytest.mark.parametrize("q_len,kv_len,capacity,code", [
+    ([3, 3], [20, 20], 40, hl.LORA_ECAPACITY), ([3], [20000], 4000, hl.LORA_EINVAL), ([3], [33], 4000, hl.LORA_EPAGE)])
+def test_a_launch_holds_no_plan_after_an_error(q_len, kv_len, capacity, code):
+    """Not the new batch's numbers with the old one's places either."""
+    L = _launch()
+    tab = np.array([[0, 1, 5000]] * len(q_len), np.int32)
+    lens = [np.array(x, np.int32) for x in (q_len, kv_len)]
+    staging, s = np.zeros(4000, np.int32), shape()
+    assert _attn(L, _kv(), scale=0.0) == hl.LORA_EINVAL and L.meta  # a plan, refused for the scale alone
+    st = hl._lib.lora_attn_prepare(ctypes.byref(s), len(q_len), lens[0].ctypes.data, lens[1].ctypes.data, tab.ctypes.data,
+                                   tab.shape[1], staging.ctypes.data, capacity, 0x1000, None, ctypes.byref(L))
+    assert st == code
+    assert not L.meta
+    assert _attn(L, _kv()) == hl.LORA_EINVAL and _write(L, _kv()) == hl.LORA_EINVAL and _read(L, _kv()) == hl.LORA_EINVAL
