@@ -1,11 +1,14 @@
 """CPU tests of the attention plan at the ends of its ranges."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
 
 import heterogeneous_adapter_batching_amd as hl
-from test_attn_plan import _attn, _kv, _launch, _read, _write, check_plan, make_table, shape
+from test_attn_plan import REPO, _attn, _kv, _launch, _read, _write, check_plan, make_table, shape
 
 LAST = 2 ** 31 - 1
 # new tokens and cached tokens with them, rows before the first token among them
@@ -48,3 +51,27 @@ def test_a_launch_holds_no_plan_after_an_error(q_len, kv_len, capacity, code):
     assert st == code
     assert not L.meta
     assert _attn(L, _kv()) == hl.LORA_EINVAL and _write(L, _kv()) == hl.LORA_EINVAL and _read(L, _kv()) == hl.LORA_EINVAL
+
+
+def _sanitize(tmp_path, planner):
+    exe = tmp_path / "attn_sanitize_edges"
+    csrc = os.path.join(REPO, "heterogeneous_adapter_batching_amd", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+                    "-I", os.path.join(REPO, "include"), "-I", csrc, planner,
+                    os.path.join(REPO, "tests", "attn_sanitize_edges.cpp"), "-o", str(exe)], check=True)
+    return subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_planner_over_its_ranges_under_sanitizers(tmp_path):
+    r = _sanitize(tmp_path, os.path.join(REPO, "heterogeneous_adapter_batching_amd", "csrc", "attn_plan.cpp"))
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "attention planner ok over its ranges" in r.stdout
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_that_test_fails_for_a_planner_that_refuses_everything(tmp_path):
+    stub = tmp_path / "refuses.cpp"
+    stub.write_text('#include "hetlora.h"\nextern "C" int32_t lora_attn_plan(const lora_attn_shape_t*, int32_t, const int32_t*, '
+                    'const int32_t*, const int32_t*, int64_t, int32_t*, int64_t, lora_attn_info_t*) { return LORA_EINVAL; }\n')
+    assert _sanitize(tmp_path, str(stub)).returncode == 1
