@@ -332,17 +332,11 @@ struct Item : lora_attn_work_t {
 // cannot index outside the buffers.
 __device__ __forceinline__ bool load_item(const AttnArgs& a, int i, int max_rows, bool merge, Item& it) {
     static_cast<lora_attn_work_t&>(it) = a.work[i];
-    if (it.seq < 0 || it.seq >= a.n_seq || it.n_new < 0 || it.kv < 0 || it.q0 < 0 || it.q0 + it.n_new > a.n_rows ||
-        it.kv > a.max_kv)
-        return false;
-    if (it.nrows < 1 || it.nrows > max_rows || it.tok0 < 0 || it.lead < 0 || it.lead >= a.group ||
-        it.tok0 + (int64_t)token_of(a, it.lead + it.nrows - 1) >= it.n_new)
-        return false;
-    if (it.nsplits > 1 && (it.part < 0 || it.part + (int64_t)it.nrows * (merge ? it.nsplits : 1) > a.part_rows))
-        return false;
+    const int last_tok = token_of(a, it.lead + it.nrows - 1);
+    if (!at_inside(&it, a.n_seq, a.n_rows, a.max_kv, a.group, max_rows, a.part_rows, last_tok, merge)) return false;
     it.p0 = it.kv - it.n_new + it.tok0;
     it.table = a.table + (int64_t)it.seq * a.ld_table;
-    it.span = at_span(it.p0, it.p0 + token_of(a, it.lead + it.nrows - 1), a.window, a.sinks);
+    it.span = at_span(it.p0, it.p0 + last_tok, a.window, a.sinks);
     it.it0 = max(it.it0, 0);
     it.it1 = min(it.it1, merge ? it.nrows : at_span_tiles(it.span));
     return true;

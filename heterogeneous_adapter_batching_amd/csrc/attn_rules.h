@@ -6,6 +6,8 @@
 
 #include <stdint.h>
 
+#include "../../include/hetlora.h"
+
 #ifndef AT_FN
 #define AT_FN static inline
 #endif
@@ -45,5 +47,22 @@ AT_FN struct AtSpan at_span(int32_t p_lo, int32_t p_hi, int32_t window, int32_t 
 }
 AT_FN int32_t at_span_tiles(struct AtSpan s) { return s.sinks + s.end - s.first; }
 AT_FN int32_t at_span_tile(struct AtSpan s, int32_t i) { return i < s.sinks ? i : s.first + (i - s.sinks); }
+
+// An item (or merge entry) of at most max_rows rows lies inside the batch and the
+// workspace.  last_tok = (lead + nrows - 1) / group.
+AT_FN int at_inside(const lora_attn_work_t* w, int32_t n_seq, int32_t n_rows, int32_t max_kv, int32_t group,
+                    int32_t max_rows, int64_t part_rows, int32_t last_tok, int merge) {
+    if (w->seq < 0 || w->seq >= n_seq || w->n_new < 0 || w->kv < 0 || w->kv > max_kv || w->q0 < 0 ||
+        w->q0 + (int64_t)w->n_new > n_rows)
+        return 0;
+    if (w->nrows < 1 || w->nrows > max_rows || w->tok0 < 0 || w->lead < 0 || w->lead >= group ||
+        w->tok0 + (int64_t)last_tok >= w->n_new)
+        return 0;
+    if (w->nsplits < 1) return 0;
+    if ((merge || w->nsplits > 1) &&
+        (w->part < 0 || w->part + (int64_t)w->nrows * (merge ? w->nsplits : 1) > part_rows))
+        return 0;
+    return 1;
+}
 
 #endif
