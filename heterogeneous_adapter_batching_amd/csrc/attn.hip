@@ -1444,7 +1444,7 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     const int64_t width = (int64_t)I.shape.n_heads * d;
     if (I.n_rows == 0) return LORA_OK;
     if (bad_rows(q, ldq, width) || bad_rows(out, ldo, width)) return LORA_EINVAL;
-    if (!(scale > 0.f) || !(scale < INFINITY)) return LORA_EINVAL;
+    if (!(scale > 0.f) || !(scale * kLog2e < INFINITY)) return LORA_EINVAL;  // 0 * infinity is no score
     if (I.workspace_floats > 0) {
         if (workspace_floats < I.workspace_floats) return LORA_ECAPACITY;
         if (!workspace || !aligned16(workspace)) return LORA_EINVAL;

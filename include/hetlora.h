@@ -832,7 +832,7 @@ int32_t lora_kv_read(const lora_attn_launch_t* launch, const lora_kv_t* kv,
  *   q      device bf16 [info.n_rows] rows of n_heads * head_dim, ldq apart,
  *          16-byte aligned, ldq % 8 == 0
  *   out    device bf16, the same layout with ldo; must not overlap q
- *   scale  > 0, finite
+ *   scale  > 0; scale * log2 e finite in fp32
  *   workspace  device fp32 [workspace_floats >= info.workspace_floats],
  *          16-byte aligned; may be NULL when info.workspace_floats is 0.
  *          Calls that overlap in time need one each

@@ -75,3 +75,9 @@ def test_that_test_fails_for_a_planner_that_refuses_everything(tmp_path):
     stub.write_text('#include "hetlora.h"\nextern "C" int32_t lora_attn_plan(const lora_attn_shape_t*, int32_t, const int32_t*, '
                     'const int32_t*, const int32_t*, int64_t, int32_t*, int64_t, lora_attn_info_t*) { return LORA_EINVAL; }\n')
     assert _sanitize(tmp_path, str(stub)).returncode == 1
+
+
+def test_attn_refuses_a_scale_that_overflows_in_base_2():
+    """Scores are multiplied by scale * log2 e, and zero by infinity is not zero."""
+    for scale in (2.4e38, 3.4e38):
+        assert _attn(_launch(), _kv(), scale=scale) == hl.LORA_EINVAL
