@@ -26,7 +26,7 @@ extern "C" const char* lora_status_string(int32_t status) {
         case LORA_EINVAL: return "invalid argument (null pointer, negative count, stride or alignment)";
         case LORA_EADAPTER: return "adapter id out of range";
         case LORA_ERANK: return "rank out of range [1, 128]";
-        case LORA_ESHAPE: return "dimension or chunk length not a positive multiple of 64";
+        case LORA_ESHAPE: return "shape that the call does not take (LoRA: a dimension or chunk length not a positive multiple of 64)";
         case LORA_ECAPACITY: return "output capacity too small";
         case LORA_EHIP: return "HIP launch error";
         case LORA_EPAGE: return "page id out of range";

@@ -86,7 +86,8 @@ extern "C" {
 #define LORA_EINVAL    -1  /* null pointer, negative count, ld < d, misaligned pointer */
 #define LORA_EADAPTER  -2  /* adapter id outside [-1, n_adapters)                     */
 #define LORA_ERANK     -3  /* rank outside [1, LORA_MAX_RANK]                          */
-#define LORA_ESHAPE    -4  /* d_in / d_out / chunk_len not a positive multiple of 64   */
+#define LORA_ESHAPE    -4  /* shape not taken: d_in / d_out / chunk_len not a positive
+                               multiple of 64, heads, pages or caches as said there     */
 #define LORA_ECAPACITY -5  /* an output capacity is too small                          */
 #define LORA_EHIP      -6  /* a HIP launch reported an error                           */
 #define LORA_EPAGE     -7  /* page id outside [0, n_pages)                             */

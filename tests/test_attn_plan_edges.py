@@ -81,3 +81,7 @@ def test_attn_refuses_a_scale_that_overflows_in_base_2():
     """Scores are multiplied by scale * log2 e, and zero by infinity is not zero."""
     for scale in (2.4e38, 3.4e38):
         assert _attn(_launch(), _kv(), scale=scale) == hl.LORA_EINVAL
+
+
+def test_status_of_a_shape_says_so():
+    assert "shape" in hl.lora_status_string(hl.LORA_ESHAPE)
