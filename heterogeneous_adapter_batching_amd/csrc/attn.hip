@@ -23,11 +23,18 @@
 // and the accumulator is rescaled only when a row's maximum grows by more than
 // 2^8 over the one in use: weights then stay below 2^8, far inside fp32 and
 // bf16, and the common tile pays neither the rescale nor a reduction over
-// lanes (prompts of up to 2048 tokens took 112 us with a rescale at any growth,
-// 108 so; 2 x 1024 tokens over 33k 2.00 and 1.98 ms).  Weights are rounded to bf16 for the second product, and the rounded
-// weights are what the row's sum adds up, so the rounding cancels where few
-// tokens dominate: the 4x4x4 MFMA with a first operand of ones gives each lane
-// the sum of the four weights that it holds itself.
+// lanes (16 prompts of up to 2048 tokens take 109 us with a rescale at any
+// growth, 104 so; 2 x 1024 tokens over 33k 1906 and 1852).
+//
+// Weights are rounded to bf16 for the second product, and the rounded weights are
+// what the row's sum adds up, so the rounding cancels where few tokens dominate:
+// the 4x4x4 MFMA with a first operand of ones gives each lane the sum of the four
+// weights that it holds itself.  In the narrow kernel, which waits for memory, a
+// second product adds what the rounding left (16 bits of a weight in all): outputs
+// are then as exact as their own type, off by 1.7e-3 of their norm where one part
+// gives 2.2e-3, for 0.2 us of a call.  In the wide one that takes 141 us where one
+// part takes 104 (prompts) and 3342 for 1903 (long chunks): its outputs are off by
+// 2.0e-3 to 2.4e-3.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -1126,23 +1133,34 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
             if (CAREFUL) return kCare * __builtin_amdgcn_exp2f((x + off) * a.sl2);
             return __builtin_amdgcn_exp2f(fmaf(x, a.sl2, off));
         };
-        uint32_t pw[4];
+        uint32_t pw[4], rest[4];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int r = 0; r < 4; r += 2) pw[2 * b + r / 2] = pack_bf16(weight(s[b][r]), weight(s[b][r + 1]));
-        l = add_weights(pw[0], pw[1], l);
-        l = add_weights(pw[2], pw[3], l);
+            for (int r = 0; r < 4; r += 2) {
+                const float p0 = weight(s[b][r]), p1 = weight(s[b][r + 1]);
+                const uint32_t w = pack_bf16(p0, p1);
+                pw[2 * b + r / 2] = w;
+                rest[2 * b + r / 2] = pack_bf16(p0 - bf16_lo(w), p1 - bf16_hi(w));
+            }
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            l = add_weights(pw[k], pw[k + 1], l);
+            l = add_weights(rest[k], rest[k + 1], l);
+        }
         if (CAREFUL && masked) {
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
-                const uint32_t cur = pw[0];
+                const uint32_t cur = pw[0], more = rest[0];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) pw[k] = pw[k + 1];
+                for (int k = 0; k < 3; ++k) {
+                    pw[k] = pw[k + 1];
+                    rest[k] = rest[k + 1];
+                }
 #pragma unroll 1
                 for (int x = 0; x < 8; ++x) {
-                    const uint32_t both = __shfl(cur, col + 16 * (x >> 1));
-                    const float p = x & 1 ? bf16_hi(both) : bf16_lo(both);
+                    const uint32_t both = __shfl(cur, col + 16 * (x >> 1)), add = __shfl(more, col + 16 * (x >> 1));
+                    const float p = x & 1 ? bf16_hi(both) + bf16_hi(add) : bf16_lo(both) + bf16_lo(add);
                     const int tok = 16 * (j >> 1) + 4 * (x >> 1) + 2 * (j & 1) + (x & 1);
                     const bool vis = sees(a, pos, t0 + tok);
 #pragma unroll
@@ -1157,14 +1175,16 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
             }
             continue;
         }
-        const u32x4_t pf = {pw[0], pw[1], pw[2], pw[3]};
+        const u32x4_t pf = {pw[0], pw[1], pw[2], pw[3]}, rf = {rest[0], rest[1], rest[2], rest[3]};
         const int r = 4 * g + (col >> 2);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
             const int ch = 2 * d + ((col & 3) >> 1), by = 8 * (col & 1);
             const u32x2_t lo = ds_tr16(vt + r * RB + 16 * n_chunk<D>(r, ch) + by);
             const u32x2_t hi = ds_tr16(vt + (r + 16) * RB + 16 * n_chunk<D>(r, ch) + by);
-            acc[d] = mfma16(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, pf, acc[d]);
+            const u32x4_t v = {lo[0], lo[1], hi[0], hi[1]};
+            acc[d] = mfma16(v, pf, acc[d]);
+            acc[d] = mfma16(v, rf, acc[d]);
         }
     }
     if (CAREFUL) m *= a.sl2;

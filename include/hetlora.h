@@ -838,8 +838,9 @@ int32_t lora_kv_read(const lora_attn_launch_t* launch, const lora_kv_t* kv,
  *          16-byte aligned; may be NULL when info.workspace_floats is 0.
  *          Calls that overlap in time need one each
  * Scores and weights' sums are fp32; the weights enter the product with v as
- * bf16, and the same rounded weights are summed.  Results do not depend on
- * the launch order.  Errors: as lora_kv_write; LORA_ECAPACITY (workspace). */
+ * bf16, in two parts (16 bits) where a sequence has up to 16 rows to a kv head
+ * (q_len * n_heads / n_kv_heads), and the same rounded weights are summed.
+ * Results do not depend on the launch order.  Errors: as lora_kv_write; LORA_ECAPACITY (workspace). */
 int32_t lora_attn(const lora_attn_launch_t* launch, const lora_kv_t* kv,
                   const uint16_t* q, int64_t ldq, uint16_t* out, int64_t ldo,
                   float scale, float* workspace, int64_t workspace_floats,

@@ -1,10 +1,11 @@
 """Attention on the GPU at the edges of its numbers, against what the formula
 gives: NaN scores, windows longer than any sequence, scores far from zero, values
-near the largest."""
+near the largest, weights next to each other."""
 import numpy as np
 import pytest
 import torch
 
+import oracle
 from heterogeneous_adapter_batching_amd.attention import AttnBatch
 from test_gpu_attn import U, check, expected, make_cache, make_table, run_case, tokens
 
@@ -140,3 +141,25 @@ def test_values_near_the_largest_in_every_part(n, kv, every):
     q.fill_(1.0)
     out = attend(cache, table, q, kv, 0.125)
     check(out, *expected(cache, table, q, [n], [kv], 4, 0, 0, 0.125))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,kv,window", [(1, 200, 0), (4, 90, 0), (1, 3000, 0), (2, 900, 300)])
+def test_weights_of_few_rows_keep_16_bits(n, kv, window, dim, dtype):
+    """Up to 16 rows to a kv head: a weight enters the product in two bf16 parts, so
+    it is off by 2^-16 of it at most (2^-8 of what the first part leaves, which is
+    2^-8 of the weight).  The rest is as in the other tests' tolerance, and the
+    fp32 sum of kv products (2^-24 of the terms each)."""
+    cache, table, q = case(n, kv, dtype, 9, dim=dim)
+    scale = dim ** -0.5
+    out = torch.zeros_like(q)
+    batch = AttnBatch(cache, 4, window, 3).refresh([n], [kv], table)
+    assert batch.info.n_work[0] > 0 and sum(batch.info.n_work) == batch.info.n_work[0]
+    batch.attn(q, out, scale)
+    torch.cuda.synchronize()
+    k, v = tokens(cache, table, 0, kv)
+    want, spread, reach = oracle.attend_ref(q.double().cpu().numpy().reshape(n, 4, dim), k, v, kv, window, 3, scale)
+    slack = 2.0 ** -16 + 2 * ((dim + 4) * 2.0 ** -24 * reach[..., None] + 2.0 ** -20)
+    err = slack * spread * 1.01 + (kv + 64) * 2.0 ** -24 * (spread + np.abs(want))
+    check(out, want, err + U * (np.abs(want) + err))
