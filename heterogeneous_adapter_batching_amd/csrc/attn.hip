@@ -23,8 +23,8 @@
 // and the accumulator is rescaled only when a row's maximum grows by more than
 // 2^8 over the one in use: weights then stay below 2^8, far inside fp32 and
 // bf16, and the common tile pays neither the rescale nor a reduction over
-// lanes (16 prompts of up to 2048 tokens take 109 us with a rescale at any
-// growth, 104 so; 2 x 1024 tokens over 33k 1906 and 1852).
+// lanes (16 prompts of up to 2048 tokens take 113 us with a rescale at any
+// growth where they take 108 so; 2 x 1024 tokens over 33k 1972 and 1904).
 //
 // Weights are rounded to bf16 for the second product, and the rounded weights are
 // what the row's sum adds up, so the rounding cancels where few tokens dominate:
@@ -257,8 +257,8 @@ struct ReadArgs {
 // A workgroup finds the sequence of its first token by bisection, a lane goes on
 // from there, and every head's loads are under way before the first is stored.
 // Bound by memory: 48 sequences of up to 16384 tokens (8 kv heads, e4m3) take
-// 173 us, 5.6 TB/s.  One head a lane, with a bisection each, took 284; eight
-// heads 174; stores that stay in the caches 186.
+// 171 us, 5.7 TB/s; eight heads a lane 174, stores that stay in the caches 186.
+// (The first form, one head a lane with a bisection each, took 284.)
 constexpr int kReadHeads = 4;
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
@@ -448,7 +448,7 @@ struct Split {
 // loads and multiplies, the same took longer than the tile's softmax: a scalar
 // instruction that waits for another takes ten cycles.)  Otherwise every lane
 // looks up the page of its own row, tile by tile: 113 us where this takes 108 (16
-// prompts of up to 2048 tokens), 2.06 ms for 1.98 (2 x 1024 tokens over 33k).
+// prompts of up to 2048 tokens), 2007 for 1904 (2 x 1024 tokens over 33k).
 template <int D, bool E4M3, bool UNI, int NW, int ROWS, typename Tiles>
 struct Places {
     typedef Split<D, NW, ROWS> S;
@@ -803,9 +803,10 @@ struct AllTiles {
 // A wave has 32 rows.  A tile of 64 tokens of 128 elements is 32 MFMAs for it
 // (1024 cycles of the matrix unit) and about as many cycles of vector
 // instructions (64 elements: 512 and as many): bound by the matrix unit where
-// the two overlap.  2 x 1024 tokens of 64 heads over 33k (pair) take 1.81 ms,
-// 1230 TFLOP/s of the 1530 that a large library product reaches; 16 prompts of
-// up to 2048 tokens of 32 heads (wide) 102 us, 553 TFLOP/s of what rows see:
+// the two overlap.  2 x 1024 tokens of 64 heads over 33k (pair) take 1803 to 1907
+// us, by card: 1230 to 1165 TFLOP/s of the 1530 that a large library product
+// reaches; 16 prompts of up to 2048 tokens of 32 heads (wide) 101 to 109 us, 560
+// to 520 TFLOP/s of what rows see:
 // there an item has 7 tiles on average, and its start and end (work item, page
 // ids and queries one after the other, the waves' different last tiles, the
 // result) take as long as three.
@@ -1202,10 +1203,10 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
 // Every byte of the cache is used once: bound by memory, as far as the tiles in
 // flight cover its latency.  One token over each of 64 contexts of 256 to 2048
 // (32 kv heads, bf16) takes 146 us, 5.9 TB/s; over each of 32 contexts of 2048
-// to 32768 (8 kv heads of 8 query heads, e4m3) 122 us, 5.1 TB/s (136 with the
-// keys through LDS too, which leaves a compute unit two workgroups, not three);
-// over a single context of 776 10 us, two launches.  The registers are bounded
-// for the workgroups that the plan counts on.
+// to 32768 (8 kv heads of 8 query heads, e4m3) 123 us, 5.1 TB/s (136, in an
+// earlier form, with the keys through LDS too, which leaves a compute unit two
+// workgroups, not three); over a single context of 776 10 us, two launches.  The
+// registers are bounded for the workgroups that the plan counts on.
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_kernel(AttnArgs a) {
     constexpr int DB = D / 16, KS = D / 32, T = 32;

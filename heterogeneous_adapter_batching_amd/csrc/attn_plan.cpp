@@ -13,7 +13,10 @@
 namespace {
 
 constexpr int64_t kUnits = 256;  // compute units
-// Workgroups of each kernel that a compute unit holds, by registers.
+// Workgroups of each kernel that are counted to a compute unit: what its registers
+// leave room for.  (The bf16 wide form for 64-wide heads leaves room for three;
+// counting them changes nothing that was measured, 56.6 us for 16 prompts of up to
+// 2048 tokens either way.)
 int64_t resident(int kind, const lora_attn_shape_t& s) {
     if (kind != LORA_ATTN_NARROW) return kind == LORA_ATTN_WIDE ? 2 : 1;
     return s.head_dim == 64 ? 4 : s.kv_dtype == LORA_KV_E4M3 ? 3 : 2;
@@ -22,20 +25,27 @@ int64_t resident(int kind, const lora_attn_shape_t& s) {
 // chip's places once where that is kFullTiles at least, else up to kFullTiles
 // with one workgroup to a compute unit, and never under kMinTiles.  A split's
 // partial result and its part of the merge cost as much as a few tiles do: one
-// token over each of 8 windows of 4096 (8 kv heads) took 34.9 us in splits of 8
-// tiles and 32.4 in splits of 16; over a single context of 776, where most
-// compute units are idle, 14.7 us whole, 12.0 in splits of 8 and 10.6 in 4.
-// One token over each of 32 e4m3 contexts of up to 32768 took 126 us on three
-// places to a unit, 143 on two, 134 on four.
+// token over each of 8 windows of 4096 (8 kv heads) takes 31.9 us in splits of 8
+// tiles and 30.7 in splits of 16 or 32; over a single context of 776, where most
+// compute units are idle, 14.8 us whole, 11.9 in splits of 8 and 10.2 in 4.
+// One token over each of 32 e4m3 contexts of up to 32768 takes 123 us on three
+// places to a unit, 141 on two, 129 on four.
 constexpr int64_t kMinTiles = 4, kFullTiles = 16;
 int64_t tiles_per_split(int64_t tiles, int64_t places) {
     const int64_t once = (tiles + places - 1) / places, spread = (tiles + kUnits - 1) / kUnits;
     return once >= kFullTiles ? once : std::max(kMinTiles, std::min(kFullTiles, spread));
 }
 // Fewest tiles of a pair item.  It has one workgroup to a compute unit, whose
-// start nothing else covers, and 256 rows end later than 128 on a causal mask:
-// 16 prompts of up to 2048 tokens (32 heads) took 154 us on pair items and 124
-// on wide ones, 2 x 1024 tokens over 33k 1.90 and 1.98 ms.
+// start nothing else covers, and 256 rows end later than 128 on a causal mask;
+// its halves alternate without a gap once it runs.  us, pair and wide:
+//   head_dim, cache                  64 bf16  64 e4m3  128 bf16  128 e4m3
+//   16 prompts of up to 2048 tokens   87/57   105/68    125/104   149/106
+//   2 x 512 tokens over 6000         119/134  151/152   191/213   208/244
+//   the same in pages of 2           127/148  167/166   201/239   245/266
+//   2 x 512 tokens over 16000        292/336  369/381   471/561   570/613
+//   2 x 1024 tokens over 33k            -        -     1904/2300     -
+// (Where a chunk straddles the limit both kernels run, one after the other: over
+// 1800 tokens, 29 to 41 tiles, that takes 7 to 16 us more than either alone.)
 constexpr int32_t kPairTiles = 32;
 
 struct Tile {  // one row tile of one sequence before it is split

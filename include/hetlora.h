@@ -634,9 +634,10 @@ int32_t lora_pool_scatter(const uint16_t* src, uint16_t* pool, int64_t n,
 
 /* ------------------------------------------------------------------ paged cache and attention
  * What lies between the q/k/v projections' lora_apply and the o projection's
- * in a layer: the new tokens' k and v go into a paged cache (S-LoRA article,
- * "Unified Paging": a sequence of S tokens occupies pages of the pool beside
- * the adapters'), and the new tokens' queries attend over it.
+ * in a layer: the new tokens' k and v go into a paged cache, and the new
+ * tokens' queries attend over it.  (The S-LoRA article's "Unified Paging" has
+ * such pages in the adapters' pool.  Here k and v are device memory of the
+ * caller's, of any strides; lora_pool_* does not manage their pages.)
  *
  * A batch has n_seq sequences.  Sequence b brings q_len[b] new tokens (rows of
  * q, k, v and out, in order, sequence after sequence) and has kv_len[b] tokens
