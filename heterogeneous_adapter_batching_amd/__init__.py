@@ -15,7 +15,7 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhetlora.so")
 
-LORA_ABI_VERSION = 11
+LORA_ABI_VERSION = 12
 LORA_STATIC_SCRATCH_BYTES = 64 << 20
 LORA_MAX_RANK = 128
 LORA_MAX_PROJ = 8
@@ -144,6 +144,11 @@ class lora_kv_write_args_t(ctypes.Structure):
                 ("reserved", _i32)]
 
 
+class lora_head_norm_t(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("ld_q", _i64), ("ld_k", _i64), ("dtype", _i32), ("centred", _i32),
+                ("eps", _f32), ("reserved", _i32)]
+
+
 _sig = {
     "lora_abi_version": (_i32, []),
     "lora_status_string": (ctypes.c_char_p, [_i32]),
@@ -175,6 +180,8 @@ _sig = {
     "lora_attn_prepare": (_i32, [_P(lora_attn_shape_t), _i32, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
                                  _P(lora_attn_launch_t)]),
     "lora_kv_write": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _P(lora_kv_write_args_t), _vp]),
+    "lora_kv_write_norm": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _P(lora_kv_write_args_t),
+                                  _P(lora_head_norm_t), _vp]),
     "lora_kv_read": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _vp, _vp, _i64, _vp]),
     "lora_attn": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _vp, _i64, _vp, _i64, _f32, _vp, _i64, _vp]),
 }

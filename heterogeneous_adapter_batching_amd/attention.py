@@ -16,7 +16,7 @@ import numpy as np
 import torch
 
 from . import (LORA_BF16, LORA_ECAPACITY, LORA_F32, LORA_KV_BF16, LORA_KV_E4M3, LORA_OK, _lib, as_int32, check_status,
-               lora_attn_launch_t, lora_attn_shape_t, lora_kv_t, lora_kv_write_args_t)
+               lora_attn_launch_t, lora_attn_shape_t, lora_head_norm_t, lora_kv_t, lora_kv_write_args_t)
 from .session import HipEvent
 
 # staging buffers of batches let go, with the event of the copy that may be reading each
@@ -210,16 +210,40 @@ class AttnBatch:
         if have < rows:
             raise ValueError(f"{name} has {have} rows: the batch needs {rows}")
 
-    def prepare_write(self, k, v, q=None, q_out=None, rope=None, cache=None, stream=None):
+    def _norm(self, q_norm, k_norm, eps, centred):
+        """lora_head_norm_t of the weights, or None."""
+        if q_norm is None and k_norm is None:
+            return None
+        kinds = {torch.float32: LORA_F32, torch.bfloat16: LORA_BF16}
+        dtype = (k_norm if q_norm is None else q_norm).dtype
+        norm = lora_head_norm_t(dtype=kinds.get(dtype, -1), centred=bool(centred), eps=eps)
+        for name, w, heads in (("q", q_norm, self.n_heads), ("k", k_norm, self.shape.n_kv_heads)):
+            if w is None:
+                continue
+            if w.shape not in ((self.shape.head_dim,), (heads, self.shape.head_dim)) or w.stride(-1) != 1 or \
+                    w.dtype != dtype or dtype not in kinds or w.device != self.device:
+                raise ValueError(f"{name}_norm: [{self.shape.head_dim}] or [{heads}, {self.shape.head_dim}], "
+                                 f"float32 or bfloat16 like the other, on {self.device}")
+            setattr(norm, name, w.data_ptr())
+            setattr(norm, "ld_" + name, w.stride(0) if w.dim() == 2 and heads > 1 else 0)
+        return norm
+
+    def prepare_write(self, k, v, q=None, q_out=None, rope=None, cache=None, stream=None, *, q_norm=None, k_norm=None,
+                      eps=1e-6, centred=False):
         """k, v (and q): the projections' outputs, fp32 or bf16 [rows, heads *
         head_dim]; q_out: bf16, takes the turned q; rope: fp32 [positions,
-        rope_dim] (rope_table) or None.  Returns fn() that writes the batch's
-        new tokens into the cache."""
+        rope_dim] (rope_table) or None; q_norm, k_norm: weights of a norm of each
+        head before the turn, fp32 or bf16 [head_dim], or [heads, head_dim] with
+        weights for each head, or None for no norm (eps and centred: as in
+        lora_head_norm_t).  Returns fn() that writes the batch's new tokens into
+        the cache."""
         cache = self._check_cache(cache)
         if k.dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("k, v and q are float32 or bfloat16")
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out go together")
+        if q is None and q_norm is not None:
+            raise ValueError("q_norm without q")
         hk = self.shape.n_kv_heads
         have = [self._rows(k, hk, k.dtype, "k"), self._rows(v, hk, k.dtype, "v")]
         args = lora_kv_write_args_t(k=k.data_ptr(), v=v.data_ptr(), ldk=k.stride(0), ldv=v.stride(0),
@@ -232,14 +256,17 @@ class AttnBatch:
                 raise ValueError("rope: contiguous float32 [positions, rope_dim]")
             args.rope, args.rope_len, args.rope_dim = rope.data_ptr(), rope.shape[0], rope.shape[1]
         h, L, rows = self._use(stream).cuda_stream, self._launch, min(have)
-        kv_ref, arg_ref, ref, call = ctypes.byref(cache.c()), ctypes.byref(args), self._ref, _lib.lora_kv_write
+        kv_ref, arg_ref, ref = ctypes.byref(cache.c()), ctypes.byref(args), self._ref
+        norm = self._norm(q_norm, k_norm, eps, centred)
+        name = "lora_kv_write" if norm is None else "lora_kv_write_norm"
+        call, more = getattr(_lib, name), () if norm is None else (ctypes.byref(norm),)
 
         def run():
             self._need(rows, L.info.n_rows, "an input or q_out")
-            st = call(ref, kv_ref, arg_ref, h)
+            st = call(ref, kv_ref, arg_ref, *more, h)
             if st != LORA_OK:
-                check_status(st, "lora_kv_write")
-        run.keep = (k, v, q, q_out, rope, cache, args)
+                check_status(st, name)
+        run.keep = (k, v, q, q_out, rope, cache, args, q_norm, k_norm, norm)
         return run
 
     def prepare_read(self, k_out, v_out, cache=None, stream=None):
@@ -281,8 +308,8 @@ class AttnBatch:
         run.keep = (q, out, cache)
         return run
 
-    def write(self, k, v, q=None, q_out=None, rope=None, cache=None, stream=None):
-        self.prepare_write(k, v, q, q_out, rope, cache, stream)()
+    def write(self, k, v, q=None, q_out=None, rope=None, cache=None, stream=None, **norm):
+        self.prepare_write(k, v, q, q_out, rope, cache, stream, **norm)()
 
     def read(self, k_out, v_out, cache=None, stream=None):
         self.prepare_read(k_out, v_out, cache, stream)()

@@ -1,8 +1,8 @@
 // gfx950 kernels of the paged cache and the attention over it, and their C-ABI
 // launchers.
 //
-//   write  k, v of the batch's new tokens into the cache's pages, q and k turned
-//          by their positions' angles first
+//   write  k, v of the batch's new tokens into the cache's pages, q and k normed
+//          (if asked for) and turned by their positions' angles first
 //   read   a batch's cached tokens back as bf16
 //   attn   out_i = sum_j w_ij v_j, w_ij = exp(scale q_i . k_j) / sum, over the
 //          tokens that row i sees
@@ -91,7 +91,12 @@ struct WriteArgs {
     const int32_t* row_pos;
     const int32_t* row_slot;
     int32_t n_heads, n_vec, n_rows, rope_dim, rope_len;
+    const void *q_norm, *k_norm;  // weights, or none
+    int64_t ld_qn, ld_kn;
+    int32_t norm_f32;
+    float eps;
 };
+enum { kNoNorm, kRms, kCentred };
 
 template <bool F32>
 __device__ __forceinline__ f32x4_t load4(const void* p, int64_t i) {
@@ -112,6 +117,44 @@ __device__ __forceinline__ float e4m3_input(float x, float inv) {
     return fabsf(x) < INFINITY ? y : __builtin_nanf("");
 }
 
+// The sum of all elements of a head that lies in LPV lanes.
+template <int LPV>
+__device__ __forceinline__ float head_sum(f32x4_t x, f32x4_t y) {
+    x += y;
+    float t = (x[0] + x[1]) + (x[2] + x[3]);
+#pragma unroll
+    for (int o = 1; o < LPV; o <<= 1) t += __shfl_xor(t, o);
+    return t;
+}
+// x and y, a lane's elements of a head, become (x - m) / sqrt(mean((x - m)^2) + eps)
+// times their weights, m the head's mean (CENTRED) or zero.  The head is scaled
+// by the power of two of its largest element first, so that squares of the
+// largest and smallest elements stay in range; down to 2^-40 only, where the
+// squares are nothing beside eps (2^80 eps after the scaling) or still in range.
+// The sum under the root is at least the least normal number: a centred head of
+// equal elements is zero, though its scaled eps may have gone under.
+template <int LPV, bool CENTRED>
+__device__ __forceinline__ void norm_head(f32x4_t& x, f32x4_t& y, f32x4_t wx, f32x4_t wy, float eps) {
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(y[j])));
+#pragma unroll
+    for (int o = 1; o < LPV; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    const int t = min(max((int)(__float_as_uint(top) >> 23) - 127, -40), 126);
+    const float unit = __uint_as_float((uint32_t)(127 - t) << 23);
+    x *= unit;
+    y *= unit;
+    if (CENTRED) {
+        const float m = head_sum<LPV>(x, y) * (1.f / (8 * LPV));
+        x -= m;
+        y -= m;
+    }
+    const float sum = head_sum<LPV>(x * x, y * y) * (1.f / (8 * LPV)) + eps * unit * unit;
+    const float r = __builtin_amdgcn_rsqf(sum < 1.17549435e-38f ? 1.17549435e-38f : sum);  // NaN stays
+    x = x * r * wx;
+    y = y * r * wy;
+}
+
 // D/8 lanes take one head's vector, 8 elements each: the pair elements c and c +
 // rope_dim/2 of a turn lie in the same lane (4 and 4 of them), so nothing
 // crosses lanes but the maximum.  The turn is written without multiply-adds:
@@ -119,7 +162,7 @@ __device__ __forceinline__ float e4m3_input(float x, float inv) {
 // that codes next to a rounding border do not depend on how it is evaluated.
 // Bound by memory: 16 prompts of 128 to 2048 tokens (32 heads, fp32 in, e4m3
 // cache) take 96 us, 5.8 TB/s; 64 single tokens 4 us, a launch.
-template <int D, bool F32, bool E4M3>
+template <int D, bool F32, bool E4M3, int NORM>
 __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
     constexpr int LPV = D / 8, VPB = 256 / LPV;
     const int row = blockIdx.y + gridDim.y * blockIdx.z;
@@ -135,6 +178,15 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
     const void* src = is_q ? a.q : is_k ? a.k : a.v;
     const int64_t at = row * (is_q ? a.ldq : is_k ? a.ldk : a.ldv) + (int64_t)head * D;
     f32x4_t x = load4<F32>(src, at + c0), y = load4<F32>(src, at + c1);
+    if constexpr (NORM != kNoNorm) {
+        const void* w = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
+        if (w) {
+            const int64_t wat = head * (is_q ? a.ld_qn : a.ld_kn);
+            const f32x4_t wx = a.norm_f32 ? load4<true>(w, wat + c0) : load4<false>(w, wat + c0);
+            const f32x4_t wy = a.norm_f32 ? load4<true>(w, wat + c1) : load4<false>(w, wat + c1);
+            norm_head<LPV, NORM == kCentred>(x, y, wx, wy, a.eps);
+        }
+    }
     if (in_turn && (is_q || is_k) && pos >= 0 && pos < a.rope_len) {
 #pragma clang fp contract(off)
         const f32x4_t c = *reinterpret_cast<const f32x4_t*>(a.rope + (int64_t)pos * a.rope_dim + c0);
@@ -1292,12 +1344,20 @@ extern "C" int32_t lora_attn_prepare(const lora_attn_shape_t* shape, int32_t n_s
     return LORA_OK;
 }
 
-extern "C" int32_t lora_kv_write(const lora_attn_launch_t* L, const lora_kv_t* kv, const lora_kv_write_args_t* w,
-                                 void* hip_stream) {
+static int32_t write_rows(const lora_attn_launch_t* L, const lora_kv_t* kv, const lora_kv_write_args_t* w,
+                          const lora_head_norm_t* n, void* hip_stream) {
     const int32_t st = check_kv(L, kv);
     if (st != LORA_OK) return st;
     if (!w || (w->dtype != LORA_F32 && w->dtype != LORA_BF16)) return LORA_EINVAL;
     const lora_attn_info_t& I = L->info;
+    if (n) {
+        if ((n->dtype != LORA_F32 && n->dtype != LORA_BF16) || !(n->eps > 0.f) || !(n->eps <= 1.f)) return LORA_EINVAL;
+        if (n->centred != 0 && n->centred != 1) return LORA_EINVAL;
+        if ((!n->q && !n->k) || (n->q && !w->q)) return LORA_EINVAL;
+        for (const int64_t ld : {n->ld_q, n->ld_k})
+            if (ld != 0 && (ld < I.shape.head_dim || ld % 8 != 0)) return LORA_EINVAL;
+        if (!aligned16(n->q) || !aligned16(n->k)) return LORA_EINVAL;
+    }
     if (I.n_rows == 0) return LORA_OK;
     const int32_t d = I.shape.head_dim, hq = w->q ? I.shape.n_heads : 0, hk = I.shape.n_kv_heads;
     if (bad_rows(w->k, w->ldk, (int64_t)hk * d) || bad_rows(w->v, w->ldv, (int64_t)hk * d)) return LORA_EINVAL;
@@ -1325,18 +1385,40 @@ extern "C" int32_t lora_kv_write(const lora_attn_launch_t* L, const lora_kv_t* k
     a.n_rows = I.n_rows;
     a.rope_dim = w->rope_dim;
     a.rope_len = w->rope_len;
+    if (n) {
+        a.q_norm = n->q;
+        a.k_norm = n->k;
+        a.ld_qn = n->ld_q;
+        a.ld_kn = n->ld_k;
+        a.norm_f32 = n->dtype == LORA_F32;
+        a.eps = n->eps;
+    }
     typedef void (*fn_t)(WriteArgs);
-    static const fn_t fn[2][2][2] = {
-        {{kv_write_kernel<64, false, false>, kv_write_kernel<64, false, true>},
-         {kv_write_kernel<64, true, false>, kv_write_kernel<64, true, true>}},
-        {{kv_write_kernel<128, false, false>, kv_write_kernel<128, false, true>},
-         {kv_write_kernel<128, true, false>, kv_write_kernel<128, true, true>}}};
+#define AT_FORMS(d, norm)                                                                  \
+    {{kv_write_kernel<d, false, false, norm>, kv_write_kernel<d, false, true, norm>},      \
+     {kv_write_kernel<d, true, false, norm>, kv_write_kernel<d, true, true, norm>}}
+    static const fn_t fn[3][2][2][2] = {{AT_FORMS(64, kNoNorm), AT_FORMS(128, kNoNorm)},
+                                        {AT_FORMS(64, kRms), AT_FORMS(128, kRms)},
+                                        {AT_FORMS(64, kCentred), AT_FORMS(128, kCentred)}};
+#undef AT_FORMS
+    const int norm = !n ? kNoNorm : n->centred ? kCentred : kRms;
     const int vpb = 256 / (d / 8);
     const unsigned gy = (unsigned)(I.n_rows < 32768 ? I.n_rows : 32768);
     const dim3 grid((unsigned)((a.n_vec + vpb - 1) / vpb), gy, (unsigned)((I.n_rows + gy - 1) / gy));
-    const hipError_t e = launch(fn[d == 128][w->dtype == LORA_F32][kv->dtype == LORA_KV_E4M3], grid, dim3(256),
+    const hipError_t e = launch(fn[norm][d == 128][w->dtype == LORA_F32][kv->dtype == LORA_KV_E4M3], grid, dim3(256),
                                 reinterpret_cast<hipStream_t>(hip_stream), a);
     return e == hipSuccess ? LORA_OK : LORA_EHIP;
+}
+
+extern "C" int32_t lora_kv_write(const lora_attn_launch_t* L, const lora_kv_t* kv, const lora_kv_write_args_t* w,
+                                 void* hip_stream) {
+    return write_rows(L, kv, w, nullptr, hip_stream);
+}
+
+extern "C" int32_t lora_kv_write_norm(const lora_attn_launch_t* L, const lora_kv_t* kv, const lora_kv_write_args_t* w,
+                                      const lora_head_norm_t* norm, void* hip_stream) {
+    if (!norm) return LORA_EINVAL;
+    return write_rows(L, kv, w, norm, hip_stream);
 }
 
 extern "C" int32_t lora_kv_read(const lora_attn_launch_t* L, const lora_kv_t* kv, uint16_t* k_out, uint16_t* v_out,

@@ -73,7 +73,7 @@
 extern "C" {
 #endif
 
-#define LORA_ABI_VERSION 11
+#define LORA_ABI_VERSION 12
 #define LORA_MAX_RANK 128   /* ranks are 1..128                              */
 #define LORA_MAX_PROJ 8     /* projections per shrink/expand call            */
 #define LORA_MAX_RANGES 48  /* kernel variants in one plan                   */
@@ -822,6 +822,32 @@ typedef struct lora_kv_write_args {
  * LORA_ESHAPE (the cache is not the plan's shape; rope_dim), LORA_EHIP. */
 int32_t lora_kv_write(const lora_attn_launch_t* launch, const lora_kv_t* kv,
                       const lora_kv_write_args_t* args, void* hip_stream);
+
+/* Norms of queries and keys, for each head x of head_dim elements:
+ *   x <- (x - m) / sqrt(mean((x - m)^2) + eps) * weight,  m = mean(x) if centred, else 0
+ *   q, k     device weights of `dtype` (LORA_F32 or LORA_BF16), head_dim
+ *            elements, 16-byte aligned; NULL: q (or k) is not normed.  One of
+ *            them at least, q only where the write has a q
+ *   ld_q, ld_k  elements from a head's weights to the next head's, a multiple of
+ *            8, at least head_dim; 0: all heads have the same
+ *   eps      0 < eps <= 1 */
+typedef struct lora_head_norm {
+    const void* q;
+    const void* k;
+    int64_t ld_q;
+    int64_t ld_k;
+    int32_t dtype;
+    int32_t centred;            /* 0 or 1                                    */
+    float eps;
+    int32_t reserved;
+} lora_head_norm_t;
+
+/* lora_kv_write with the heads of q and k normed before they are turned.
+ * Everything is fp32 up to the one rounding at the end; v is as in
+ * lora_kv_write.  Errors: as lora_kv_write. */
+int32_t lora_kv_write_norm(const lora_attn_launch_t* launch, const lora_kv_t* kv,
+                           const lora_kv_write_args_t* args, const lora_head_norm_t* norm,
+                           void* hip_stream);
 
 /* Read all tokens of the batch's sequences back as bf16 (exact for both
  * cache types): k_out and v_out device bf16 [info.n_tokens] rows of n_kv_heads

@@ -39,11 +39,11 @@ from .segments import build_segments_ref, SegmentsRef, dense_offsets_ref, Segmen
 from .lora import gather_rows_ref, apply_ref, merge_ref, unmerge_ref, merge_dense_ref
 from .plan_check import check_plan_coverage
 from .mixture import mixture_ref
-from .attention import attend_ref, e4m3_nearest, e4m3_values, quantise_ref, turn_ref, visible_ref
+from .attention import attend_ref, e4m3_nearest, e4m3_values, norm_ref, quantise_ref, turn_ref, visible_ref
 
 __all__ = [
     "bf16_to_f64", "f64_to_bf16_rne", "build_segments_ref", "SegmentsRef",
     "dense_offsets_ref", "SegmentError", "gather_rows_ref", "apply_ref",
     "merge_ref", "unmerge_ref", "merge_dense_ref", "check_plan_coverage", "mixture_ref",
-    "attend_ref", "e4m3_nearest", "e4m3_values", "quantise_ref", "turn_ref", "visible_ref",
+    "attend_ref", "e4m3_nearest", "e4m3_values", "norm_ref", "quantise_ref", "turn_ref", "visible_ref",
 ]

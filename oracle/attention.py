@@ -56,6 +56,13 @@ def turn_ref(x, angles):
     return np.concatenate([a * cos - b * sin, a * sin + b * cos, x[..., 2 * half:]], -1)
 
 
+def norm_ref(x, weight, eps, centred):
+    """x [..., dim] normed along its last axis: (x - m) / sqrt(mean((x - m)^2) + eps) * weight."""
+    x = np.asarray(x, np.float64)
+    y = x - x.mean(-1, keepdims=True) if centred else x
+    return y / np.sqrt((y * y).mean(-1, keepdims=True) + eps) * weight
+
+
 def visible_ref(p, kv_len, window, sinks):
     """Tokens that the row at position p sees."""
     return [j for j in range(kv_len) if j <= p and (not window or j > p - window or j < sinks)]
