@@ -121,6 +121,11 @@ class lora_kv_t(ctypes.Structure):
                 ("page_stride", _i64), ("head_stride", _i64), ("token_stride", _i64)]
 
 
+class lora_kv_bounds_t(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("exps", _vp), ("n_pages", _i32), ("n_kv_heads", _i32), ("head_dim", _i32),
+                ("reserved", _i32)]
+
+
 class lora_attn_shape_t(ctypes.Structure):
     _fields_ = [("n_heads", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("page_tokens", _i32),
                 ("n_pages", _i32), ("kv_dtype", _i32), ("window", _i32), ("sinks", _i32)]
@@ -142,6 +147,20 @@ class lora_kv_write_args_t(ctypes.Structure):
     _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("ldq", _i64), ("ldk", _i64), ("ldv", _i64), ("rope", _vp),
                 ("q_out", _vp), ("ld_out", _i64), ("dtype", _i32), ("rope_len", _i32), ("rope_dim", _i32),
                 ("reserved", _i32)]
+
+
+class lora_sparse_shape_t(ctypes.Structure):
+    _fields_ = [("select", _i32), ("first", _i32), ("last", _i32), ("reserved", _i32)]
+
+
+class lora_sparse_info_t(ctypes.Structure):
+    _fields_ = [("shape", lora_sparse_shape_t), ("n_items", _i32), ("n_work", _i32), ("n_merge", _i32),
+                ("n_fresh", _i32), ("max_scored", _i32), ("item_tokens", _i32), ("part_rows", _i64),
+                ("off_items", _i64), ("off_work", _i64), ("off_merge", _i64), ("off_fresh", _i64)]
+
+
+class lora_sparse_launch_t(ctypes.Structure):
+    _fields_ = [("attn", lora_attn_launch_t), ("info", lora_sparse_info_t)]
 
 
 class lora_head_norm_t(ctypes.Structure):
@@ -182,7 +201,26 @@ _sig = {
     "lora_kv_write": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _P(lora_kv_write_args_t), _vp]),
     "lora_kv_write_norm": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _P(lora_kv_write_args_t),
                                   _P(lora_head_norm_t), _vp]),
+    "lora_kv_copy": (_i32, [_i32, _P(lora_kv_t), _P(lora_kv_t), _P(lora_kv_bounds_t), _P(lora_kv_bounds_t), _i32, _vp,
+                            _vp, _vp, _vp]),
+    "lora_kv_pages_create": (_i32, [_i32, _i32, _i32, _P(_vp)]),
+    "lora_kv_pages_destroy": (_i32, [_vp]),
+    "lora_kv_pages_append": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _P(_i32)]),
+    "lora_kv_pages_fork": (_i32, [_vp, _i32, _i32, _vp]),
+    "lora_kv_pages_truncate": (_i32, [_vp, _i32, _i32]),
+    "lora_kv_pages_free": (_i32, [_vp, _i32, _vp]),
+    "lora_kv_pages_compact": (_i32, [_vp, _i32, _vp, _vp, _vp, _P(_i32)]),
+    "lora_kv_pages_table": (_i32, [_vp, _i32, _vp, _i64, _vp, _vp, _P(_i32)]),
+    "lora_kv_pages_stats": (_i32, [_vp, _P(_i32), _P(_i32), _P(_i32)]),
     "lora_kv_read": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _vp, _vp, _i64, _vp]),
+    "lora_sparse_plan": (_i32, [_P(lora_attn_shape_t), _P(lora_sparse_shape_t), _i32, _vp, _vp, _vp, _vp, _i64, _vp,
+                                _i64, _P(lora_attn_info_t), _P(lora_sparse_info_t)]),
+    "lora_sparse_prepare": (_i32, [_P(lora_attn_shape_t), _P(lora_sparse_shape_t), _i32, _vp, _vp, _vp, _vp, _i64, _vp,
+                                   _i64, _vp, _vp, _P(lora_sparse_launch_t)]),
+    "lora_kv_bounds": (_i32, [_P(lora_sparse_launch_t), _P(lora_kv_t), _P(lora_kv_bounds_t), _vp]),
+    "lora_sparse_select": (_i32, [_P(lora_sparse_launch_t), _P(lora_kv_bounds_t), _vp, _i64, _vp, _vp, _i64, _vp]),
+    "lora_sparse_attn": (_i32, [_P(lora_sparse_launch_t), _P(lora_kv_t), _vp, _i64, _vp, _vp, _i64, _f32, _vp, _i64,
+                                _vp]),
     "lora_attn": (_i32, [_P(lora_attn_launch_t), _P(lora_kv_t), _vp, _i64, _vp, _i64, _f32, _vp, _i64, _vp]),
 }
 # HIP runtime calls the binding makes itself (events), resolved through the
@@ -367,6 +405,31 @@ def lora_attn_plan(shape, q_len, kv_len, block_table=None, staging_capacity=None
         return st, staging[:int(staging_capacity)], info
     _check(st, "lora_attn_plan")
     return staging[:int(info.n_staged)], info
+
+
+def lora_sparse_plan(shape, sparse, q_len, kv_len, block_table=None, bounded=None, staging_capacity=None, raw=False):
+    """Plan of a batch's attention and its sparse part (host).  Arguments as
+    lora_attn_plan; bounded: tokens of each sequence whose pages have bounds, or
+    None.  Returns (staging int32, attn info, sparse info), or (status, staging,
+    attn info, sparse info) with raw=True."""
+    ql, kl = as_int32(q_len, "q_len"), as_int32(kv_len, "kv_len")
+    assert ql.shape == kl.shape and ql.ndim == 1
+    tab = None if block_table is None else as_int32(block_table, "block_table")
+    bnd = None if bounded is None else as_int32(bounded, "bounded")
+    assert (tab is None or (tab.ndim == 2 and tab.shape[0] == ql.shape[0])) and (bnd is None or bnd.shape == ql.shape)
+    attn, info = lora_attn_info_t(), lora_sparse_info_t()
+    args = (ctypes.byref(shape), ctypes.byref(sparse), ql.shape[0], ql.ctypes.data, kl.ctypes.data, _ptr(bnd), _ptr(tab),
+            0 if tab is None else tab.shape[1])
+    out = ctypes.byref(attn), ctypes.byref(info)
+    if staging_capacity is None:
+        st = _lib.lora_sparse_plan(*args, None, 0, *out)
+        staging_capacity = int(attn.n_staged) if st in (LORA_OK, LORA_ECAPACITY) else 0
+    staging = np.zeros(max(1, int(staging_capacity)), np.int32)
+    st = _lib.lora_sparse_plan(*args, staging.ctypes.data, int(staging_capacity), *out)
+    if raw:
+        return st, staging[:int(staging_capacity)], attn, info
+    _check(st, "lora_sparse_plan")
+    return staging[:int(attn.n_staged)], attn, info
 
 
 def _ptr(a):

@@ -166,10 +166,7 @@ class AttnBatch:
         if not self._host.shape[0]:
             self._alloc(1 << 12, s)
         while True:
-            st = _lib.lora_attn_prepare(ctypes.byref(self.shape), ql.shape[0], ql.ctypes.data, kl.ctypes.data,
-                                        None if tab is None else tab.ctypes.data, 0 if tab is None else tab.shape[1],
-                                        self._host.data_ptr(), self._host.shape[0], self._dev.data_ptr(), h,
-                                        self._ref)
+            st = self._prepare(ql, kl, tab, self._host.data_ptr(), self._host.shape[0], self._dev.data_ptr(), h)
             if st != LORA_ECAPACITY or self._launch.info.n_staged <= self._host.shape[0]:
                 break
             self._alloc(int(self._launch.info.n_staged) * 2, s)
@@ -182,6 +179,11 @@ class AttnBatch:
             self._workspace = self._empty(int(self.info.workspace_floats), torch.float32, s)
         self._planned = True
         return self
+
+    def _prepare(self, ql, kl, tab, staging, capacity, dev, h):
+        return _lib.lora_attn_prepare(ctypes.byref(self.shape), ql.shape[0], ql.ctypes.data, kl.ctypes.data,
+                                      None if tab is None else tab.ctypes.data, 0 if tab is None else tab.shape[1],
+                                      staging, capacity, dev, h, self._ref)
 
     @property
     def info(self):

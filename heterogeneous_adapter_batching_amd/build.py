@@ -1,8 +1,7 @@
 """Build libhetlora.so in-tree for gfx950.
 
-host.cpp, pool.cpp and attn_plan.cpp (no HIP) are compiled by g++, kernels.hip
-and attn.hip by hipcc; hipcc links the shared library next to this file.  Every build compiles from
-scratch.
+The .cpp files (no HIP) are compiled by g++, the .hip files by hipcc; hipcc links
+the shared library next to this file.  Every build compiles from scratch.
 """
 import os
 import shutil
@@ -43,7 +42,7 @@ def build(verbose=False, out=LIB, defines=(), build_dir=None):
     out_dir = build_dir or os.path.join(HERE, "_build")
     os.makedirs(out_dir, exist_ok=True)
     dflags = [f"-D{d}" for d in defines]
-    host, kern = ("host", "pool", "attn_plan"), ("kernels", "attn")
+    host, kern = ("host", "pool", "attn_plan", "kv_pages"), ("kernels", "attn", "kv_copy", "sparse")
     cmds = [["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", f"-I{INCLUDE}", *dflags, "-c",
              os.path.join(CSRC, f"{n}.cpp"), "-o", os.path.join(out_dir, f"{n}.o")] for n in host]
     cmds += [[_hipcc(), *HIP_FLAGS, *dflags, "-c", os.path.join(CSRC, f"{n}.hip"), "-o",

@@ -35,6 +35,8 @@
 // gives 2.2e-3, for 0.2 us of a call.  In the wide one that takes 141 us where one
 // part takes 104 (prompts) and 3342 for 1903 (long chunks): its outputs are off by
 // 2.0e-3 to 2.4e-3.
+#include <algorithm>
+
 #include "kv_device.h"
 
 namespace {
@@ -315,7 +317,8 @@ struct AttnArgs {
     uint16_t* out;
     float* part;  // [n_kv_heads][part_rows][D] splits' outputs, then [n_kv_heads][part_rows][2] of (maximum, sum)
     int64_t ldq, ldo, part_rows;
-    int32_t n_seq, n_rows, max_kv, ld_table, group, window, sinks;
+    int64_t ld_table, table_head;  // from a sequence's page table to the next one's, and to its next kv head's
+    int32_t n_seq, n_rows, max_kv, group, window, sinks;
     uint32_t inv_group;  // 2^31 / group, rounded up
     float sl2;  // scale * log2 e
 };
@@ -336,7 +339,7 @@ __device__ __forceinline__ bool load_item(const AttnArgs& a, int i, int max_rows
     const int last_tok = token_of(a, it.lead + it.nrows - 1);
     if (!at_inside(&it, a.n_seq, a.n_rows, a.max_kv, a.group, max_rows, a.part_rows, last_tok, merge)) return false;
     it.p0 = it.kv - it.n_new + it.tok0;
-    it.table = a.table + (int64_t)it.seq * a.ld_table;
+    it.table = a.table + it.seq * a.ld_table;
     it.span = at_span(it.p0, it.p0 + last_tok, a.window, a.sinks);
     it.it0 = max(it.it0, 0);
     it.it1 = min(it.it1, merge ? it.nrows : at_span_tiles(it.span));
@@ -1210,6 +1213,7 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
     const int col = lane & 15, g = lane >> 4;
     Item it;
     if (!load_item(a, blockIdx.x / a.kv.n_kv_heads, AT_NARROW_ROWS, false, it)) return;
+    it.table += head * a.table_head;
 
     const int row = min(col, it.nrows - 1);
     const int pos = row_pos(a, it, row), p_lo = it.p0, p_hi = row_pos(a, it, it.nrows - 1);
@@ -1442,43 +1446,59 @@ extern "C" int32_t lora_kv_read(const lora_attn_launch_t* L, const lora_kv_t* kv
     return e == hipSuccess ? LORA_OK : LORA_EHIP;
 }
 
-extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, const uint16_t* q, int64_t ldq,
-                             uint16_t* out, int64_t ldo, float scale, float* workspace, int64_t workspace_floats,
-                             void* hip_stream) {
-    const int32_t st = check_kv(L, kv);
-    if (st != LORA_OK) return st;
+// What lora_attn and lora_sparse_attn check and hand to their kernels alike.
+static int32_t attn_args(const lora_attn_launch_t* L, const lora_kv_t* kv, const uint16_t* q, int64_t ldq, uint16_t* out,
+                         int64_t ldo, float scale, float* workspace, int64_t workspace_floats, AttnArgs& a) {
     const lora_attn_info_t& I = L->info;
     const int32_t d = I.shape.head_dim, hk = I.shape.n_kv_heads;
     const int64_t width = (int64_t)I.shape.n_heads * d;
-    if (I.n_rows == 0) return LORA_OK;
     if (bad_rows(q, ldq, width) || bad_rows(out, ldo, width)) return LORA_EINVAL;
     if (!(scale > 0.f) || !(scale * kLog2e < INFINITY)) return LORA_EINVAL;  // 0 * infinity is no score
     if (I.workspace_floats > 0) {
         if (workspace_floats < I.workspace_floats) return LORA_ECAPACITY;
         if (!workspace || !aligned16(workspace)) return LORA_EINVAL;
     }
-    for (const int64_t n : {I.n_work[0], I.n_work[1], I.n_work[2], I.n_merge})
-        if (n < 0 || n * hk > kMaxBlocks) return LORA_EINVAL;
-    AttnArgs a;
     memset(&a, 0, sizeof(a));
     a.kv = to_kv(*kv);
-    a.table = L->meta + I.off_table;
     a.q = q;
     a.out = out;
     a.part = workspace;
     a.ldq = ldq;
     a.ldo = ldo;
-    a.part_rows = I.part_rows;
-    a.n_seq = I.n_seq;
     a.n_rows = I.n_rows;
-    a.max_kv = I.max_kv;
-    a.ld_table = I.ld_table;
     a.group = I.shape.n_heads / hk;
     if (a.group > AT_MAX_GROUP) return LORA_ESHAPE;
     a.inv_group = (uint32_t)((((int64_t)1 << 31) + a.group - 1) / a.group);
+    a.sl2 = scale * kLog2e;
+    return LORA_OK;
+}
+static const struct {
+    void (*narrow[2][2])(AttnArgs);
+    void (*merge[2])(AttnArgs);
+} kNarrow = {{{attn_narrow_kernel<64, false>, attn_narrow_kernel<64, true>},
+              {attn_narrow_kernel<128, false>, attn_narrow_kernel<128, true>}},
+             {attn_merge_kernel<64>, attn_merge_kernel<128>}};
+
+extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, const uint16_t* q, int64_t ldq,
+                             uint16_t* out, int64_t ldo, float scale, float* workspace, int64_t workspace_floats,
+                             void* hip_stream) {
+    int32_t st = check_kv(L, kv);
+    if (st != LORA_OK) return st;
+    const lora_attn_info_t& I = L->info;
+    const int32_t d = I.shape.head_dim, hk = I.shape.n_kv_heads;
+    if (I.n_rows == 0) return LORA_OK;
+    AttnArgs a;
+    st = attn_args(L, kv, q, ldq, out, ldo, scale, workspace, workspace_floats, a);
+    if (st != LORA_OK) return st;
+    for (const int64_t n : {I.n_work[0], I.n_work[1], I.n_work[2], I.n_merge})
+        if (n < 0 || n * hk > kMaxBlocks) return LORA_EINVAL;
+    a.table = L->meta + I.off_table;
+    a.part_rows = I.part_rows;
+    a.n_seq = I.n_seq;
+    a.max_kv = I.max_kv;
+    a.ld_table = I.ld_table;
     a.window = I.shape.window;
     a.sinks = I.shape.sinks;
-    a.sl2 = scale * kLog2e;
     const hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
     const bool e4m3 = kv->dtype == LORA_KV_E4M3;
     typedef void (*fn_t)(AttnArgs);
@@ -1488,8 +1508,6 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     static const fn_t wide[2][2][2][2] = {
         {AT_FORMS(attn_wide_kernel, 64, false), AT_FORMS(attn_wide_kernel, 128, false)},
         {AT_FORMS(attn_wide_kernel, 64, true), AT_FORMS(attn_wide_kernel, 128, true)}};
-    static const fn_t narrow[2][2] = {{attn_narrow_kernel<64, false>, attn_narrow_kernel<64, true>},
-                                      {attn_narrow_kernel<128, false>, attn_narrow_kernel<128, true>}};
 #undef AT_FORMS
     // where Places can work with scalar page offsets: a step's rows in one page, 32-bit strides and scale offsets
     const bool uni = kv->page_tokens >= 64 / (d / 8) && kv->token_stride <= INT32_MAX / 64 &&
@@ -1498,14 +1516,50 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
         if (I.n_work[kind] == 0) continue;
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_work[kind]);
         const dim3 grid((unsigned)(I.n_work[kind] * hk)), block(kind == LORA_ATTN_PAIR ? 512 : 256);
-        const fn_t fn = kind == LORA_ATTN_NARROW ? narrow[d == 128][e4m3]
+        const fn_t fn = kind == LORA_ATTN_NARROW ? kNarrow.narrow[d == 128][e4m3]
                                                  : wide[kind == LORA_ATTN_PAIR][d == 128][e4m3][uni];
         if (launch(fn, grid, block, s, a) != hipSuccess) return LORA_EHIP;
     }
     if (I.n_merge > 0) {
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_merge);
         const dim3 grid((unsigned)(I.n_merge * hk));
-        if (launch(d == 128 ? attn_merge_kernel<128> : attn_merge_kernel<64>, grid, dim3(256), s, a) != hipSuccess)
+        if (launch(kNarrow.merge[d == 128], grid, dim3(256), s, a) != hipSuccess) return LORA_EHIP;
+    }
+    return LORA_OK;
+}
+
+extern "C" int32_t lora_sparse_attn(const lora_sparse_launch_t* L, const lora_kv_t* kv, const uint16_t* q, int64_t ldq,
+                                    const int32_t* selected, uint16_t* out, int64_t ldo, float scale, float* workspace,
+                                    int64_t workspace_floats, void* hip_stream) {
+    if (!L) return LORA_EINVAL;
+    int32_t st = check_kv(&L->attn, kv);
+    if (st == LORA_OK) st = check_sparse(*L);
+    if (st != LORA_OK) return st;
+    const lora_attn_info_t& I = L->attn.info;
+    const lora_sparse_info_t& S = L->info;
+    const int32_t d = I.shape.head_dim, hk = I.shape.n_kv_heads;
+    if (I.n_rows == 0) return LORA_OK;
+    if (!selected || ((uintptr_t)selected & 3u)) return LORA_EINVAL;
+    AttnArgs a;
+    st = attn_args(&L->attn, kv, q, ldq, out, ldo, scale, workspace, workspace_floats, a);
+    if (st != LORA_OK) return st;
+    for (const int64_t n : {S.n_work, S.n_merge})
+        if (n * hk > kMaxBlocks) return LORA_EINVAL;
+    // every row is a sequence of its own, with a page table for each kv head
+    a.table = selected;
+    a.table_head = S.shape.select;
+    a.ld_table = (int64_t)S.shape.select * hk;
+    a.part_rows = S.part_rows;
+    a.n_seq = I.n_rows;
+    a.max_kv = (int32_t)std::min((int64_t)S.shape.select * I.shape.page_tokens, (int64_t)I.max_kv);
+    const hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+    a.work = reinterpret_cast<const lora_attn_work_t*>(L->attn.meta + S.off_work);
+    if (launch(kNarrow.narrow[d == 128][kv->dtype == LORA_KV_E4M3], dim3((unsigned)(S.n_work * hk)), dim3(256), s, a) !=
+        hipSuccess)
+        return LORA_EHIP;
+    if (S.n_merge > 0) {
+        a.work = reinterpret_cast<const lora_attn_work_t*>(L->attn.meta + S.off_merge);
+        if (launch(kNarrow.merge[d == 128], dim3((unsigned)(S.n_merge * hk)), dim3(256), s, a) != hipSuccess)
             return LORA_EHIP;
     }
     return LORA_OK;

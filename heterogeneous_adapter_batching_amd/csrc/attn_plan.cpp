@@ -207,6 +207,88 @@ int32_t plan_impl(const lora_attn_shape_t& s, int32_t n_seq, const int32_t* q_le
     return LORA_OK;
 }
 
+// The sparse part behind a plan of the same batch.  Every new token is a sequence
+// of its own to the attention: the tokens of its pages on end, the own page's up
+// to itself, so that nothing is left to mask; its page table is what the
+// selection writes.
+int32_t sparse_impl(const lora_attn_shape_t& s, const lora_sparse_shape_t& sp, int32_t n_seq, const int32_t* q_len,
+                    const int32_t* kv_len, const int32_t* bounded, const int32_t* table, int64_t ld_table,
+                    int32_t* staging, int64_t capacity, lora_attn_info_t* attn, lora_sparse_info_t* info) {
+    const int32_t group = s.n_heads / s.n_kv_heads, page = s.page_tokens;
+    for (int32_t b = 0; b < n_seq && bounded; ++b)
+        if (bounded[b] < 0 || bounded[b] > kv_len[b]) return LORA_EINVAL;
+    lora_sparse_info_t out;
+    memset(&out, 0, sizeof(out));
+    out.shape = sp;
+    // tokens of an item: rows of their heads fill a tile of 16, and their scores fit
+    int32_t pad = 1;
+    while (pad < 16 && pad < group) pad *= 2;
+    const int64_t always = (int64_t)sp.first + sp.last;
+    for (int32_t b = 0; b < n_seq; ++b)
+        if (q_len[b] > 0 && kv_len[b] > 0) {
+            const int32_t pages = (kv_len[b] - 1) / page + 1;
+            if (pages > sp.select) out.max_scored = std::max(out.max_scored, (int32_t)(pages - always));
+        }
+    out.item_tokens = std::max(1, std::min(16 / pad, SP_ITEM_KEYS / std::max(1, out.max_scored)));
+
+    std::vector<lora_sparse_item_t> items;
+    std::vector<Tile> tiles;
+    std::vector<int32_t> fresh;
+    int32_t row = 0;
+    for (int32_t b = 0; b < n_seq; ++b) {
+        const int32_t p0 = kv_len[b] - q_len[b];
+        for (int32_t i = 0; i < q_len[b]; i += out.item_tokens)
+            items.push_back({b, row + i, std::min(out.item_tokens, q_len[b] - i), p0 + i});
+        for (int32_t i = 0; i < q_len[b]; ++i, ++row) {
+            const int32_t p = p0 + i;
+            const int32_t kv = p < 0 ? 0 : (std::min(p / page + 1, sp.select) - 1) * page + p % page + 1;
+            for (int32_t r = 0; r < group; r += AT_NARROW_ROWS) {
+                const int32_t n = std::min(group - r, (int32_t)AT_NARROW_ROWS);
+                tiles.push_back({{row, r, n, 0, 0, 1, -1, row, 1, kv, 0, r}, (kv + AT_TILE - 1) / AT_TILE});
+            }
+        }
+        const int32_t from = bounded ? bounded[b] : std::max(0, p0);
+        for (int32_t i = from / page; i < kv_len[b] / page; ++i) fresh.push_back(table[b * ld_table + i]);
+    }
+    std::vector<lora_attn_work_t> work, merge;
+    int64_t part_rows = 0;
+    split(tiles, kUnits * resident(LORA_ATTN_NARROW, s), s, work, merge, part_rows);
+    if (part_rows > INT32_MAX || items.size() > INT32_MAX || work.size() > INT32_MAX || merge.size() > INT32_MAX ||
+        fresh.size() > INT32_MAX)
+        return LORA_EINVAL;
+    out.n_items = (int32_t)items.size();
+    out.n_work = (int32_t)work.size();
+    out.n_merge = (int32_t)merge.size();
+    out.n_fresh = (int32_t)fresh.size();
+    out.part_rows = part_rows;
+    int64_t floats = part_rows * s.n_kv_heads * (s.head_dim + 2);
+    if (!sp_in_lds(out.max_scored, out.item_tokens)) {
+        const int64_t per = sp_keys(out.max_scored, out.item_tokens, s.n_kv_heads);
+        floats = std::max(floats, per * sp_slab(per, out.n_items));
+    }
+    int64_t off = attn->n_staged;
+    const auto place = [&off](int64_t n) {
+        const int64_t at = off;
+        off += (n + 3) / 4 * 4;
+        return at;
+    };
+    constexpr int64_t wi = sizeof(lora_attn_work_t) / sizeof(int32_t), si = sizeof(lora_sparse_item_t) / sizeof(int32_t);
+    out.off_items = place(si * out.n_items);
+    out.off_work = place(wi * out.n_work);
+    out.off_merge = place(wi * out.n_merge);
+    out.off_fresh = place(out.n_fresh);
+    attn->n_staged = off;
+    attn->workspace_floats = std::max(attn->workspace_floats, floats);
+    *info = out;
+    if (off > capacity) return LORA_ECAPACITY;
+    if (off > 0 && staging == nullptr) return LORA_EINVAL;
+    if (!items.empty()) memcpy(staging + out.off_items, items.data(), items.size() * sizeof(lora_sparse_item_t));
+    if (!work.empty()) memcpy(staging + out.off_work, work.data(), work.size() * sizeof(lora_attn_work_t));
+    if (!merge.empty()) memcpy(staging + out.off_merge, merge.data(), merge.size() * sizeof(lora_attn_work_t));
+    if (!fresh.empty()) memcpy(staging + out.off_fresh, fresh.data(), fresh.size() * sizeof(int32_t));
+    return LORA_OK;
+}
+
 }  // namespace
 
 extern "C" int32_t lora_attn_plan(const lora_attn_shape_t* shape, int32_t n_seq, const int32_t* q_len,
@@ -221,6 +303,26 @@ extern "C" int32_t lora_attn_plan(const lora_attn_shape_t* shape, int32_t n_seq,
     s.sinks = std::min(s.sinks, AT_MAX_TOKENS);
     try {
         return plan_impl(s, n_seq, q_len, kv_len, block_table, ld_table, staging, staging_capacity, info);
+    } catch (const std::bad_alloc&) {
+        return LORA_ENOMEM;
+    }
+}
+
+extern "C" int32_t lora_sparse_plan(const lora_attn_shape_t* shape, const lora_sparse_shape_t* sparse, int32_t n_seq,
+                                    const int32_t* q_len, const int32_t* kv_len, const int32_t* bounded,
+                                    const int32_t* block_table, int64_t ld_table, int32_t* staging,
+                                    int64_t staging_capacity, lora_attn_info_t* attn, lora_sparse_info_t* info) {
+    if (!shape || !sparse || !attn || !info) return LORA_EINVAL;
+    if (shape->window != 0 || shape->sinks != 0) return LORA_EINVAL;
+    if (sparse->first < 0 || sparse->last < 1 || sparse->select > AT_MAX_TOKENS ||
+        sparse->select < (int64_t)sparse->first + sparse->last)
+        return LORA_EINVAL;
+    const int32_t st = lora_attn_plan(shape, n_seq, q_len, kv_len, block_table, ld_table, staging, staging_capacity, attn);
+    if (st != LORA_OK && st != LORA_ECAPACITY) return st;
+    if (shape->page_tokens < SP_MIN_PAGE) return LORA_ESHAPE;
+    try {
+        return sparse_impl(*shape, *sparse, n_seq, q_len, kv_len, bounded, block_table, ld_table, staging,
+                           staging_capacity, attn, info);
     } catch (const std::bad_alloc&) {
         return LORA_ENOMEM;
     }

@@ -1,0 +1,209 @@
+// gfx950 kernel that copies pages of a paged cache, and its C entry point.
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "kv_device.h"
+
+namespace {
+
+// One cache's tensors: pages go from the first of each pair to the second.
+struct CopyCache {
+    const char *k, *v;
+    char *k_to, *v_to;
+    const uint8_t *k_scale, *v_scale;
+    uint8_t *k_scale_to, *v_scale_to;
+    const int8_t* codes;  // bounds, or none
+    int8_t* codes_to;
+    const uint8_t* exps;
+    uint8_t* exps_to;
+};
+struct CopyPair {
+    int32_t from, to, tokens;
+};
+// Caches and pairs travel in the launch's arguments: nothing is staged, and the
+// lists are free again when the call returns.
+constexpr int kCopyCaches = 16, kCopyPairs = 192;
+struct CopyArgs {
+    int64_t from_page, from_head, from_token, to_page, to_head, to_token;  // strides in bytes
+    int32_t n_heads, page_shift, token_blocks, bound_bytes;
+    CopyCache cache[kCopyCaches];
+    CopyPair pair[kCopyPairs];
+};
+static_assert(sizeof(CopyArgs) <= 4096, "a kernel's arguments are at most 4 KiB");
+
+// VPR lanes take a token of a head, 16 bytes each, and a workgroup 256 / VPR
+// tokens: of one head, or where a page holds fewer of several heads side by side.
+constexpr int kCopyHeads = 4;  // such steps to a workgroup: eight loads of a lane are under way
+template <int VPR, bool SCALES>
+__global__ __launch_bounds__(256) void kv_copy_kernel(CopyArgs a) {
+    constexpr int ROWS = 256 / VPR;
+    const CopyCache& c = a.cache[blockIdx.z];
+    const CopyPair p = a.pair[blockIdx.y];
+    const int shift = min(a.page_shift, __builtin_ctz(ROWS));  // tokens of a workgroup
+    const int token_block = blockIdx.x % a.token_blocks, head0 = blockIdx.x / a.token_blocks * (kCopyHeads * ROWS >> shift);
+    const int row = threadIdx.x / VPR, col = threadIdx.x % VPR;
+    const int token = (token_block << shift) + (row & ((1 << shift) - 1));
+    if (token < p.tokens) {
+        u32x4_t k[kCopyHeads], v[kCopyHeads];
+        uint8_t ks[kCopyHeads], vs[kCopyHeads];
+#pragma unroll
+        for (int i = 0; i < kCopyHeads; ++i) {
+            const int head = head0 + i * (ROWS >> shift) + (row >> shift);
+            if (head >= a.n_heads) break;
+            const int64_t at = p.from * a.from_page + head * a.from_head + token * a.from_token + 16 * col;
+            k[i] = *reinterpret_cast<const u32x4_t*>(c.k + at);
+            v[i] = *reinterpret_cast<const u32x4_t*>(c.v + at);
+            if (SCALES && col == 0) {
+                const int64_t s = (((int64_t)p.from * a.n_heads + head) << a.page_shift) + token;
+                ks[i] = c.k_scale[s];
+                vs[i] = c.v_scale[s];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kCopyHeads; ++i) {
+            const int head = head0 + i * (ROWS >> shift) + (row >> shift);
+            if (head >= a.n_heads) break;
+            const int64_t at = p.to * a.to_page + head * a.to_head + token * a.to_token + 16 * col;
+            *reinterpret_cast<u32x4_t*>(c.k_to + at) = k[i];
+            *reinterpret_cast<u32x4_t*>(c.v_to + at) = v[i];
+            if (SCALES && col == 0) {
+                const int64_t s = (((int64_t)p.to * a.n_heads + head) << a.page_shift) + token;
+                c.k_scale_to[s] = ks[i];
+                c.v_scale_to[s] = vs[i];
+            }
+        }
+    }
+    // bounds of a whole page, all heads': one workgroup of the page
+    if (c.codes && blockIdx.x == 0 && p.tokens >> a.page_shift) {
+        const int64_t bytes = (int64_t)a.n_heads * a.bound_bytes;
+        for (int64_t i = 16 * threadIdx.x; i < bytes; i += 16 * 256)
+            *reinterpret_cast<u32x4_t*>(c.codes_to + p.to * bytes + i) =
+                *reinterpret_cast<const u32x4_t*>(c.codes + p.from * bytes + i);
+        for (int h = threadIdx.x; h < a.n_heads; h += 256)
+            c.exps_to[(int64_t)p.to * a.n_heads + h] = c.exps[(int64_t)p.from * a.n_heads + h];
+    }
+}
+
+int32_t check_cache(const lora_kv_t& c, const lora_kv_t& like) {
+    if (!c.k || !c.v || !aligned16(c.k) || !aligned16(c.v) || c.n_pages < 1 || c.n_kv_heads < 1) return LORA_EINVAL;
+    if (c.dtype != LORA_KV_BF16 && c.dtype != LORA_KV_E4M3) return LORA_EINVAL;
+    if ((c.head_dim != 64 && c.head_dim != 128) || c.n_kv_heads > 65535) return LORA_ESHAPE;
+    if (c.page_tokens < 1 || c.page_tokens > 1024 || (c.page_tokens & (c.page_tokens - 1)) != 0) return LORA_ESHAPE;
+    if (c.dtype != like.dtype || c.head_dim != like.head_dim || c.n_kv_heads != like.n_kv_heads ||
+        c.page_tokens != like.page_tokens || c.n_pages != like.n_pages)
+        return LORA_ESHAPE;
+    const int64_t per = c.dtype == LORA_KV_E4M3 ? 16 : 8;
+    if (c.page_stride < 0 || c.head_stride < 0 || c.token_stride < 0 || c.page_stride % per || c.head_stride % per ||
+        c.token_stride % per)
+        return LORA_EINVAL;
+    if (c.dtype == LORA_KV_E4M3 && (!c.k_scale || !c.v_scale)) return LORA_EINVAL;
+    return LORA_OK;
+}
+int32_t check_bounds(const lora_kv_bounds_t& b, const lora_kv_t& c) {
+    if (!b.codes || !b.exps || !aligned16(b.codes)) return LORA_EINVAL;
+    if (b.n_pages != c.n_pages || b.n_kv_heads != c.n_kv_heads || b.head_dim != c.head_dim) return LORA_ESHAPE;
+    return LORA_OK;
+}
+bool same_strides(const lora_kv_t& a, const lora_kv_t& b) {
+    return a.page_stride == b.page_stride && a.head_stride == b.head_stride && a.token_stride == b.token_stride;
+}
+
+// Every page that is written is written once, and none is read that is also
+// written where source and destination share memory.
+int32_t check_pairs(int32_t n, const int32_t* from, const int32_t* to, const int32_t* tokens, int32_t from_pages,
+                    int32_t to_pages, int32_t page_tokens, bool shared) {
+    for (int32_t i = 0; i < n; ++i) {
+        if (from[i] < 0 || from[i] >= from_pages || to[i] < 0 || to[i] >= to_pages) return LORA_EPAGE;
+        if (tokens && (tokens[i] < 0 || tokens[i] > page_tokens)) return LORA_EINVAL;
+    }
+    if (n < 2 && !(n == 1 && shared)) return LORA_OK;
+    try {
+        std::vector<int32_t> written(to, to + n);
+        std::sort(written.begin(), written.end());
+        if (std::adjacent_find(written.begin(), written.end()) != written.end()) return LORA_EINVAL;
+        for (int32_t i = 0; i < n && shared; ++i)
+            if (std::binary_search(written.begin(), written.end(), from[i])) return LORA_EINVAL;
+    } catch (const std::bad_alloc&) {
+        return LORA_ENOMEM;
+    }
+    return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const lora_kv_t* to,
+                                const lora_kv_bounds_t* from_bounds, const lora_kv_bounds_t* to_bounds, int32_t n_pairs,
+                                const int32_t* from_page, const int32_t* to_page, const int32_t* tokens,
+                                void* hip_stream) {
+    if (n_caches < 1 || n_pairs < 0 || !from || (n_pairs > 0 && (!from_page || !to_page))) return LORA_EINVAL;
+    if (!to && to_bounds) return LORA_EINVAL;
+    if (to && (from_bounds != nullptr) != (to_bounds != nullptr)) return LORA_EINVAL;
+    const lora_kv_t* dst = to ? to : from;
+    const lora_kv_bounds_t* dst_bounds = to ? to_bounds : from_bounds;
+    bool shared = !to;
+    for (int32_t i = 0; i < n_caches; ++i) {
+        int32_t st = check_cache(from[i], from[0]);
+        if (st == LORA_OK && to) st = check_cache(to[i], to[0]);
+        if (st == LORA_OK && from_bounds) st = check_bounds(from_bounds[i], from[i]);
+        if (st == LORA_OK && dst_bounds) st = check_bounds(dst_bounds[i], dst[i]);
+        if (st != LORA_OK) return st;
+        shared = shared || from[i].k == dst[i].k || from[i].v == dst[i].v;
+    }
+    const lora_kv_t& c = from[0];
+    if (dst->dtype != c.dtype || dst->head_dim != c.head_dim || dst->n_kv_heads != c.n_kv_heads ||
+        dst->page_tokens != c.page_tokens)
+        return LORA_ESHAPE;
+    const int32_t st = check_pairs(n_pairs, from_page, to_page, tokens, c.n_pages, dst->n_pages, c.page_tokens, shared);
+    if (st != LORA_OK) return st;
+
+    const bool e4m3 = c.dtype == LORA_KV_E4M3;
+    const int es = e4m3 ? 1 : 2, vpr = c.head_dim * es / 16, rows = 256 / vpr;
+    const int32_t block = std::min(c.page_tokens, rows);  // tokens of a workgroup
+    const int32_t token_blocks = c.page_tokens / block, heads = kCopyHeads * rows / block;
+    CopyArgs a;
+    memset(&a, 0, sizeof(a));
+    a.n_heads = c.n_kv_heads;
+    a.page_shift = __builtin_ctz((unsigned)c.page_tokens);
+    a.token_blocks = token_blocks;
+    a.bound_bytes = 2 * c.head_dim;
+    typedef void (*fn_t)(CopyArgs);
+    const fn_t fn = e4m3 ? (vpr == 8 ? kv_copy_kernel<8, true> : kv_copy_kernel<4, true>)
+                         : (vpr == 16 ? kv_copy_kernel<16, false> : kv_copy_kernel<8, false>);
+    const unsigned gx = (unsigned)(token_blocks * ((c.n_kv_heads + heads - 1) / heads));
+    for (int32_t i = 0; i < n_caches;) {
+        int32_t n = 0;  // caches of one launch: those on end with the same strides
+        for (; i + n < n_caches && n < kCopyCaches && same_strides(from[i], from[i + n]) && same_strides(dst[i], dst[i + n]);
+             ++n) {
+            const lora_kv_t &f = from[i + n], &t = dst[i + n];
+            CopyCache& x = a.cache[n];
+            x = CopyCache{static_cast<const char*>(f.k), static_cast<const char*>(f.v), static_cast<char*>(t.k),
+                          static_cast<char*>(t.v), f.k_scale, f.v_scale, t.k_scale, t.v_scale, nullptr, nullptr, nullptr,
+                          nullptr};
+            if (from_bounds) {
+                x.codes = from_bounds[i + n].codes;
+                x.exps = from_bounds[i + n].exps;
+                x.codes_to = dst_bounds[i + n].codes;
+                x.exps_to = dst_bounds[i + n].exps;
+            }
+        }
+        a.from_page = from[i].page_stride * es;
+        a.from_head = from[i].head_stride * es;
+        a.from_token = from[i].token_stride * es;
+        a.to_page = dst[i].page_stride * es;
+        a.to_head = dst[i].head_stride * es;
+        a.to_token = dst[i].token_stride * es;
+        for (int32_t j = 0; j < n_pairs;) {
+            int32_t m = 0;
+            for (; j < n_pairs && m < kCopyPairs; ++j) {
+                const int32_t count = tokens ? tokens[j] : c.page_tokens;
+                if (count > 0) a.pair[m++] = CopyPair{from_page[j], to_page[j], count};
+            }
+            if (m > 0 && launch(fn, dim3(gx, (unsigned)m, (unsigned)n), dim3(256),
+                                reinterpret_cast<hipStream_t>(hip_stream), a) != hipSuccess)
+                return LORA_EHIP;
+        }
+        i += n;
+    }
+    return LORA_OK;
+}

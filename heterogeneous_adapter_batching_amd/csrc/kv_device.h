@@ -78,7 +78,7 @@ hipError_t launch(void (*fn)(A), dim3 grid, dim3 block, hipStream_t s, A& args) 
     return hipLaunchKernel(reinterpret_cast<const void*>(fn), grid, block, p, 0, s);
 }
 
-int32_t check_kv(const lora_attn_launch_t* L, const lora_kv_t* c) {
+inline int32_t check_kv(const lora_attn_launch_t* L, const lora_kv_t* c) {
     if (!L || !c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return LORA_EINVAL;
     const lora_attn_info_t& I = L->info;
     const lora_attn_shape_t& s = I.shape;
@@ -100,11 +100,29 @@ int32_t check_kv(const lora_attn_launch_t* L, const lora_kv_t* c) {
     if (s.kv_dtype == LORA_KV_E4M3 && (!c->k_scale || !c->v_scale)) return LORA_EINVAL;
     return LORA_OK;
 }
-Kv to_kv(const lora_kv_t& c) {
+// A plan that no cache is given with, and its sparse part.
+inline int32_t check_sparse(const lora_sparse_launch_t& L) {
+    const lora_attn_info_t& I = L.attn.info;
+    const lora_attn_shape_t& s = I.shape;
+    const lora_sparse_info_t& S = L.info;
+    if (I.n_seq < 0 || I.n_rows < 0 || I.n_tokens < 0 || (I.n_staged > 0 && !L.attn.meta) || !aligned16(L.attn.meta))
+        return LORA_EINVAL;
+    if ((s.head_dim != 64 && s.head_dim != 128) || s.n_kv_heads < 1 || s.n_heads < 1 || s.n_heads % s.n_kv_heads ||
+        s.n_heads / s.n_kv_heads > AT_MAX_GROUP || s.page_tokens < SP_MIN_PAGE ||
+        (s.page_tokens & (s.page_tokens - 1)) || s.n_pages < 1)
+        return LORA_ESHAPE;
+    if (s.window != 0 || s.sinks != 0 || S.shape.first < 0 || S.shape.last < 1 || S.shape.select > AT_MAX_TOKENS ||
+        S.shape.select < (int64_t)S.shape.first + S.shape.last)
+        return LORA_EINVAL;
+    if (S.n_items < 0 || S.n_work < 0 || S.n_merge < 0 || S.n_fresh < 0 || S.max_scored < 0 || S.item_tokens < 1)
+        return LORA_EINVAL;
+    return LORA_OK;
+}
+inline Kv to_kv(const lora_kv_t& c) {
     return Kv{static_cast<const char*>(c.k), static_cast<const char*>(c.v), c.k_scale, c.v_scale, c.page_stride,
               c.head_stride, c.token_stride, c.n_pages, __builtin_ctz((unsigned)c.page_tokens), c.n_kv_heads};
 }
-bool bad_rows(const void* p, int64_t ld, int64_t d) { return !p || !aligned16(p) || ld < d || ld % 8 != 0; }
+inline bool bad_rows(const void* p, int64_t ld, int64_t d) { return !p || !aligned16(p) || ld < d || ld % 8 != 0; }
 
 }  // namespace
 

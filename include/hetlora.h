@@ -691,6 +691,22 @@ typedef struct lora_kv {
     int64_t token_stride;
 } lora_kv_t;
 
+/* Bounds of the keys of a cache's pages (lora_kv_bounds), what pages are chosen
+ * by for a sparse attention.
+ *   codes  device int8 [n_pages][n_kv_heads][2][head_dim], 16-byte aligned: for
+ *          each element the largest key of the page, then the smallest (which is
+ *          no larger: scores are computed on that)
+ *   exps   device uint8 [n_pages][n_kv_heads]: exponents e biased by 127; a
+ *          bound is code * 2^e                                               */
+typedef struct lora_kv_bounds {
+    int8_t* codes;
+    uint8_t* exps;
+    int32_t n_pages;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t reserved;
+} lora_kv_bounds_t;
+
 /* What a plan is made for. */
 typedef struct lora_attn_shape {
     int32_t n_heads;            /* a multiple of n_kv_heads, at most 4096 of them */
@@ -872,6 +888,188 @@ int32_t lora_attn(const lora_attn_launch_t* launch, const lora_kv_t* kv,
                   const uint16_t* q, int64_t ldq, uint16_t* out, int64_t ldo,
                   float scale, float* workspace, int64_t workspace_floats,
                   void* hip_stream);
+
+/* ------------------------------------------------------------------ pages of the cache
+ * Copy of pages, within each cache or from one cache to another.  For every pair
+ * i, tokens [0, tokens[i]) of page from_page[i] of every cache from[c] go to
+ * page to_page[i] of to[c]: k, v and, of an e4m3 cache, their scales; what else
+ * the page holds stays.  All caches are copied with the same pairs (the layers
+ * of a model).
+ *   from, to  host [n_caches] of one shape and type (page_tokens, n_kv_heads,
+ *             head_dim, dtype; n_pages among from and among to); strides are
+ *             each cache's own.  to NULL: within each cache
+ *   from_bounds, to_bounds  host [n_caches]: bounds that go with a whole page
+ *             (tokens[i] == page_tokens), or NULL; to_bounds with to only
+ *   from_page, to_page, tokens  host int32 [n_pairs]; tokens NULL: whole pages.
+ *             They are read before the call returns.  A page is written by one
+ *             pair at most, and within a cache (to NULL, or of the same memory)
+ *             no page that is written is also read
+ * Caches of different memory must not overlap.  One launch for each 192 pairs of
+ * 16 caches with the same strides.  Errors: LORA_EINVAL, LORA_ESHAPE, LORA_EPAGE,
+ * LORA_ENOMEM, LORA_EHIP. */
+int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const lora_kv_t* to,
+                     const lora_kv_bounds_t* from_bounds, const lora_kv_bounds_t* to_bounds,
+                     int32_t n_pairs, const int32_t* from_page, const int32_t* to_page,
+                     const int32_t* tokens, void* hip_stream);
+
+/* Manager of a cache's pages (host state only, like lora_pool_*): which pages
+ * hold the tokens of sequences 0 .. n_seqs-1, shared pages counted.  All layers'
+ * caches have the same pages.  It only says what has to be copied (lora_kv_copy
+ * takes the lists as they are); the copies go to the stream before the work that
+ * the new tables are for.  Not thread-safe.  After an error nothing has changed. */
+typedef struct lora_kv_pages lora_kv_pages_t;
+
+/* Errors: LORA_EINVAL (null out, n_pages or n_seqs under 1, more than 2^31 - 1
+ * tokens in all), LORA_ESHAPE (page_tokens not a power of two up to 1024),
+ * LORA_ENOMEM. */
+int32_t lora_kv_pages_create(int32_t n_pages, int32_t page_tokens, int32_t n_seqs, lora_kv_pages_t** out);
+int32_t lora_kv_pages_destroy(lora_kv_pages_t* pages);
+
+/* Room for tokens[i] more tokens of sequence seqs[i], no sequence twice, all of
+ * them or none.  A sequence whose last page is not full and is shared gets a copy
+ * of its own of that page first: src, dst and len (host int32 [n] each) list the
+ * *n_copies of them, len the tokens to copy.  (Of sequences that share such a page
+ * and are all listed, the last keeps it.)  Errors: LORA_EINVAL (a sequence that is
+ * not there or listed twice, negative tokens, more than 2^30 of one),
+ * LORA_ECAPACITY (not enough free pages), LORA_ENOMEM. */
+int32_t lora_kv_pages_append(lora_kv_pages_t* pages, int32_t n, const int32_t* seqs, const int32_t* tokens,
+                             int32_t* src, int32_t* dst, int32_t* len, int32_t* n_copies);
+
+/* The n children, which hold no tokens, get the parent's tokens, in its pages.
+ * Errors: LORA_EINVAL (a sequence that is not there, a child that holds tokens, is
+ * the parent or is listed twice), LORA_ENOMEM. */
+int32_t lora_kv_pages_fork(lora_kv_pages_t* pages, int32_t parent, int32_t n, const int32_t* children);
+
+/* The sequence keeps its first `tokens` tokens; and the sequences keep none (one
+ * listed twice is freed once).  Pages that nobody else holds are free again.
+ * Errors: LORA_EINVAL (a sequence that is not there; more tokens than it has). */
+int32_t lora_kv_pages_truncate(lora_kv_pages_t* pages, int32_t seq, int32_t tokens);
+int32_t lora_kv_pages_free(lora_kv_pages_t* pages, int32_t n, const int32_t* seqs);
+
+/* Moves pages so that those in use are the cache's first: src, dst and len (host
+ * int32 [capacity]) list the *n_moves moves, len the tokens that a page holds; no
+ * page is both read and written.  Errors: LORA_EINVAL, LORA_ECAPACITY (*n_moves
+ * holds the number needed), LORA_ENOMEM. */
+int32_t lora_kv_pages_compact(lora_kv_pages_t* pages, int32_t capacity, int32_t* src, int32_t* dst,
+                              int32_t* len, int32_t* n_moves);
+
+/* Page table and lengths of the n sequences, as lora_attn_plan takes them: table
+ * host int32 [n][ld_table], zero past a sequence's pages, kv_len host int32 [n];
+ * *n_columns = the most pages of one.  Errors: LORA_EINVAL, LORA_ECAPACITY
+ * (n_columns > ld_table: only *n_columns is written). */
+int32_t lora_kv_pages_table(const lora_kv_pages_t* pages, int32_t n, const int32_t* seqs, int64_t ld_table,
+                            int32_t* table, int32_t* kv_len, int32_t* n_columns);
+
+/* Free pages, pages that several sequences hold, and one more than the last page
+ * in use (any may be NULL). */
+int32_t lora_kv_pages_stats(const lora_kv_pages_t* pages, int32_t* n_free, int32_t* n_shared, int32_t* end);
+
+/* ------------------------------------------------------------------ sparse attention
+ * Attention in which every new token sees the tokens of a few pages only, chosen
+ * for it and for each kv head by a cheap score, and of these the ones up to
+ * itself.  In three steps, after lora_kv_write:
+ *
+ *   bounds  of every page that the batch has completed: its largest and smallest
+ *           key, element by element (lora_kv_bounds)
+ *   select  the pages that each new token sees (lora_sparse_select): all of
+ *           them, c + 1, where c = p / page_tokens and c + 1 <= select; else the
+ *           pages i < first, the pages i > c - last (the token's own, c, among
+ *           them), and of the others the select - first - last of the highest
+ *           score, the earlier ones among equals.  Score of page i:
+ *               2^e_i max over the kv head's query heads h of
+ *                     sum over elements of max(r_h hi_i, r_h lo_i)
+ *           with hi_i, lo_i and e_i the codes and exponent of the page's bounds
+ *           and r_h = rint(q_h 2^-f) limited to +-127, NaN 0, f the least
+ *           exponent in [-100, 100] with |q| <= 127 * 2^f over the finite
+ *           elements of the kv head's query heads.  That is 2^-f times the most
+ *           that a key inside the bounds could score, up to the two roundings.
+ *           It is a whole number below 2^21 times a power of two: exact, so the
+ *           choice depends on no order of summation
+ *   attn    lora_attn's formula over the chosen pages (lora_sparse_attn)
+ *
+ * Bounds: e is the least in [-100, 100] with |x| <= 127 * 2^e over the page's
+ * finite keys of the head; a code is rint(x 2^-e) limited to +-127, x the largest
+ * (smallest) key of the element that is not NaN, 0 where all are.  Only pages of
+ * page_tokens cached tokens have bounds; the others are never scored. */
+
+typedef struct lora_sparse_shape {
+    int32_t select;             /* pages that a token sees; >= first + last  */
+    int32_t first;              /* pages that it always sees: the first ones, >= 0, */
+    int32_t last;               /* and the last ones, its own among them, >= 1 */
+    int32_t reserved;
+} lora_sparse_shape_t;
+
+/* One unit of selecting, for every kv head: tokens [row, row + n) of the batch's
+ * rows, of sequence seq, the first at position pos. */
+typedef struct lora_sparse_item {
+    int32_t seq;
+    int32_t row;
+    int32_t n;
+    int32_t pos;
+} lora_sparse_item_t;
+
+typedef struct lora_sparse_info {
+    lora_sparse_shape_t shape;
+    int32_t n_items;
+    int32_t n_work;             /* attention items (LORA_ATTN_NARROW)        */
+    int32_t n_merge;
+    int32_t n_fresh;            /* pages that lora_kv_bounds summarises      */
+    int32_t max_scored;         /* most pages scored for a token             */
+    int32_t item_tokens;        /* most tokens of an item                    */
+    int64_t part_rows;          /* rows of partial results per kv head       */
+    int64_t off_items;          /* lora_sparse_item_t [n_items]              */
+    int64_t off_work;           /* lora_attn_work_t [n_work]                 */
+    int64_t off_merge;          /* lora_attn_work_t [n_merge]                */
+    int64_t off_fresh;          /* [n_fresh] page ids                        */
+} lora_sparse_info_t;
+
+/* attn serves lora_kv_write, lora_kv_read and lora_attn too (layers whose
+ * attention is not sparse), on the same staging buffer and workspace. */
+typedef struct lora_sparse_launch {
+    lora_attn_launch_t attn;
+    lora_sparse_info_t info;
+} lora_sparse_launch_t;
+
+/* lora_attn_plan with a sparse plan behind it: attn->n_staged and
+ * attn->workspace_floats are those of both together.
+ *   bounded  host int32 [n_seq]: tokens of each sequence whose complete pages
+ *            have bounds already, 0 .. kv_len; NULL: those before the new tokens
+ *            (kv_len - q_len, not under 0)
+ * Errors: as lora_attn_plan; LORA_EINVAL also for a window or sinks, a select
+ * under first + last or over 2^30, a negative first, a last under 1, a bounded
+ * outside its range; LORA_ESHAPE for pages of under 16 tokens. */
+int32_t lora_sparse_plan(const lora_attn_shape_t* shape, const lora_sparse_shape_t* sparse, int32_t n_seq,
+                         const int32_t* q_len, const int32_t* kv_len, const int32_t* bounded,
+                         const int32_t* block_table, int64_t ld_table, int32_t* staging,
+                         int64_t staging_capacity, lora_attn_info_t* attn, lora_sparse_info_t* info);
+
+/* lora_sparse_plan, and the copy of the staging buffer, as lora_attn_prepare. */
+int32_t lora_sparse_prepare(const lora_attn_shape_t* shape, const lora_sparse_shape_t* sparse, int32_t n_seq,
+                            const int32_t* q_len, const int32_t* kv_len, const int32_t* bounded,
+                            const int32_t* block_table, int64_t ld_table, int32_t* staging,
+                            int64_t staging_capacity, void* dev_staging, void* hip_stream,
+                            lora_sparse_launch_t* out);
+
+/* Bounds of the plan's fresh pages (those complete pages of the batch's sequences
+ * that hold tokens from `bounded` on).  One launch.  Errors: as lora_kv_write. */
+int32_t lora_kv_bounds(const lora_sparse_launch_t* launch, const lora_kv_t* kv, const lora_kv_bounds_t* bounds,
+                       void* hip_stream);
+
+/* The pages that every row of the batch sees.
+ *   q         as in lora_attn
+ *   selected  device int32 [n_rows][n_kv_heads][select]: page ids in the order of
+ *             the sequence, -1 behind them (rows with p < 0: -1 throughout)
+ *   workspace  as in lora_attn
+ * Errors: as lora_attn (cache errors apart). */
+int32_t lora_sparse_select(const lora_sparse_launch_t* launch, const lora_kv_bounds_t* bounds,
+                           const uint16_t* q, int64_t ldq, int32_t* selected, float* workspace,
+                           int64_t workspace_floats, void* hip_stream);
+
+/* lora_attn over the pages selected (by lora_sparse_select on this plan, for this
+ * layer or for another one).  Errors: as lora_attn. */
+int32_t lora_sparse_attn(const lora_sparse_launch_t* launch, const lora_kv_t* kv, const uint16_t* q,
+                         int64_t ldq, const int32_t* selected, uint16_t* out, int64_t ldo, float scale,
+                         float* workspace, int64_t workspace_floats, void* hip_stream);
 
 #ifdef __cplusplus
 }

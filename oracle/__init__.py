@@ -40,10 +40,12 @@ from .lora import gather_rows_ref, apply_ref, merge_ref, unmerge_ref, merge_dens
 from .plan_check import check_plan_coverage
 from .mixture import mixture_ref
 from .attention import attend_ref, e4m3_nearest, e4m3_values, norm_ref, quantise_ref, turn_ref, visible_ref
+from .sparse import bounds_ref, code_ref, exponent_ref, scores_ref, select_ref
 
 __all__ = [
     "bf16_to_f64", "f64_to_bf16_rne", "build_segments_ref", "SegmentsRef",
     "dense_offsets_ref", "SegmentError", "gather_rows_ref", "apply_ref",
     "merge_ref", "unmerge_ref", "merge_dense_ref", "check_plan_coverage", "mixture_ref",
     "attend_ref", "e4m3_nearest", "e4m3_values", "norm_ref", "quantise_ref", "turn_ref", "visible_ref",
+    "bounds_ref", "code_ref", "exponent_ref", "scores_ref", "select_ref",
 ]
