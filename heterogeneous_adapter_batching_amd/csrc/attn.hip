@@ -986,13 +986,14 @@ __global__ __launch_bounds__(PAIR ? 512 : 256, 2) void attn_wide_kernel(AttnArgs
     x.finish(a, it, head, 32 * w + col < it.nrows, unit);
 }
 
-// Tile number -> first token of the tiles of 32 that one of the narrow kernel's
-// four waves takes.
-struct EveryFourth {
+// Tile number -> first token of the tiles of 32 that one of the SHARE waves which
+// take an item in turn gets.
+template <int SHARE>
+struct EveryNth {
     AtSpan span;
     int32_t first, last;
     __device__ __forceinline__ int operator()(int i) const {
-        const int x = min(first + 4 * i, last);
+        const int x = min(first + SHARE * i, last);
         return AT_TILE * at_span_tile(span, x >> 1) + 32 * (x & 1);
     }
 };
@@ -1066,15 +1067,98 @@ struct NarrowTile {
     }
 };
 
-template <int D, bool E4M3, bool CAREFUL>
+// A tile of 32 tokens for a wave that has its items to itself, in pages of 16 tokens
+// at least: keys and values go through LDS both, so that a row of a token goes to
+// lanes on end.  (The loads of NarrowTile give the cache that serves them 64
+// requests of 16 bytes where these give 16 of 64.  That is no matter where memory
+// is waited for; but of the pages that many tokens see, most come from the L2.)
+// The rows of half a tile lie in one page: one base, and the same offsets
+// throughout, but where the sequence ends.
+template <int D, bool E4M3>
+struct StagedTile {
+    static constexpr int ES = E4M3 ? 1 : 2, CPR = D * ES / 16, RPI = 64 / CPR, STEPS = 16 / RPI;
+    u32x4_t k[2][STEPS], v[2][STEPS];
+    uint32_t k_exp[2][STEPS], v_exp[2][STEPS];
+    int32_t page[2];
+    uint64_t at[2];   // of the half's first key from the head's first one, in bytes
+    uint32_t row[2][STEPS];  // the lane's rows, from there
+    int64_t sc[2];
+    static __device__ __forceinline__ int q_part(int k, int g) { return 32 * k + 8 * g; }
+
+    __device__ __forceinline__ void look_up(const Kv& c, const Item& it, int t0) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) page[b] = it.table[min(t0 + 16 * b, it.kv - 1) >> c.page_shift];
+    }
+    __device__ __forceinline__ void place(const Kv& c, const Item& it, int t0, int head) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int first = min(t0 + 16 * b, it.kv - 1), slot = first & ((1 << c.page_shift) - 1);
+            const int32_t pg = clamp_page(c, __builtin_amdgcn_readfirstlane(page[b]));
+            at[b] = (uint64_t)(ES * (pg * c.page_stride + slot * c.token_stride));
+            if constexpr (E4M3) sc[b] = scale_off(c, pg, head, slot);
+            // tokens past the end take the last one's place
+            const int last = it.kv - 1 - first;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) row[b][s] = min(RPI * s + (int)(threadIdx.x & 63) / CPR, last);
+        }
+    }
+    __device__ __forceinline__ void load(u32x4_t (&to)[2][STEPS], uint32_t (&exp)[2][STEPS], const char* from,
+                                         const uint8_t* scales, uint32_t row_bytes) {
+        const uint32_t col = 16 * ((threadIdx.x & 63) % CPR);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                to[b][s] = *reinterpret_cast<const u32x4_t*>(from + at[b] + (row[b][s] * row_bytes + col));
+                if constexpr (E4M3) exp[b][s] = scales[sc[b] + row[b][s]];
+            }
+    }
+    __device__ __forceinline__ void load_k(const Kv& c, int head) {
+        load(k, k_exp, c.k + ES * head * c.head_stride, c.k_scale, (uint32_t)c.token_stride * ES);
+    }
+    __device__ __forceinline__ void load_v(const Kv& c, int head) {
+        load(v, v_exp, c.v + ES * head * c.head_stride, c.v_scale, (uint32_t)c.token_stride * ES);
+    }
+    template <bool VALUES>
+    __device__ __forceinline__ static void store(const u32x4_t (&x)[2][STEPS], const uint32_t (&exp)[2][STEPS], char* to) {
+        const int col = (threadIdx.x & 63) % CPR;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int r = 16 * b + RPI * s + (threadIdx.x & 63) / CPR;
+                const auto put = [&](int c, u32x4_t y) {
+                    *reinterpret_cast<u32x4_t*>(to + r * (2 * D) + 16 * (VALUES ? n_chunk<D>(r, c) : k_chunk<D>(r, c))) = y;
+                };
+                if constexpr (E4M3) {
+                    put(2 * col, dequant8(u32x2_t{x[b][s][0], x[b][s][1]}, scale_of(exp[b][s])));
+                    put(2 * col + 1, dequant8(u32x2_t{x[b][s][2], x[b][s][3]}, scale_of(exp[b][s])));
+                } else {
+                    put(col, x[b][s]);
+                }
+            }
+    }
+    __device__ __forceinline__ void store_k(char* kt) const { store<false>(k, k_exp, kt); }
+    __device__ __forceinline__ void store_v(char* vt) const { store<true>(v, v_exp, vt); }
+    // operand k of keys 16 b .. 16 b + 15
+    __device__ __forceinline__ static u32x4_t key(const char* kt, int b, int k) {
+        const int lane = threadIdx.x & 63, r = 16 * b + (lane & 15);
+        return *reinterpret_cast<const u32x4_t*>(kt + r * (2 * D) + 16 * k_chunk<D>(r, 4 * k + (lane >> 4)));
+    }
+};
+
+// SHARE waves take the item's tiles in turn.  Tiles of a wave that is alone with its
+// item (SHARE 1) are StagedTiles: vt has the values, and behind them the keys.
+template <int D, bool E4M3, bool CAREFUL, int SHARE>
 __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, int pos, int p_lo, int p_hi, int head,
                                             int w, const u32x4_t (&qf)[D / 32], char* vt, f32x4_t (&acc)[D / 16],
                                             float& m, f32x4_t& l) {
     constexpr int RB = 2 * D, DB = D / 16, KS = D / 32, T = 32;
-    typedef NarrowTile<D, E4M3> Tile;
+    constexpr bool STAGED = SHARE == 1;
+    typedef typename std::conditional<STAGED, StagedTile<D, E4M3>, NarrowTile<D, E4M3>>::type Tile;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-    const int n = max(0, 2 * it.it1 - 2 * it.it0 - w + 3) >> 2;
-    const EveryFourth tile{it.span, 2 * it.it0 + w, 2 * it.it1 - 1};
+    const int n = max(0, 2 * it.it1 - 2 * it.it0 - w + SHARE - 1) / SHARE;
+    const EveryNth<SHARE> tile{it.span, 2 * it.it0 + w, 2 * it.it1 - 1};
 #pragma unroll
     for (int d = 0; d < DB; ++d) acc[d] = f32x4_t{};
     m = -INFINITY;
@@ -1090,16 +1174,26 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
     for (int i = 0; i < n; ++i) {
         const int t0 = tile(i);
         f32x4_t s[2] = {f32x4_t{}, f32x4_t{}};
+        if constexpr (STAGED) {
+            x.store_k(vt + T * RB);
+        } else {
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) s[b] = mfma16(Tile::part(x.k[b], x.k_exp[b], k), qf[k], s[b]);
+                for (int b = 0; b < 2; ++b) s[b] = mfma16(Tile::part(x.k[b], x.k_exp[b], k), qf[k], s[b]);
+        }
         x.store_v(vt);
         if (i + 1 < n) {
             x.place(a.kv, it, tile(i + 1), head);
             x.look_up(a.kv, it, tile(i + 2));
             x.load_k(a.kv, head);
             x.load_v(a.kv, head);
+        }
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) s[b] = mfma16(Tile::key(vt + T * RB, b, k), qf[k], s[b]);
         }
         if (none_sees(a, p_lo, p_hi, t0, t0 + T - 1)) continue;
 
@@ -1228,9 +1322,9 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
     float m;
     f32x4_t sum;
     float unit = 1.f;  // of the sum
-    if (narrow_pass<D, E4M3, false>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w], acc, m, sum)) {
+    if (narrow_pass<D, E4M3, false, 4>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w], acc, m, sum)) {
         unit = kCare;
-        narrow_pass<D, E4M3, true>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w], acc, m, sum);
+        narrow_pass<D, E4M3, true, 4>(a, it, pos, p_lo, p_hi, head, w, qf, lds[w], acc, m, sum);
     }
 
     // join the waves: each leaves its maximum, sum and [row][D] output in LDS
@@ -1275,6 +1369,56 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
             float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D + 2 * pr;
             ml[0] = top;
             ml[1] = total;
+        }
+    }
+}
+
+// The same with a wave to an item, for many items: those that are under way at
+// once are four times as many, so that neighbours which see the same pages (of a
+// sparse attention) find them in the caches more often, and nothing is joined.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_solo_kernel(AttnArgs a, int32_t n_items) {
+    constexpr int DB = D / 16, KS = D / 32, T = 32;
+    __shared__ __align__(16) char lds[4][2 * T * 2 * D];
+    const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
+    const int col = lane & 15, g = lane >> 4, item = 4 * (blockIdx.x / a.kv.n_kv_heads) + w;
+    Item it;
+    if (item >= n_items || !load_item(a, item, AT_NARROW_ROWS, false, it)) return;
+    it.table += head * a.table_head;
+
+    const int row = min(col, it.nrows - 1);
+    const int pos = row_pos(a, it, row), p_lo = it.p0, p_hi = row_pos(a, it, it.nrows - 1);
+    u32x4_t qf[KS];
+    const uint16_t* q = a.q + row_off(a, it, row, head, a.ldq, D);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const u32x4_t*>(q + StagedTile<D, E4M3>::q_part(k, g));
+    f32x4_t acc[DB];
+    float m;
+    f32x4_t sum;
+    float unit = 1.f;  // of the sum
+    if (narrow_pass<D, E4M3, false, 1>(a, it, pos, p_lo, p_hi, head, 0, qf, lds[w], acc, m, sum)) {
+        unit = kCare;
+        narrow_pass<D, E4M3, true, 1>(a, it, pos, p_lo, p_hi, head, 0, qf, lds[w], acc, m, sum);
+    }
+    float l = sum[0] + __shfl_xor(sum[0], 16);
+    l += __shfl_xor(l, 32);
+    const float own = reciprocal(l);
+    if (col >= it.nrows) return;
+    if (it.nsplits == 1) {
+        uint16_t* dst = a.out + row_off(a, it, row, head, a.ldo, D) + 4 * g;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+            const f32x4_t o = acc[d] * own;
+            *reinterpret_cast<u32x2_t*>(dst + 16 * d) = u32x2_t{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+        }
+    } else {
+        const int64_t pr = head * a.part_rows + it.part + row;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) *reinterpret_cast<f32x4_t*>(a.part + pr * D + 16 * d + 4 * g) = acc[d] * own;
+        if (g == 0) {
+            float* ml = a.part + (int64_t)a.kv.n_kv_heads * a.part_rows * D + 2 * pr;
+            ml[0] = m;
+            ml[1] = l / unit;
         }
     }
 }
@@ -1528,6 +1672,8 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     return LORA_OK;
 }
 
+constexpr int64_t kSoloItems = 2048;
+
 extern "C" int32_t lora_sparse_attn(const lora_sparse_launch_t* L, const lora_kv_t* kv, const uint16_t* q, int64_t ldq,
                                     const int32_t* selected, uint16_t* out, int64_t ldo, float scale, float* workspace,
                                     int64_t workspace_floats, void* hip_stream) {
@@ -1554,9 +1700,20 @@ extern "C" int32_t lora_sparse_attn(const lora_sparse_launch_t* L, const lora_kv
     a.max_kv = (int32_t)std::min((int64_t)S.shape.select * I.shape.page_tokens, (int64_t)I.max_kv);
     const hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
     a.work = reinterpret_cast<const lora_attn_work_t*>(L->attn.meta + S.off_work);
-    if (launch(kNarrow.narrow[d == 128][kv->dtype == LORA_KV_E4M3], dim3((unsigned)(S.n_work * hk)), dim3(256), s, a) !=
-        hipSuccess)
+    const bool e4m3 = kv->dtype == LORA_KV_E4M3;
+    // (a page's rows lie within 32 bits of its first one)
+    if ((int64_t)S.n_work * hk >= kSoloItems && kv->token_stride <= INT32_MAX / 2048) {
+        typedef void (*fn_t)(AttnArgs, int32_t);
+        static const fn_t solo[2][2] = {{attn_solo_kernel<64, false>, attn_solo_kernel<64, true>},
+                                        {attn_solo_kernel<128, false>, attn_solo_kernel<128, true>}};
+        int32_t n = S.n_work;
+        void* p[] = {&a, &n};
+        if (hipLaunchKernel(reinterpret_cast<const void*>(solo[d == 128][e4m3]), dim3((unsigned)((n + 3) / 4 * hk)),
+                            dim3(256), p, 0, s) != hipSuccess)
+            return LORA_EHIP;
+    } else if (launch(kNarrow.narrow[d == 128][e4m3], dim3((unsigned)(S.n_work * hk)), dim3(256), s, a) != hipSuccess) {
         return LORA_EHIP;
+    }
     if (S.n_merge > 0) {
         a.work = reinterpret_cast<const lora_attn_work_t*>(L->attn.meta + S.off_merge);
         if (launch(kNarrow.merge[d == 128], dim3((unsigned)(S.n_merge * hk)), dim3(256), s, a) != hipSuccess)

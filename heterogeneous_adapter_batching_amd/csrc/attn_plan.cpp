@@ -48,6 +48,9 @@ int64_t tiles_per_split(int64_t tiles, int64_t places) {
 // 1800 tokens, 29 to 41 tiles, that takes 7 to 16 us more than either alone.)
 constexpr int32_t kPairTiles = 32;
 
+// Items of a selection, of all kv heads together, that are wanted at least.
+constexpr int64_t kSelectItems = 2 * kUnits;
+
 struct Tile {  // one row tile of one sequence before it is split
     lora_attn_work_t work;
     int32_t tiles;
@@ -220,16 +223,21 @@ int32_t sparse_impl(const lora_attn_shape_t& s, const lora_sparse_shape_t& sp, i
     lora_sparse_info_t out;
     memset(&out, 0, sizeof(out));
     out.shape = sp;
-    // tokens of an item: rows of their heads fill a tile of 16, and their scores fit
-    int32_t pad = 1;
+    int32_t pad = 1;  // rows of a token in a tile of 16
     while (pad < 16 && pad < group) pad *= 2;
+    int64_t rows = 0;
     const int64_t always = (int64_t)sp.first + sp.last;
     for (int32_t b = 0; b < n_seq; ++b)
         if (q_len[b] > 0 && kv_len[b] > 0) {
             const int32_t pages = (kv_len[b] - 1) / page + 1;
             if (pages > sp.select) out.max_scored = std::max(out.max_scored, (int32_t)(pages - always));
+            rows += q_len[b];
         }
-    out.item_tokens = std::max(1, std::min(16 / pad, SP_ITEM_KEYS / std::max(1, out.max_scored)));
+    // Tokens of an item: their rows fill the tiles that are scored at once, their
+    // scores fit LDS, and there are items enough to fill the chip.
+    const int64_t spread = rows * s.n_kv_heads / kSelectItems;
+    out.item_tokens = (int32_t)std::max<int64_t>(
+        1, std::min({(int64_t)(16 * SP_ROW_TILES / pad), (int64_t)(SP_LDS_KEYS / std::max(1, out.max_scored)), spread}));
 
     std::vector<lora_sparse_item_t> items;
     std::vector<Tile> tiles;
@@ -263,7 +271,7 @@ int32_t sparse_impl(const lora_attn_shape_t& s, const lora_sparse_shape_t& sp, i
     out.part_rows = part_rows;
     int64_t floats = part_rows * s.n_kv_heads * (s.head_dim + 2);
     if (!sp_in_lds(out.max_scored, out.item_tokens)) {
-        const int64_t per = sp_keys(out.max_scored, out.item_tokens, s.n_kv_heads);
+        const int64_t per = (int64_t)out.max_scored * s.n_kv_heads;
         floats = std::max(floats, per * sp_slab(per, out.n_items));
     }
     int64_t off = attn->n_staged;

@@ -68,17 +68,14 @@ AT_FN int at_inside(const lora_attn_work_t* w, int32_t n_seq, int32_t n_rows, in
 // ------------------------------------------------------------------ sparse attention
 #define SP_MIN_PAGE 16       // fewest tokens of a page: under that its bounds are as much as its keys
 #define SP_EXP 100           // exponents of bounds are within +-SP_EXP
-// Keys (scores) that a selecting workgroup holds in LDS: 48 KB of them, three
-// workgroups to a compute unit.  An item has as many tokens as fit a third of it.
+// Keys (scores) that a selecting workgroup holds in LDS at most, and tiles of 16
+// rows (query heads of its tokens) that it scores at once.
 #define SP_LDS_KEYS 12288
-#define SP_ITEM_KEYS 4096
+#define SP_ROW_TILES 2
 #define SP_SLAB_KEYS (1 << 24)  // keys in memory at once, where LDS does not hold one token's
 
 AT_FN int sp_in_lds(int32_t max_scored, int32_t item_tokens) { return (int64_t)max_scored * item_tokens <= SP_LDS_KEYS; }
-// keys of one item, and items of one launch, where they go through memory
-AT_FN int64_t sp_keys(int32_t max_scored, int32_t item_tokens, int32_t heads) {
-    return (int64_t)max_scored * item_tokens * heads;
-}
+// items of one launch, where the keys of each (of one token, all heads') go through memory
 AT_FN int64_t sp_slab(int64_t per_item, int64_t n_items) {
     const int64_t fit = SP_SLAB_KEYS / per_item;
     return fit < 1 ? 1 : fit < n_items ? fit : n_items;

@@ -185,7 +185,7 @@ struct SelectArgs {
     const lora_sparse_item_t* items;
     const int32_t* table;
     int32_t* selected;
-    uint32_t* keys;  // of one launch's items, where they do not fit LDS: [item][token][head][max_scored]
+    uint32_t* keys;  // of one launch's items, where they do not fit LDS: [item][head][max_scored]
     int64_t ldq;
     int32_t n_pages, page_shift, n_kv_heads, group, pad_shift;  // 2^pad_shift rows to a token
     int32_t n_seq, n_rows, ld_table, select, first, last, max_scored, item_tokens;
@@ -221,16 +221,18 @@ struct Rows16 {
     s32x4_t up[S], down[S];  // max(r, 0) and min(r, 0) of row lane % 16: elements 64 s + 16 (lane / 16) + 0..15
 
     __device__ __forceinline__ static int heads(const SelectArgs& a) { return (a.group + 15) >> 4; }  // tiles of a token
-    __device__ __forceinline__ static const uint16_t* row(const SelectArgs& a, const SelectItem& it, int head, int tile) {
-        const int r = threadIdx.x & 15, token = min(r >> a.pad_shift, it.n - 1);
+    __device__ __forceinline__ static const uint16_t* row(const SelectArgs& a, const SelectItem& it, int head, int tile,
+                                                          int first) {
+        const int r = threadIdx.x & 15, token = min(first + (r >> a.pad_shift), it.n - 1);
         const int h = min(16 * tile + (r & ((1 << a.pad_shift) - 1)), a.group - 1);  // the last head again changes no maximum
         return a.q + (it.row + token) * a.ldq + ((int64_t)head * a.group + h) * D + 16 * (threadIdx.x >> 4 & 3);
     }
-    __device__ __forceinline__ void load(const SelectArgs& a, const SelectItem& it, int head, int tile) {
+    // tokens from `first` on of the item, heads of `tile`
+    __device__ __forceinline__ void load(const SelectArgs& a, const SelectItem& it, int head, int tile, int first) {
         uint32_t top = 0;
         u32x4_t x[2 * S];
         const auto read = [&](int t) {
-            const uint16_t* q = row(a, it, head, t);
+            const uint16_t* q = row(a, it, head, t, first);
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 x[2 * s] = *reinterpret_cast<const u32x4_t*>(q + 64 * s);
@@ -296,52 +298,91 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 // Keys of the item's scored pages, tiles of 16 pages from `tile` on in steps of
-// `step`; put(token, page, key, again) takes them, `again` where an earlier tile
+// `step`, for up to R tiles of rows at once; the bounds of AHEAD tiles are under
+// way.  put(token, page, key, again) takes the keys, `again` where an earlier tile
 // of heads has given one.  The same lane gives a page's key every time.
-template <int D, typename Put>
+template <int D, int R, int AHEAD, typename Put>
 __device__ __forceinline__ void score_pages(const SelectArgs& a, const SelectItem& it, int head, int tile, int step,
                                             int end, Put put) {
-    const int col = threadIdx.x & 15, g = threadIdx.x >> 4 & 3, count = it.scored(a, it.n - 1);
+    const int col = threadIdx.x & 15, g = threadIdx.x >> 4 & 3, count = it.scored(a, it.n - 1), per = 16 >> a.pad_shift;
     const int32_t* table = it.table + a.first;
     for (int t = 0; t < Rows16<D>::heads(a); ++t) {
-        Rows16<D> r;
-        r.load(a, it, head, t);
         if (tile >= end) return;
-        Pages16<D> next;
-        next.load(a, table[min(16 * tile + col, count - 1)], head);
-        int32_t page = table[min(16 * (tile + step) + col, count - 1)];
-        for (int i = tile; i < end; i += step) {
-            const Pages16<D> p = next;
-            if (i + step < end) {
-                next.load(a, page, head);
-                page = table[min(16 * (i + 2 * step) + col, count - 1)];
-            }
-            const s32x4_t x = p.score(r);
-            const float unit = scale_of(p.exp);
-            const int at = 16 * i + col;
-            const auto give = [&](int token, int score) {
-                if (token < it.n && at < count) put(token, at, key_of((float)score * unit), t > 0);
-            };
-            // rows 4 g + 0..3 of page `col` are here
-            if (a.pad_shift == 0) {
-                for (int j = 0; j < 4; ++j) give(4 * g + j, x[j]);
-            } else if (a.pad_shift == 1) {
-                give(2 * g, max(x[0], x[1]));
-                give(2 * g + 1, max(x[2], x[3]));
-            } else {
-                int m = max(max(x[0], x[1]), max(x[2], x[3]));
-                if (a.pad_shift > 2) m = max(m, __shfl_xor(m, 16));
-                if (a.pad_shift > 3) m = max(m, __shfl_xor(m, 32));
-                if ((g & ((1 << (a.pad_shift - 2)) - 1)) == 0) give(g >> (a.pad_shift - 2), m);
+        Pages16<D> p[AHEAD];
+        int32_t page[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) page[j] = table[min(16 * (tile + j * step) + col, count - 1)];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (tile + j * step < end) p[j].load(a, page[j], head);
+            page[j] = table[min(16 * (tile + (j + AHEAD) * step) + col, count - 1)];
+        }
+        Rows16<D> r[R];
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+            if (x == 0 || x * per < it.n) r[x].load(a, it, head, t, x * per);
+        for (int i = tile; i < end;) {
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j, i += step) {
+                if (i >= end) break;
+                s32x4_t score[R];
+#pragma unroll
+                for (int x = 0; x < R; ++x)
+                    if (x == 0 || x * per < it.n) score[x] = p[j].score(r[x]);
+                const float unit = scale_of(p[j].exp);
+                if (i + AHEAD * step < end) p[j].load(a, page[j], head);
+                page[j] = table[min(16 * (i + 2 * AHEAD * step) + col, count - 1)];
+                const int at = 16 * i + col;
+#pragma unroll
+                for (int x = 0; x < R; ++x) {
+                    if (x > 0 && x * per >= it.n) continue;
+                    const auto give = [&](int token, int best) {
+                        token += x * per;
+                        if (token < it.n && at < count) put(token, at, key_of((float)best * unit), t > 0);
+                    };
+                    const s32x4_t y = score[x];
+                    // rows 4 g + 0..3 of page `col` are here
+                    if (a.pad_shift == 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) give(4 * g + k, y[k]);
+                    } else if (a.pad_shift == 1) {
+                        give(2 * g, max(y[0], y[1]));
+                        give(2 * g + 1, max(y[2], y[3]));
+                    } else {
+                        int m = max(max(y[0], y[1]), max(y[2], y[3]));
+                        if (a.pad_shift > 2) m = max(m, __shfl_xor(m, 16));
+                        if (a.pad_shift > 3) m = max(m, __shfl_xor(m, 32));
+                        if ((g & ((1 << (a.pad_shift - 2)) - 1)) == 0) give(g >> (a.pad_shift - 2), m);
+                    }
+                }
             }
         }
     }
 }
 
-constexpr int kSelectWaves = 4;
+// f(x, ...) over a wave's lanes by moves between them: the result of all lanes up
+// to each (F, 0 or none as `none`), in lane 63 that of all.
+template <typename F>
+__device__ __forceinline__ int wave_scan(int x, int none, F f) {
+#define SP_STEP(ctrl, rows) x = f(x, __builtin_amdgcn_update_dpp(none, x, ctrl, rows, 0xF, false))
+    SP_STEP(0x111, 0xF);  // from 1, 2, 4 and 8 lanes before, within 16
+    SP_STEP(0x112, 0xF);
+    SP_STEP(0x114, 0xF);
+    SP_STEP(0x118, 0xF);
+    SP_STEP(0x142, 0xA);  // the last of 16 to the next 16, the last of 32 to the other 32
+    SP_STEP(0x143, 0xC);
+#undef SP_STEP
+    return x;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    const int y = wave_scan((int)x, 0, [](int u, int v) { return (int)max((uint32_t)u, (uint32_t)v); });
+    return (uint32_t)__builtin_amdgcn_readlane(y, 63);
+}
+
+template <int WAVES>
 struct SelectScratch {
     uint32_t hist[256];
-    uint32_t gt[kSelectWaves], eq[kSelectWaves];
+    uint32_t gt[WAVES], eq[WAVES];
 };
 template <int TEAM>
 __device__ __forceinline__ void team_sync() {
@@ -358,9 +399,9 @@ __device__ __forceinline__ void team_sync() {
 // order.  A team of waves (all of a workgroup, or one) finds the k-th key digit by
 // digit from the first bit in which the keys differ, by counting; then every wave
 // goes through a part of them of its own.
-template <int TEAM, typename Keys>
+template <int TEAM, typename Keys, typename Scratch>
 __device__ __forceinline__ void take_largest(const Keys& key, int n, int k, const int32_t* pages, int32_t* out,
-                                             SelectScratch& s) {
+                                             Scratch& s) {
     const int lane = threadIdx.x & 63, wave = TEAM > 1 ? wave_id() : 0;
     const int self = 64 * wave + lane;
     uint32_t most = 0, least = 0xFFFFFFFFu;
@@ -369,10 +410,8 @@ __device__ __forceinline__ void take_largest(const Keys& key, int n, int k, cons
         most = max(most, x);
         least = min(least, x);
     }
-    for (int o = 1; o < 64; o <<= 1) {
-        most = max(most, (uint32_t)__shfl_xor((int)most, o));
-        least = min(least, (uint32_t)__shfl_xor((int)least, o));
-    }
+    most = wave_max(most);
+    least = ~wave_max(~least);
     if constexpr (TEAM > 1) {
         if (lane == 0) {
             s.gt[wave] = most;
@@ -404,11 +443,7 @@ __device__ __forceinline__ void take_largest(const Keys& key, int n, int k, cons
             // digits from the largest down, four to a lane
             int c[4], sum = 0;
             for (int j = 0; j < 4; ++j) sum += c[j] = (int)s.hist[255 - 4 * lane - j];
-            int upto = sum;
-            for (int o = 1; o < 64; o <<= 1) {
-                const int x = __shfl_up(upto, o);
-                upto += lane >= o ? x : 0;
-            }
+            const int upto = wave_scan(sum, 0, [](int u, int v) { return u + v; });
             const int at = __ffsll((unsigned long long)__ballot(upto >= want)) - 1;
             int above = upto - sum, digit = 255 - 4 * lane, count = c[0];
             for (int j = 1; j < 4; ++j)
@@ -417,9 +452,9 @@ __device__ __forceinline__ void take_largest(const Keys& key, int n, int k, cons
                     count = c[j];
                     --digit;
                 }
-            above = __shfl(above, at);
-            digit = __shfl(digit, at);
-            count = __shfl(count, at);
+            above = __builtin_amdgcn_readlane(above, at);
+            digit = __builtin_amdgcn_readlane(digit, at);
+            count = __builtin_amdgcn_readlane(count, at);
             want -= above;
             mask |= 255u << shift;
             prefix |= (uint32_t)digit << shift;
@@ -463,9 +498,9 @@ __device__ __forceinline__ void take_largest(const Keys& key, int n, int k, cons
 }
 
 // Token i's row of the result.
-template <int TEAM, typename Keys>
+template <int TEAM, typename Keys, typename Scratch>
 __device__ __forceinline__ void select_token(const SelectArgs& a, const SelectItem& it, int head, int i, const Keys& key,
-                                             SelectScratch& s) {
+                                             Scratch& s) {
     const int self = TEAM > 1 ? threadIdx.x : threadIdx.x & 63;
     int32_t* out = a.selected + ((int64_t)(it.row + i) * a.n_kv_heads + head) * a.select;
     const int n = it.scored(a, i), own = it.own(a, i);
@@ -481,63 +516,53 @@ __device__ __forceinline__ void select_token(const SelectArgs& a, const SelectIt
     const int k = a.select - a.first - a.last;
     if (k > 0) take_largest<TEAM>(key, n, k, it.table + a.first, out + a.first, s);
 }
-template <typename Keys>
-__device__ __forceinline__ void select_item(const SelectArgs& a, const SelectItem& it, int head, const Keys& key,
-                                            SelectScratch* s) {
-    if (it.n >= kSelectWaves) {
-        const int w = wave_id();
-        for (int i = w; i < it.n; i += kSelectWaves)
-            select_token<1>(a, it, head, i, [&](int x) { return key(i, x); }, s[w]);
+
+// Scores in LDS, and the choice, in one: of a single token (ONE) by 16 waves, which
+// have 190 KB of bounds under way between them, or of several by four, each of
+// which chooses for tokens of its own.
+template <int D, bool ONE>
+__global__ __launch_bounds__(ONE ? 1024 : 256, ONE ? 4 : 2) void select_kernel(SelectArgs a) {
+    constexpr int WAVES = ONE ? 16 : 4;
+    extern __shared__ uint32_t keys[];
+    __shared__ SelectScratch<WAVES> s[ONE ? 1 : WAVES];
+    const int head = blockIdx.x % a.n_kv_heads, w = wave_id();
+    SelectItem it;
+    if (!load_select(a, blockIdx.x / a.n_kv_heads, it)) return;
+    const int tiles = it.tiles(a);
+    if (tiles > 0) {
+        score_pages<D, ONE ? 1 : SP_ROW_TILES, ONE ? 2 : 1>(a, it, head, w, WAVES, tiles,
+                                                            [&](int token, int page, uint32_t x, bool again) {
+                                                                uint32_t& to = keys[token * a.max_scored + page];
+                                                                to = again ? max(to, x) : x;
+                                                            });
+        __syncthreads();
+    }
+    if constexpr (ONE) {
+        select_token<WAVES>(a, it, head, 0, [&](int page) { return keys[page]; }, s[0]);
     } else {
-        for (int i = 0; i < it.n; ++i) {
-            if (i) __syncthreads();
-            select_token<kSelectWaves>(a, it, head, i, [&](int x) { return key(i, x); }, s[0]);
-        }
+        for (int i = w; i < it.n; i += WAVES)
+            select_token<1>(a, it, head, i, [&](int page) { return keys[i * a.max_scored + page]; }, s[w]);
     }
 }
 
-// Scores in LDS, and the choice, in one.
+// The same for single tokens in two launches, by way of memory.
+constexpr int kScoreTiles = 32;  // tiles of 16 pages of a workgroup, about
 template <int D>
-__global__ __launch_bounds__(64 * kSelectWaves) void select_kernel(SelectArgs a) {
-    extern __shared__ uint32_t keys[];
-    __shared__ SelectScratch s[kSelectWaves];
+__global__ __launch_bounds__(256) void score_kernel(SelectArgs a) {
     const int head = blockIdx.x % a.n_kv_heads;
     SelectItem it;
     if (!load_select(a, blockIdx.x / a.n_kv_heads, it)) return;
-    if (it.tiles(a) > 0) {
-        score_pages<D>(a, it, head, wave_id(), kSelectWaves, it.tiles(a), [&](int token, int page, uint32_t x, bool again) {
-            uint32_t& to = keys[token * a.max_scored + page];
-            to = again ? max(to, x) : x;
-        });
-        __syncthreads();
-    }
-    select_item(a, it, head, [&](int token, int page) { return keys[token * a.max_scored + page]; }, s);
+    uint32_t* keys = a.keys + (int64_t)blockIdx.x * a.max_scored;
+    score_pages<D, 1, 2>(a, it, head, blockIdx.y * 4 + wave_id(), gridDim.y * 4, it.tiles(a),
+                         [&](int, int page, uint32_t x, bool again) { keys[page] = again ? max(keys[page], x) : x; });
 }
-
-// The same in two launches, by way of memory.
-__device__ __forceinline__ int64_t key_row(const SelectArgs& a, int item, int head) {
-    return ((int64_t)item * a.item_tokens * a.n_kv_heads + head) * a.max_scored;
-}
-constexpr int kScoreTiles = 32;  // tiles of 16 pages of a workgroup, about
-template <int D>
-__global__ __launch_bounds__(64 * kSelectWaves) void score_kernel(SelectArgs a) {
-    const int head = blockIdx.x % a.n_kv_heads, item = blockIdx.x / a.n_kv_heads;
+__global__ __launch_bounds__(1024) void choose_kernel(SelectArgs a) {
+    __shared__ SelectScratch<16> s;
+    const int head = blockIdx.x % a.n_kv_heads;
     SelectItem it;
-    if (!load_select(a, item, it)) return;
-    uint32_t* keys = a.keys + key_row(a, item, head);
-    score_pages<D>(a, it, head, blockIdx.y * kSelectWaves + wave_id(), gridDim.y * kSelectWaves, it.tiles(a), [&](int token, int page, uint32_t x, bool again) {
-        uint32_t* to = keys + (int64_t)token * a.n_kv_heads * a.max_scored + page;
-        *to = again ? max(*to, x) : x;
-    });
-}
-__global__ __launch_bounds__(64 * kSelectWaves) void choose_kernel(SelectArgs a) {
-    __shared__ SelectScratch s[kSelectWaves];
-    const int head = blockIdx.x % a.n_kv_heads, item = blockIdx.x / a.n_kv_heads;
-    SelectItem it;
-    if (!load_select(a, item, it)) return;
-    const uint32_t* keys = a.keys + key_row(a, item, head);
-    select_item(a, it, head,
-                [&](int token, int page) { return keys[(int64_t)token * a.n_kv_heads * a.max_scored + page]; }, s);
+    if (!load_select(a, blockIdx.x / a.n_kv_heads, it)) return;
+    const uint32_t* keys = a.keys + (int64_t)blockIdx.x * a.max_scored;
+    select_token<16>(a, it, head, 0, [&](int page) { return keys[page]; }, s);
 }
 
 int32_t check_bounds(const lora_kv_bounds_t* b, const lora_attn_shape_t& s) {
@@ -618,23 +643,26 @@ extern "C" int32_t lora_sparse_select(const lora_sparse_launch_t* L, const lora_
     a.last = S.shape.last;
     a.max_scored = S.max_scored;
     a.item_tokens = S.item_tokens;
-    if (a.item_tokens < 1 || a.item_tokens << a.pad_shift > 16) return LORA_EINVAL;
+    if (a.item_tokens < 1 || a.item_tokens > (16 * SP_ROW_TILES) >> a.pad_shift) return LORA_EINVAL;
     const lora_sparse_item_t* items = reinterpret_cast<const lora_sparse_item_t*>(L->attn.meta + S.off_items);
     const hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
     if (sp_in_lds(S.max_scored, S.item_tokens)) {
         if ((int64_t)S.n_items * hk > kMaxBlocks) return LORA_EINVAL;
         a.items = items;
         void* p[] = {&a};
-        const void* fn = d == 128 ? reinterpret_cast<const void*>(select_kernel<128>)
-                                  : reinterpret_cast<const void*>(select_kernel<64>);
+        const bool one = S.item_tokens == 1;
+        typedef void (*fn_t)(SelectArgs);
+        static const fn_t fn[2][2] = {{select_kernel<64, false>, select_kernel<64, true>},
+                                      {select_kernel<128, false>, select_kernel<128, true>}};
         const size_t lds = sizeof(uint32_t) * (size_t)S.max_scored * (size_t)S.item_tokens;
-        return hipLaunchKernel(fn, dim3((unsigned)(S.n_items * hk)), dim3(64 * kSelectWaves), p, lds, stream) == hipSuccess
-                   ? LORA_OK
-                   : LORA_EHIP;
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn[d == 128][one]),
+                                             dim3((unsigned)(S.n_items * hk)), dim3(one ? 1024 : 256), p, lds, stream);
+        return e == hipSuccess ? LORA_OK : LORA_EHIP;
     }
     if (workspace_floats < I.workspace_floats) return LORA_ECAPACITY;
     if (!workspace || !aligned16(workspace)) return LORA_EINVAL;
-    const int64_t per = sp_keys(S.max_scored, S.item_tokens, hk), slab = sp_slab(per, S.n_items);
+    if (S.item_tokens != 1) return LORA_EINVAL;
+    const int64_t per = (int64_t)S.max_scored * hk, slab = sp_slab(per, S.n_items);
     if (slab * per > I.workspace_floats || slab * hk > kMaxBlocks) return LORA_EINVAL;
     a.keys = reinterpret_cast<uint32_t*>(workspace);
     const int64_t parts = (S.max_scored + 16 * kScoreTiles - 1) / (16 * kScoreTiles);
@@ -642,9 +670,9 @@ extern "C" int32_t lora_sparse_select(const lora_sparse_launch_t* L, const lora_
         a.items = items + i;
         const unsigned blocks = (unsigned)((S.n_items - i < slab ? S.n_items - i : slab) * hk);
         const unsigned gy = (unsigned)std::max<int64_t>(1, std::min(std::min<int64_t>(parts, 4096), kMaxBlocks / blocks));
-        if (launch(d == 128 ? score_kernel<128> : score_kernel<64>, dim3(blocks, gy), dim3(64 * kSelectWaves), stream, a) !=
+        if (launch(d == 128 ? score_kernel<128> : score_kernel<64>, dim3(blocks, gy), dim3(256), stream, a) !=
                 hipSuccess ||
-            launch(choose_kernel, dim3(blocks), dim3(64 * kSelectWaves), stream, a) != hipSuccess)
+            launch(choose_kernel, dim3(blocks), dim3(1024), stream, a) != hipSuccess)
             return LORA_EHIP;
     }
     return LORA_OK;

@@ -247,6 +247,23 @@ def test_split_contexts():
     run_case([(1, 3000), (2, 1500)], 4, 2, 64, 16, "e4m3", 120, 2, 3)
 
 
+# more than 2048 items: a wave to each
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim,page,heads,kv_heads,n", [(128, 16, 8, 8, 260), (64, 32, 8, 4, 530), (128, 64, 14, 2, 1030),
+                                                       (64, 16, 20, 1, 1030)])
+def test_many_tokens(dim, page, heads, kv_heads, n, dtype):
+    batch, *_ = run_case([(n, n + 90), (1, 1), (4, 2), (1, 37)], heads, kv_heads, dim, page, dtype, 3)
+    assert batch.sparse_info.n_work * kv_heads >= 2048
+    run_case([(n, n), (1, 300)], heads, kv_heads, dim, page, dtype, 4, 0, 2, token_major=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_many_tokens_and_long_ones(dtype):
+    """Items that are split among many that are not."""
+    batch, *_ = run_case([(1100, 1100)] + [(1, 4000)] * 3, 2, 2, 64, 16, dtype, 200)
+    assert batch.sparse_info.n_merge > 0 and batch.sparse_info.n_work * 2 >= 2048
+
+
 def test_what_is_not_seen_does_not_matter():
     """NaN and infinities in pages that are not chosen, in unused pages, and past the row in its own page."""
     rng = np.random.default_rng(6)

@@ -41,7 +41,7 @@ def check_sparse(s, sp, q_len, kv_len, table, bounded, staging, attn, info):
     pad = 1
     while pad < min(group, 16):
         pad *= 2
-    assert info.item_tokens * pad <= 16
+    assert info.item_tokens * pad <= 64 and (info.item_tokens == 1 or info.item_tokens * info.max_scored <= 12288)
     # attention items: every row and head over every tile once
     tiles, parts = {}, 0
     for w in ints(staging, info.off_work, info.n_work, hl.ATTN_WORK_INTS):
@@ -184,7 +184,7 @@ def test_calls_refuse_arguments():
         assert call("select", **kw) == bad and call("attn", **kw) == bad, kw
     for kw in (dict(out=None), dict(ldo=512), dict(scale=0.0), dict(scale=float("inf")), dict(scale=float("nan"))):
         assert call("attn", **kw) == bad, kw
-    assert call("select", L=launch(item_tokens=8)) == bad  # more rows than a tile
+    assert call("select", L=launch(item_tokens=17)) == bad  # more rows than are scored at once
     for name in ("bounds", "attn"):
         assert call(name, c=kv(n_pages=999)) == hl.LORA_ESHAPE and call(name, c=kv(k=None)) == bad
     assert hl._lib.lora_sparse_attn(None, None, 16, 8, 16, 16, 8, 1.0, None, 0, None) == bad
