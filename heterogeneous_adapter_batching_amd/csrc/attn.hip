@@ -389,10 +389,6 @@ __device__ __forceinline__ bool none_sees(const AttnArgs& a, int p_lo, int p_hi,
 // rows of two neighbouring column blocks (wide) or of 8 rows (narrow); the row's
 // low bits move the pair of chunks, and leave the pair's last bit to bit 2.
 template <int D>
-__device__ __forceinline__ int k_chunk(int row, int c) {
-    return c ^ (D == 128 ? row & 15 : (row >> 1) & 7);
-}
-template <int D>
 __device__ __forceinline__ int v_chunk(int row, int c) {
     return c ^ ((D == 128 ? (row & 3) << 2 : (row & 2) << 1) | ((row >> 1) & 2));
 }

@@ -67,6 +67,19 @@ __device__ __forceinline__ u32x4_t dequant8(u32x2_t c, float scale) {
     return r;
 }
 
+// Where chunk c (16 bytes) of a row lies in LDS, rows of 2 D bytes: the 16 lanes that
+// read one chunk of 16 rows hit all banks once.
+template <int D>
+__device__ __forceinline__ int k_chunk(int row, int c) {
+    return c ^ (D == 128 ? row & 15 : (row >> 1) & 7);
+}
+// Everything that the wave has written to LDS is there for its other lanes.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ------------------------------------------------------------------ launchers
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 

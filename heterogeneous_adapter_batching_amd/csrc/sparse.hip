@@ -197,9 +197,9 @@ struct SelectItem : lora_sparse_item_t {
     __device__ __forceinline__ int scored(const SelectArgs& a, int i) const {
         return pos + i < 0 || own(a, i) + 1 <= a.select ? 0 : own(a, i) + 1 - a.last - a.first;
     }
-    // tiles of 16 pages to score
-    __device__ __forceinline__ int tiles(const SelectArgs& a) const {
-        return a.select > a.first + a.last ? (scored(a, n - 1) + 15) >> 4 : 0;
+    // there is something to choose
+    __device__ __forceinline__ bool scores(const SelectArgs& a) const {
+        return a.select > a.first + a.last && scored(a, n - 1) > 0;
     }
 };
 // Items that do not lie inside the batch are skipped.
@@ -211,84 +211,143 @@ __device__ __forceinline__ bool load_select(const SelectArgs& a, int i, SelectIt
     return it.pos + it.n - 1 < 0 || (it.own(a, it.n - 1) < a.ld_table && it.scored(a, it.n - 1) <= a.max_scored);
 }
 
+// f over lanes by moves between them: the result of all lanes up to each, within 16
+// lanes (row_scan) or the wave; `none` changes nothing.
+template <typename F>
+__device__ __forceinline__ int row_scan(int x, int none, F f) {
+#define SP_STEP(ctrl, rows) x = f(x, __builtin_amdgcn_update_dpp(none, x, ctrl, rows, 0xF, false))
+    SP_STEP(0x111, 0xF);  // from 1, 2, 4 and 8 lanes before
+    SP_STEP(0x112, 0xF);
+    SP_STEP(0x114, 0xF);
+    SP_STEP(0x118, 0xF);
+    return x;
+}
+template <typename F>
+__device__ __forceinline__ int wave_scan(int x, int none, F f) {
+    x = row_scan(x, none, f);
+    SP_STEP(0x142, 0xA);  // the last of 16 to the next 16, the last of 32 to the other 32
+    SP_STEP(0x143, 0xC);
+#undef SP_STEP
+    return x;
+}
+__device__ __forceinline__ int larger(int u, int v) { return (int)max((uint32_t)u, (uint32_t)v); }
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_readlane(wave_scan((int)x, 0, larger), 63);
+}
+
 // Scores are the products of a tile of 16 rows (query heads of one or more
 // tokens) with 16 pages on the 8-bit matrix unit: sum max(r hi, r lo) =
 // max(r, 0) . hi + min(r, 0) . lo.  As whole numbers they are exact; times their
 // power of two they are below 2^121 and at least 2^-100, exact in fp32 as well.
+//
+// Tiles of rows and of pages lie in LDS alike: 2 D bytes a row, max(r, 0) or hi
+// first.  A lane's operands: 16 bytes of row lane % 16 for each 64 elements.
 template <int D>
-struct Rows16 {
-    static constexpr int S = D / 64;
-    s32x4_t up[S], down[S];  // max(r, 0) and min(r, 0) of row lane % 16: elements 64 s + 16 (lane / 16) + 0..15
-
-    __device__ __forceinline__ static int heads(const SelectArgs& a) { return (a.group + 15) >> 4; }  // tiles of a token
-    __device__ __forceinline__ static const uint16_t* row(const SelectArgs& a, const SelectItem& it, int head, int tile,
-                                                          int first) {
-        const int r = threadIdx.x & 15, token = min(first + (r >> a.pad_shift), it.n - 1);
-        const int h = min(16 * tile + (r & ((1 << a.pad_shift) - 1)), a.group - 1);  // the last head again changes no maximum
-        return a.q + (it.row + token) * a.ldq + ((int64_t)head * a.group + h) * D + 16 * (threadIdx.x >> 4 & 3);
-    }
-    // tokens from `first` on of the item, heads of `tile`
-    __device__ __forceinline__ void load(const SelectArgs& a, const SelectItem& it, int head, int tile, int first) {
-        uint32_t top = 0;
-        u32x4_t x[2 * S];
-        const auto read = [&](int t) {
-            const uint16_t* q = row(a, it, head, t, first);
+struct Operand {
+    s32x4_t up[D / 64], down[D / 64];
+    __device__ __forceinline__ void read(const char* lds) {
+        const int col = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                x[2 * s] = *reinterpret_cast<const u32x4_t*>(q + 64 * s);
-                x[2 * s + 1] = *reinterpret_cast<const u32x4_t*>(q + 64 * s + 8);
-            }
-        };
-        const int tiles = heads(a);
-        for (int t = 1; t <= tiles; ++t) {  // the tile itself last
-            read((tile + t) % tiles);
-#pragma unroll
-            for (int i = 0; i < 2 * S; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t lo = x[i][j] & 0x7FFFu, hi = x[i][j] >> 16 & 0x7FFFu;
-                    top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-                }
+        for (int s = 0; s < D / 64; ++s) {
+            up[s] = *reinterpret_cast<const s32x4_t*>(lds + col * (2 * D) + 16 * k_chunk<D>(col, 4 * s + g));
+            down[s] = *reinterpret_cast<const s32x4_t*>(lds + col * (2 * D) + 16 * k_chunk<D>(col, D / 16 + 4 * s + g));
         }
-        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        for (int o = 1; o < 1 << a.pad_shift; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-        const float unit = power(-code_exponent(top));
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t w0 = x[2 * s + j / 2][2 * (j % 2)], w1 = x[2 * s + j / 2][2 * (j % 2) + 1];
-                const int c0 = code(bf16_lo(w0), unit), c1 = code(bf16_hi(w0), unit);
-                const int c2 = code(bf16_lo(w1), unit), c3 = code(bf16_hi(w1), unit);
-                up[s][j] = (int)pack4(max(c0, 0), max(c1, 0), max(c2, 0), max(c3, 0));
-                down[s][j] = (int)pack4(min(c0, 0), min(c1, 0), min(c2, 0), min(c3, 0));
-            }
     }
 };
 template <int D>
-struct Pages16 {
-    static constexpr int S = D / 64;
-    s32x4_t hi[S], lo[S];
-    uint32_t exp;
-    __device__ __forceinline__ void load(const SelectArgs& a, int32_t page, int head) {
-        const int64_t at = (int64_t)min((uint32_t)page, (uint32_t)(a.n_pages - 1)) * a.n_kv_heads + head;
-        const int8_t* p = a.codes + at * 2 * D + 16 * (threadIdx.x >> 4 & 3);
+__device__ __forceinline__ s32x4_t score(const Operand<D>& rows, const Operand<D>& pages) {
+    s32x4_t x = {0, 0, 0, 0};
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            hi[s] = *reinterpret_cast<const s32x4_t*>(p + 64 * s);
-            lo[s] = *reinterpret_cast<const s32x4_t*>(p + D + 64 * s);
-        }
-        exp = a.exps[at];
+    for (int s = 0; s < D / 64; ++s) {
+        x = __builtin_amdgcn_mfma_i32_16x16x64_i8(rows.up[s], pages.up[s], x, 0, 0, 0);
+        x = __builtin_amdgcn_mfma_i32_16x16x64_i8(rows.down[s], pages.down[s], x, 0, 0, 0);
     }
-    __device__ __forceinline__ s32x4_t score(const Rows16<D>& r) const {
-        s32x4_t x = {0, 0, 0, 0};
+    return x;
+}
+
+// The item's queries as codes, R tiles of rows, made by all WAVES of a workgroup
+// together: D/2 lanes to a row, two elements each.  (Every wave for itself, lane by
+// lane as the operand wants them, took longer than the scores of 500 pages.)
+// Where a token has more heads than a tile, tiles of heads follow one another:
+// code() is called for each, all of them after load().
+template <int D, int R, int WAVES>
+struct Rows {
+    static constexpr int LANES = D / 2, STEP = WAVES * 64 / LANES, N = (16 * R + STEP - 1) / STEP;
+    uint32_t x[N];
+
+    __device__ __forceinline__ static int heads(const SelectArgs& a) { return (a.group + 15) >> 4; }
+    __device__ __forceinline__ static int row(int j) { return j * STEP + (int)threadIdx.x / LANES; }
+    __device__ __forceinline__ static int token(const SelectArgs& a, const SelectItem& it, int r) {
+        return min(r >> a.pad_shift, it.n - 1);  // rows of tokens that are not there: of the last one again
+    }
+    __device__ __forceinline__ void load(const SelectArgs& a, const SelectItem& it, int head, int tile) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            x = __builtin_amdgcn_mfma_i32_16x16x64_i8(r.up[s], hi[s], x, 0, 0, 0);
-            x = __builtin_amdgcn_mfma_i32_16x16x64_i8(r.down[s], lo[s], x, 0, 0, 0);
+        for (int j = 0; j < N; ++j) {
+            const int r = row(j);  // (the last head again changes no maximum)
+            const int h = min(16 * tile + (r & ((1 << a.pad_shift) - 1)), a.group - 1);
+            const int64_t at = (it.row + token(a, it, r)) * a.ldq + ((int64_t)head * a.group + h) * D;
+            x[j] = *reinterpret_cast<const uint32_t*>(a.q + at + 2 * (threadIdx.x % LANES));
         }
-        return x;
+    }
+    // top[token]: the bits of the token's largest finite |q|; starts at zero
+    __device__ __forceinline__ void find_top(const SelectArgs& a, const SelectItem& it, uint32_t* top) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint32_t lo = x[j] & 0x7FFFu, hi = x[j] >> 16 & 0x7FFFu;
+            const int m = row_scan((int)max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u), 0, larger);
+            if ((threadIdx.x & 15) == 15) atomicMax(&top[token(a, it, row(j))], (uint32_t)m);
+        }
+    }
+    __device__ __forceinline__ void store(const SelectArgs& a, const SelectItem& it, const uint32_t* top, char* lds) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int r = row(j), col = threadIdx.x % LANES;
+            if (r >= 16 * R) break;
+            const float unit = power(-code_exponent(top[token(a, it, r)]));
+            const int c0 = code(bf16_lo(x[j]), unit), c1 = code(bf16_hi(x[j]), unit);
+            char* to = lds + r * (2 * D) + 2 * (col % 8);
+            const auto put = [&](int c, int u, int v) {
+                *reinterpret_cast<uint16_t*>(to + 16 * k_chunk<D>(r & 15, c)) = (uint16_t)((u & 255) | (v & 255) << 8);
+            };
+            put(col / 8, max(c0, 0), max(c1, 0));
+            put(D / 16 + col / 8, min(c0, 0), min(c1, 0));
+        }
+    }
+};
+
+// The bounds of 16 pages, which go through LDS: lanes on end load a page's 2 D bytes
+// (as operands, 16 bytes of each of 16 pages to lanes on end, the loads took four
+// times as long: the cache serves 64 bytes at a time), and each gets what the
+// product wants of page lane % 16 back.
+template <int D>
+struct Pages16 {
+    static constexpr int S = D / 64, CPR = D / 8, RPI = 64 / CPR, LOADS = 16 / RPI;
+    u32x4_t raw[LOADS];
+    uint32_t exp;         // of page lane % 16
+    int32_t ids[LOADS];   // pages that the lane loads of, and page lane % 16: of the tile to load next
+    int32_t id;
+
+    __device__ __forceinline__ void look_up(const int32_t* table, int tile, int count) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) ids[j] = table[(uint32_t)min(16 * tile + RPI * j + lane / CPR, count - 1)];
+        id = table[(uint32_t)min(16 * tile + (lane & 15), count - 1)];
+    }
+    __device__ __forceinline__ void load(const SelectArgs& a, int head) {
+        const int8_t* codes = a.codes + (int64_t)head * (2 * D) + 16 * ((threadIdx.x & 63) % CPR);
+        const uint32_t page_bytes = (uint32_t)a.n_kv_heads * (2 * D), last = (uint32_t)(a.n_pages - 1);
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j)
+            raw[j] = *reinterpret_cast<const u32x4_t*>(codes + (uint64_t)min((uint32_t)ids[j], last) * page_bytes);
+        exp = a.exps[head + (uint64_t)min((uint32_t)id, last) * (uint32_t)a.n_kv_heads];
+    }
+    __device__ __forceinline__ void store(char* lds) const {
+        const int lane = threadIdx.x & 63, col = lane % CPR;
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+            const int r = RPI * j + lane / CPR;
+            *reinterpret_cast<u32x4_t*>(lds + r * (2 * D) + 16 * k_chunk<D>(r, col)) = raw[j];
+        }
     }
 };
 // An unsigned number of the order of x.
@@ -297,132 +356,144 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// Keys of the item's scored pages, tiles of 16 pages from `tile` on in steps of
-// `step`, for up to R tiles of rows at once; the bounds of AHEAD tiles are under
-// way.  put(token, page, key, again) takes the keys, `again` where an earlier tile
-// of heads has given one.  The same lane gives a page's key every time.
-template <int D, int R, int AHEAD, typename Put>
-__device__ __forceinline__ void score_pages(const SelectArgs& a, const SelectItem& it, int head, int tile, int step,
-                                            int end, Put put) {
-    const int col = threadIdx.x & 15, g = threadIdx.x >> 4 & 3, count = it.scored(a, it.n - 1), per = 16 >> a.pad_shift;
+// What a workgroup that scores needs of LDS.
+template <int D, int R, int WAVES>
+struct ScoreLds {
+    __align__(16) char pages[WAVES][32 * D];
+    __align__(16) char rows[R * 32 * D];
+    uint32_t top[16 * R];
+};
+// Keys of the item's scored pages, a tile of 16 pages to a wave of each of `parts`
+// workgroups in turn, for up to R tiles of rows at once.  put(token, page, key,
+// again) takes a token's key of one head, or the largest of several, `again` where
+// an earlier tile of heads has given some; the same lane takes a page's every time.
+template <int D, int R, int WAVES, typename Put>
+__device__ __forceinline__ void score_pages(const SelectArgs& a, const SelectItem& it, int head, int part, int parts,
+                                            ScoreLds<D, R, WAVES>& lds, Put put) {
+    const int w = wave_id(), count = it.scored(a, it.n - 1), end = (count + 15) >> 4, tile = part * WAVES + w, step = parts * WAVES;
+    const int rows = R == 1 ? 1 : ((it.n << a.pad_shift) + 15) >> 4;
     const int32_t* table = it.table + a.first;
-    for (int t = 0; t < Rows16<D>::heads(a); ++t) {
-        if (tile >= end) return;
-        Pages16<D> p[AHEAD];
-        int32_t page[AHEAD];
-#pragma unroll
-        for (int j = 0; j < AHEAD; ++j) page[j] = table[min(16 * (tile + j * step) + col, count - 1)];
-#pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-            if (tile + j * step < end) p[j].load(a, page[j], head);
-            page[j] = table[min(16 * (tile + (j + AHEAD) * step) + col, count - 1)];
+    Rows<D, R, WAVES> q;
+    Pages16<D> p;
+    const int heads = q.heads(a);
+    p.look_up(table, tile, count);
+    q.load(a, it, head, heads - 1);
+    for (int i = threadIdx.x; i < 16 * R; i += 64 * WAVES) lds.top[i] = 0;
+    __syncthreads();
+    for (int t = heads - 1; t > 0; --t) {
+        q.find_top(a, it, lds.top);
+        q.load(a, it, head, t - 1);
+    }
+    p.load(a, head);
+    p.look_up(table, tile + step, count);
+    q.find_top(a, it, lds.top);
+    __syncthreads();
+    for (int t = 0; t < heads; ++t) {
+        if (t > 0) {
+            __syncthreads();
+            q.load(a, it, head, t);
+            p.look_up(table, tile, count);
+            p.load(a, head);
+            p.look_up(table, tile + step, count);
         }
-        Rows16<D> r[R];
+        q.store(a, it, lds.top, lds.rows);
+        __syncthreads();
+        Operand<D> r;
+        if (R == 1) r.read(lds.rows);
+        for (int i = tile; i < end; i += step) {
+            wave_sync();
+            p.store(lds.pages[w]);
+            wave_sync();
+            const float unit = scale_of(p.exp);
+            if (i + step < end) {
+                p.load(a, head);
+                p.look_up(table, i + 2 * step, count);
+            }
+            Operand<D> b;
+            b.read(lds.pages[w]);
+            const int at = 16 * i + (int)(threadIdx.x & 15), g = threadIdx.x >> 4 & 3;
+            for (int x = 0; x < rows; ++x) {
+                if (R > 1) r.read(lds.rows + x * 32 * D);
+                const s32x4_t y = score<D>(r, b);  // rows 4 g + 0..3 of page lane % 16
+                if (at >= count) continue;
+                const auto give = [&](int row, int best) {
+                    put(min((16 * x + row) >> a.pad_shift, it.n - 1), at, key_of((float)best * unit), t > 0);
+                };
+                if (R > 1 && a.pad_shift == 0) {
 #pragma unroll
-        for (int x = 0; x < R; ++x)
-            if (x == 0 || x * per < it.n) r[x].load(a, it, head, t, x * per);
-        for (int i = tile; i < end;) {
-#pragma unroll
-            for (int j = 0; j < AHEAD; ++j, i += step) {
-                if (i >= end) break;
-                s32x4_t score[R];
-#pragma unroll
-                for (int x = 0; x < R; ++x)
-                    if (x == 0 || x * per < it.n) score[x] = p[j].score(r[x]);
-                const float unit = scale_of(p[j].exp);
-                if (i + AHEAD * step < end) p[j].load(a, page[j], head);
-                page[j] = table[min(16 * (i + 2 * AHEAD * step) + col, count - 1)];
-                const int at = 16 * i + col;
-#pragma unroll
-                for (int x = 0; x < R; ++x) {
-                    if (x > 0 && x * per >= it.n) continue;
-                    const auto give = [&](int token, int best) {
-                        token += x * per;
-                        if (token < it.n && at < count) put(token, at, key_of((float)best * unit), t > 0);
-                    };
-                    const s32x4_t y = score[x];
-                    // rows 4 g + 0..3 of page `col` are here
-                    if (a.pad_shift == 0) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) give(4 * g + k, y[k]);
-                    } else if (a.pad_shift == 1) {
-                        give(2 * g, max(y[0], y[1]));
-                        give(2 * g + 1, max(y[2], y[3]));
-                    } else {
-                        int m = max(max(y[0], y[1]), max(y[2], y[3]));
-                        if (a.pad_shift > 2) m = max(m, __shfl_xor(m, 16));
-                        if (a.pad_shift > 3) m = max(m, __shfl_xor(m, 32));
-                        if ((g & ((1 << (a.pad_shift - 2)) - 1)) == 0) give(g >> (a.pad_shift - 2), m);
-                    }
+                    for (int k = 0; k < 4; ++k) give(4 * g + k, y[k]);
+                } else if (R > 1 && a.pad_shift == 1) {
+                    give(4 * g, max(y[0], y[1]));
+                    give(4 * g + 2, max(y[2], y[3]));
+                } else {
+                    give(4 * g, max(max(y[0], y[1]), max(y[2], y[3])));
                 }
             }
         }
     }
 }
 
-// f(x, ...) over a wave's lanes by moves between them: the result of all lanes up
-// to each (F, 0 or none as `none`), in lane 63 that of all.
-template <typename F>
-__device__ __forceinline__ int wave_scan(int x, int none, F f) {
-#define SP_STEP(ctrl, rows) x = f(x, __builtin_amdgcn_update_dpp(none, x, ctrl, rows, 0xF, false))
-    SP_STEP(0x111, 0xF);  // from 1, 2, 4 and 8 lanes before, within 16
-    SP_STEP(0x112, 0xF);
-    SP_STEP(0x114, 0xF);
-    SP_STEP(0x118, 0xF);
-    SP_STEP(0x142, 0xA);  // the last of 16 to the next 16, the last of 32 to the other 32
-    SP_STEP(0x143, 0xC);
-#undef SP_STEP
-    return x;
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-    const int y = wave_scan((int)x, 0, [](int u, int v) { return (int)max((uint32_t)u, (uint32_t)v); });
-    return (uint32_t)__builtin_amdgcn_readlane(y, 63);
-}
-
 template <int WAVES>
 struct SelectScratch {
-    uint32_t hist[256];
+    __align__(16) uint32_t hist[256];
     uint32_t gt[WAVES], eq[WAVES];
 };
 template <int TEAM>
 __device__ __forceinline__ void team_sync() {
-    if constexpr (TEAM > 1) {
-        __syncthreads();
-    } else {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    }
+    if constexpr (TEAM > 1) __syncthreads();
+    else wave_sync();
 }
 
 // Writes the page ids of the k largest of n keys, the earlier among equals, in
-// order.  A team of waves (all of a workgroup, or one) finds the k-th key digit by
-// digit from the first bit in which the keys differ, by counting; then every wave
-// goes through a part of them of its own.
-template <int TEAM, typename Keys, typename Scratch>
+// order.  A team of waves (the first ones of a workgroup, the others are gone, or one)
+// finds the k-th key digit by digit from the first bit in which the keys differ, by
+// counting.  A wave goes through a part of the keys of its own, up to 64 HELD of
+// them in registers (HELD 0: any number, from where they are each time).
+template <int TEAM, int HELD, typename Keys, typename Scratch>
 __device__ __forceinline__ void take_largest(const Keys& key, int n, int k, const int32_t* pages, int32_t* out,
                                              Scratch& s) {
     const int lane = threadIdx.x & 63, wave = TEAM > 1 ? wave_id() : 0;
-    const int self = 64 * wave + lane;
-    uint32_t most = 0, least = 0xFFFFFFFFu;
-    for (int i = self; i < n; i += 64 * TEAM) {
-        const uint32_t x = key(i);
-        most = max(most, x);
-        least = min(least, x);
+    const int part = (n + 64 * TEAM - 1) / (64 * TEAM) * 64;
+    const int begin = min(n, wave * part), end = min(n, begin + part);
+    uint32_t held[HELD > 0 ? HELD : 1];
+    int32_t ids[HELD > 0 ? HELD : 1];
+    if constexpr (HELD > 0) {
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) ids[j] = pages[min(begin + 64 * j + lane, n - 1)];
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) held[j] = key(min(begin + 64 * j + lane, n - 1));
     }
+    // each(key, there, page id): 64 pages at a time, in order
+    const auto all = [&](auto each) {
+        if constexpr (HELD > 0) {
+#pragma unroll
+            for (int j = 0; j < HELD; ++j) {
+                if (begin + 64 * j >= end) break;
+                each(held[j], begin + 64 * j + lane < end, [&] { return ids[j]; });
+            }
+        } else {
+            for (int i = begin + lane; i < end + lane; i += 64) each(key(min(i, n - 1)), i < end, [&] { return pages[i]; });
+        }
+    };
+    uint32_t most = 0, rest = 0;
+    all([&](uint32_t x, bool there, auto) {
+        most = max(most, there ? x : 0u);
+        rest = max(rest, there ? ~x : 0u);
+    });
     most = wave_max(most);
-    least = ~wave_max(~least);
+    rest = wave_max(rest);
     if constexpr (TEAM > 1) {
         if (lane == 0) {
             s.gt[wave] = most;
-            s.eq[wave] = least;
+            s.eq[wave] = rest;
         }
         __syncthreads();
         for (int w = 0; w < TEAM; ++w) {
             most = max(most, s.gt[w]);
-            least = min(least, s.eq[w]);
+            rest = max(rest, s.eq[w]);
         }
     }
+    const uint32_t least = ~rest;
     // the keys that are taken for certain are above (prefix under mask), `want` of those equal to it
     uint32_t mask = 0xFFFFFFFFu, prefix = most;
     int want = k;
@@ -433,23 +504,23 @@ __device__ __forceinline__ void take_largest(const Keys& key, int n, int k, cons
         prefix &= mask;
         while (true) {
             team_sync<TEAM>();
-            for (int i = self; i < 256; i += 64 * TEAM) s.hist[i] = 0;
+            if (TEAM == 1 || wave == 0) *reinterpret_cast<u32x4_t*>(s.hist + 4 * lane) = u32x4_t{0, 0, 0, 0};
             team_sync<TEAM>();
-            for (int i = self; i < n; i += 64 * TEAM) {
-                const uint32_t x = key(i);
-                if ((x & mask) == prefix) atomicAdd(&s.hist[x >> shift & 255u], 1u);
-            }
+            all([&](uint32_t x, bool there, auto) {
+                if (there && (x & mask) == prefix) atomicAdd(&s.hist[x >> shift & 255u], 1u);
+            });
             team_sync<TEAM>();
             // digits from the largest down, four to a lane
-            int c[4], sum = 0;
-            for (int j = 0; j < 4; ++j) sum += c[j] = (int)s.hist[255 - 4 * lane - j];
+            const u32x4_t c = *reinterpret_cast<const u32x4_t*>(s.hist + 252 - 4 * lane);
+            const int sum = (int)(c[0] + c[1] + c[2] + c[3]);
             const int upto = wave_scan(sum, 0, [](int u, int v) { return u + v; });
             const int at = __ffsll((unsigned long long)__ballot(upto >= want)) - 1;
-            int above = upto - sum, digit = 255 - 4 * lane, count = c[0];
-            for (int j = 1; j < 4; ++j)
+            int above = upto - sum, digit = 255 - 4 * lane, count = (int)c[3];
+#pragma unroll
+            for (int j = 2; j >= 0; --j)
                 if (above + count < want) {
                     above += count;
-                    count = c[j];
+                    count = (int)c[j];
                     --digit;
                 }
             above = __builtin_amdgcn_readlane(above, at);
@@ -462,16 +533,13 @@ __device__ __forceinline__ void take_largest(const Keys& key, int n, int k, cons
             shift = max(0, shift - 8);
         }
     }
-    const int part = TEAM > 1 ? (n + 64 * TEAM - 1) / (64 * TEAM) * 64 : n;
-    const int begin = min(n, wave * part), end = min(n, begin + part);
     int taken = 0, equal = 0;
     if constexpr (TEAM > 1) {
         uint32_t gt = 0, eq = 0;
-        for (int i = begin + lane; i < begin + (end - begin + 63) / 64 * 64; i += 64) {
-            const uint32_t x = i < end ? key(i) & mask : 0;
-            gt += __popcll(__ballot(i < end && x > prefix));
-            eq += __popcll(__ballot(i < end && x == prefix));
-        }
+        all([&](uint32_t x, bool there, auto) {
+            gt += __popcll(__ballot(there && (x & mask) > prefix));
+            eq += __popcll(__ballot(there && (x & mask) == prefix));
+        });
         __syncthreads();
         if (lane == 0) {
             s.gt[wave] = gt;
@@ -485,20 +553,19 @@ __device__ __forceinline__ void take_largest(const Keys& key, int n, int k, cons
         taken += min(equal, want);
     }
     const unsigned long long before = (1ull << lane) - 1;
-    for (int i = begin + lane; i < begin + (end - begin + 63) / 64 * 64; i += 64) {
-        const uint32_t x = i < end ? key(i) & mask : 0;
-        const bool same = i < end && x == prefix;
+    all([&](uint32_t x, bool there, auto id) {
+        const bool same = there && (x & mask) == prefix;
         const unsigned long long eq = __ballot(same);
-        const bool take = (i < end && x > prefix) || (same && equal + __popcll(eq & before) < want);
-        const unsigned long long all = __ballot(take);
-        if (take) out[taken + __popcll(all & before)] = pages[i];
-        taken += __popcll(all);
+        const bool take = (there && (x & mask) > prefix) || (same && equal + __popcll(eq & before) < want);
+        const unsigned long long now = __ballot(take);
+        if (take) out[taken + __popcll(now & before)] = id();
+        taken += __popcll(now);
         equal += __popcll(eq);
-    }
+    });
 }
 
 // Token i's row of the result.
-template <int TEAM, typename Keys, typename Scratch>
+template <int TEAM, int HELD, typename Keys, typename Scratch>
 __device__ __forceinline__ void select_token(const SelectArgs& a, const SelectItem& it, int head, int i, const Keys& key,
                                              Scratch& s) {
     const int self = TEAM > 1 ? threadIdx.x : threadIdx.x & 63;
@@ -514,34 +581,37 @@ __device__ __forceinline__ void select_token(const SelectArgs& a, const SelectIt
         out[begin ? j : j + a.select - a.first - a.last] = it.table[begin ? j : own + 1 - a.last + j - a.first];
     }
     const int k = a.select - a.first - a.last;
-    if (k > 0) take_largest<TEAM>(key, n, k, it.table + a.first, out + a.first, s);
+    if (k == 0) return;
+    if (n <= 64 * TEAM * HELD) take_largest<TEAM, HELD>(key, n, k, it.table + a.first, out + a.first, s);
+    else take_largest<TEAM, 0>(key, n, k, it.table + a.first, out + a.first, s);
 }
 
-// Scores in LDS, and the choice, in one: of a single token (ONE) by 16 waves, which
-// have 190 KB of bounds under way between them, or of several by four, each of
-// which chooses for tokens of its own.
+// Scores in LDS, and the choice, in one: of a single token (ONE) by 16 waves, the
+// first kTeam of which choose, or of several by eight, each of which chooses for tokens of
+// its own.
+constexpr int kTeam = 4;
 template <int D, bool ONE>
-__global__ __launch_bounds__(ONE ? 1024 : 256, ONE ? 4 : 2) void select_kernel(SelectArgs a) {
-    constexpr int WAVES = ONE ? 16 : 4;
+__global__ __launch_bounds__(ONE ? 1024 : 512, 4) void select_kernel(SelectArgs a) {
+    constexpr int WAVES = ONE ? 16 : 8, R = ONE ? 1 : SP_ROW_TILES;
     extern __shared__ uint32_t keys[];
-    __shared__ SelectScratch<WAVES> s[ONE ? 1 : WAVES];
+    __shared__ SelectScratch<kTeam> s[ONE ? 1 : WAVES];
+    __shared__ ScoreLds<D, R, WAVES> lds;
     const int head = blockIdx.x % a.n_kv_heads, w = wave_id();
     SelectItem it;
     if (!load_select(a, blockIdx.x / a.n_kv_heads, it)) return;
-    const int tiles = it.tiles(a);
-    if (tiles > 0) {
-        score_pages<D, ONE ? 1 : SP_ROW_TILES, ONE ? 2 : 1>(a, it, head, w, WAVES, tiles,
-                                                            [&](int token, int page, uint32_t x, bool again) {
-                                                                uint32_t& to = keys[token * a.max_scored + page];
-                                                                to = again ? max(to, x) : x;
-                                                            });
+    if (it.scores(a)) {
+        for (int i = threadIdx.x; i < it.n * a.max_scored; i += 64 * WAVES) keys[i] = 0;  // every key is more
+        score_pages<D, R, WAVES>(a, it, head, 0, 1, lds, [&](int token, int page, uint32_t x, bool) {
+            atomicMax(&keys[token * a.max_scored + page], x);
+        });
         __syncthreads();
     }
     if constexpr (ONE) {
-        select_token<WAVES>(a, it, head, 0, [&](int page) { return keys[page]; }, s[0]);
+        if (w >= kTeam) return;  // a barrier waits for the waves that are left
+        select_token<kTeam, 8>(a, it, head, 0, [&](int page) { return keys[page]; }, s[0]);
     } else {
         for (int i = w; i < it.n; i += WAVES)
-            select_token<1>(a, it, head, i, [&](int page) { return keys[i * a.max_scored + page]; }, s[w]);
+            select_token<1, 8>(a, it, head, i, [&](int page) { return keys[i * a.max_scored + page]; }, s[w]);
     }
 }
 
@@ -549,12 +619,16 @@ __global__ __launch_bounds__(ONE ? 1024 : 256, ONE ? 4 : 2) void select_kernel(S
 constexpr int kScoreTiles = 32;  // tiles of 16 pages of a workgroup, about
 template <int D>
 __global__ __launch_bounds__(256) void score_kernel(SelectArgs a) {
+    __shared__ ScoreLds<D, 1, 4> lds;
     const int head = blockIdx.x % a.n_kv_heads;
     SelectItem it;
-    if (!load_select(a, blockIdx.x / a.n_kv_heads, it)) return;
+    if (!load_select(a, blockIdx.x / a.n_kv_heads, it) || !it.scores(a)) return;
     uint32_t* keys = a.keys + (int64_t)blockIdx.x * a.max_scored;
-    score_pages<D, 1, 2>(a, it, head, blockIdx.y * 4 + wave_id(), gridDim.y * 4, it.tiles(a),
-                         [&](int, int page, uint32_t x, bool again) { keys[page] = again ? max(keys[page], x) : x; });
+    score_pages<D, 1, 4>(a, it, head, blockIdx.y, gridDim.y, lds, [&](int, int page, uint32_t x, bool again) {
+        x = max(x, (uint32_t)__shfl_xor((int)x, 16));
+        x = max(x, (uint32_t)__shfl_xor((int)x, 32));
+        if ((threadIdx.x & 48) == 0) keys[page] = again ? max(keys[page], x) : x;
+    });
 }
 __global__ __launch_bounds__(1024) void choose_kernel(SelectArgs a) {
     __shared__ SelectScratch<16> s;
@@ -562,7 +636,7 @@ __global__ __launch_bounds__(1024) void choose_kernel(SelectArgs a) {
     SelectItem it;
     if (!load_select(a, blockIdx.x / a.n_kv_heads, it)) return;
     const uint32_t* keys = a.keys + (int64_t)blockIdx.x * a.max_scored;
-    select_token<16>(a, it, head, 0, [&](int page) { return keys[page]; }, s);
+    select_token<16, 16>(a, it, head, 0, [&](int page) { return keys[page]; }, s);
 }
 
 int32_t check_bounds(const lora_kv_bounds_t* b, const lora_attn_shape_t& s) {
@@ -656,7 +730,7 @@ extern "C" int32_t lora_sparse_select(const lora_sparse_launch_t* L, const lora_
                                       {select_kernel<128, false>, select_kernel<128, true>}};
         const size_t lds = sizeof(uint32_t) * (size_t)S.max_scored * (size_t)S.item_tokens;
         const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn[d == 128][one]),
-                                             dim3((unsigned)(S.n_items * hk)), dim3(one ? 1024 : 256), p, lds, stream);
+                                             dim3((unsigned)(S.n_items * hk)), dim3(one ? 1024 : 512), p, lds, stream);
         return e == hipSuccess ? LORA_OK : LORA_EHIP;
     }
     if (workspace_floats < I.workspace_floats) return LORA_ECAPACITY;
