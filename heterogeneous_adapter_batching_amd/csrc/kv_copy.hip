@@ -7,81 +7,67 @@
 
 namespace {
 
-// One cache's tensors: pages go from the first of each pair to the second.
+// One cache's tensors.
 struct CopyCache {
-    const char *k, *v;
-    char *k_to, *v_to;
-    const uint8_t *k_scale, *v_scale;
-    uint8_t *k_scale_to, *v_scale_to;
-    const int8_t* codes;  // bounds, or none
-    int8_t* codes_to;
-    const uint8_t* exps;
-    uint8_t* exps_to;
+    char *k, *v;
+    uint8_t *k_scale, *v_scale;
+    int8_t* codes;  // bounds, or none
+    uint8_t* exps;
 };
 struct CopyPair {
     int32_t from, to, tokens;
 };
 // Caches and pairs travel in the launch's arguments: nothing is staged, and the
-// lists are free again when the call returns.
-constexpr int kCopyCaches = 16, kCopyPairs = 192;
+// lists are free again when the call returns.  Copies within caches have one entry
+// to a cache, others the source's and, kCopyCaches / 2 on, the destination's.
+constexpr int kCopyCaches = 32, kCopyPairs = 192;
 struct CopyArgs {
     int64_t from_page, from_head, from_token, to_page, to_head, to_token;  // strides in bytes
-    int32_t n_heads, page_shift, token_blocks, bound_bytes;
+    int32_t n_heads, page_shift, token_blocks, bound_bytes, to_cache;
     CopyCache cache[kCopyCaches];
     CopyPair pair[kCopyPairs];
 };
 static_assert(sizeof(CopyArgs) <= 4096, "a kernel's arguments are at most 4 KiB");
 
-// VPR lanes take a token of a head, 16 bytes each, and a workgroup 256 / VPR
-// tokens: of one head, or where a page holds fewer of several heads side by side.
-constexpr int kCopyHeads = 4;  // such steps to a workgroup: eight loads of a lane are under way
+// VPR lanes take a token of a head, 16 bytes of its key and of its value each, and a
+// workgroup 256 / VPR tokens: of one head, or where a page holds fewer of several
+// heads side by side.  Bound by memory: 64 forks inside pages of 16 (8 kv heads,
+// bf16, 32 layers: 132 MB moved) take 24.7 us, 5.4 TB/s; 700 whole e4m3 pages of 64
+// of 4 layers, with scales and bounds (751 MB), 163 us, 4.6 TB/s in four launches.
+// Small workgroups, since all of a launch's copies are under way at once anyway: two
+// and four such steps to a workgroup take 26.5 and 27.9 us (fork).  Stores go past
+// the caches (without: 32.7 and 174); loads do not, the pages of a fork having been
+// written a step before (with: 26.3 and 155).
 template <int VPR, bool SCALES>
 __global__ __launch_bounds__(256) void kv_copy_kernel(CopyArgs a) {
     constexpr int ROWS = 256 / VPR;
-    const CopyCache& c = a.cache[blockIdx.z];
+    const CopyCache &c = a.cache[blockIdx.z], &t = a.cache[blockIdx.z + a.to_cache];
     const CopyPair p = a.pair[blockIdx.y];
     const int shift = min(a.page_shift, __builtin_ctz(ROWS));  // tokens of a workgroup
-    const int token_block = blockIdx.x % a.token_blocks, head0 = blockIdx.x / a.token_blocks * (kCopyHeads * ROWS >> shift);
     const int row = threadIdx.x / VPR, col = threadIdx.x % VPR;
-    const int token = (token_block << shift) + (row & ((1 << shift) - 1));
-    if (token < p.tokens) {
-        u32x4_t k[kCopyHeads], v[kCopyHeads];
-        uint8_t ks[kCopyHeads], vs[kCopyHeads];
-#pragma unroll
-        for (int i = 0; i < kCopyHeads; ++i) {
-            const int head = head0 + i * (ROWS >> shift) + (row >> shift);
-            if (head >= a.n_heads) break;
-            const int64_t at = p.from * a.from_page + head * a.from_head + token * a.from_token + 16 * col;
-            k[i] = *reinterpret_cast<const u32x4_t*>(c.k + at);
-            v[i] = *reinterpret_cast<const u32x4_t*>(c.v + at);
-            if (SCALES && col == 0) {
-                const int64_t s = (((int64_t)p.from * a.n_heads + head) << a.page_shift) + token;
-                ks[i] = c.k_scale[s];
-                vs[i] = c.v_scale[s];
-            }
+    const int token = ((int)(blockIdx.x % a.token_blocks) << shift) + (row & ((1 << shift) - 1));
+    const int head = (int)(blockIdx.x / a.token_blocks) * (ROWS >> shift) + (row >> shift);
+    if (token < p.tokens && head < a.n_heads) {
+        const int64_t at = p.from * a.from_page + head * a.from_head + token * a.from_token + 16 * col;
+        const int64_t to = p.to * a.to_page + head * a.to_head + token * a.to_token + 16 * col;
+        const u32x4_t k = *reinterpret_cast<const u32x4_t*>(c.k + at), v = *reinterpret_cast<const u32x4_t*>(c.v + at);
+        if (SCALES && col == 0) {
+            const int64_t s = (((int64_t)p.from * a.n_heads + head) << a.page_shift) + token;
+            const int64_t d = (((int64_t)p.to * a.n_heads + head) << a.page_shift) + token;
+            t.k_scale[d] = c.k_scale[s];
+            t.v_scale[d] = c.v_scale[s];
         }
-#pragma unroll
-        for (int i = 0; i < kCopyHeads; ++i) {
-            const int head = head0 + i * (ROWS >> shift) + (row >> shift);
-            if (head >= a.n_heads) break;
-            const int64_t at = p.to * a.to_page + head * a.to_head + token * a.to_token + 16 * col;
-            *reinterpret_cast<u32x4_t*>(c.k_to + at) = k[i];
-            *reinterpret_cast<u32x4_t*>(c.v_to + at) = v[i];
-            if (SCALES && col == 0) {
-                const int64_t s = (((int64_t)p.to * a.n_heads + head) << a.page_shift) + token;
-                c.k_scale_to[s] = ks[i];
-                c.v_scale_to[s] = vs[i];
-            }
-        }
+        __builtin_nontemporal_store(k, reinterpret_cast<u32x4_t*>(t.k + to));
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(t.v + to));
     }
     // bounds of a whole page, all heads': one workgroup of the page
     if (c.codes && blockIdx.x == 0 && p.tokens >> a.page_shift) {
         const int64_t bytes = (int64_t)a.n_heads * a.bound_bytes;
         for (int64_t i = 16 * threadIdx.x; i < bytes; i += 16 * 256)
-            *reinterpret_cast<u32x4_t*>(c.codes_to + p.to * bytes + i) =
+            *reinterpret_cast<u32x4_t*>(t.codes + p.to * bytes + i) =
                 *reinterpret_cast<const u32x4_t*>(c.codes + p.from * bytes + i);
         for (int h = threadIdx.x; h < a.n_heads; h += 256)
-            c.exps_to[(int64_t)p.to * a.n_heads + h] = c.exps[(int64_t)p.from * a.n_heads + h];
+            t.exps[(int64_t)p.to * a.n_heads + h] = c.exps[(int64_t)p.from * a.n_heads + h];
     }
 }
 
@@ -104,6 +90,10 @@ int32_t check_bounds(const lora_kv_bounds_t& b, const lora_kv_t& c) {
     if (!b.codes || !b.exps || !aligned16(b.codes)) return LORA_EINVAL;
     if (b.n_pages != c.n_pages || b.n_kv_heads != c.n_kv_heads || b.head_dim != c.head_dim) return LORA_ESHAPE;
     return LORA_OK;
+}
+CopyCache side(const lora_kv_t& c, const lora_kv_bounds_t* b) {
+    return CopyCache{static_cast<char*>(c.k), static_cast<char*>(c.v), c.k_scale, c.v_scale, b ? b->codes : nullptr,
+                     b ? b->exps : nullptr};
 }
 bool same_strides(const lora_kv_t& a, const lora_kv_t& b) {
     return a.page_stride == b.page_stride && a.head_stride == b.head_stride && a.token_stride == b.token_stride;
@@ -160,32 +150,24 @@ extern "C" int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const l
     const bool e4m3 = c.dtype == LORA_KV_E4M3;
     const int es = e4m3 ? 1 : 2, vpr = c.head_dim * es / 16, rows = 256 / vpr;
     const int32_t block = std::min(c.page_tokens, rows);  // tokens of a workgroup
-    const int32_t token_blocks = c.page_tokens / block, heads = kCopyHeads * rows / block;
+    const int32_t token_blocks = c.page_tokens / block, heads = rows / block;
     CopyArgs a;
     memset(&a, 0, sizeof(a));
     a.n_heads = c.n_kv_heads;
     a.page_shift = __builtin_ctz((unsigned)c.page_tokens);
     a.token_blocks = token_blocks;
     a.bound_bytes = 2 * c.head_dim;
+    const int32_t most = to ? kCopyCaches / 2 : kCopyCaches;  // caches of a launch
+    a.to_cache = to ? most : 0;
     typedef void (*fn_t)(CopyArgs);
     const fn_t fn = e4m3 ? (vpr == 8 ? kv_copy_kernel<8, true> : kv_copy_kernel<4, true>)
                          : (vpr == 16 ? kv_copy_kernel<16, false> : kv_copy_kernel<8, false>);
     const unsigned gx = (unsigned)(token_blocks * ((c.n_kv_heads + heads - 1) / heads));
     for (int32_t i = 0; i < n_caches;) {
         int32_t n = 0;  // caches of one launch: those on end with the same strides
-        for (; i + n < n_caches && n < kCopyCaches && same_strides(from[i], from[i + n]) && same_strides(dst[i], dst[i + n]);
-             ++n) {
-            const lora_kv_t &f = from[i + n], &t = dst[i + n];
-            CopyCache& x = a.cache[n];
-            x = CopyCache{static_cast<const char*>(f.k), static_cast<const char*>(f.v), static_cast<char*>(t.k),
-                          static_cast<char*>(t.v), f.k_scale, f.v_scale, t.k_scale, t.v_scale, nullptr, nullptr, nullptr,
-                          nullptr};
-            if (from_bounds) {
-                x.codes = from_bounds[i + n].codes;
-                x.exps = from_bounds[i + n].exps;
-                x.codes_to = dst_bounds[i + n].codes;
-                x.exps_to = dst_bounds[i + n].exps;
-            }
+        for (; i + n < n_caches && n < most && same_strides(from[i], from[i + n]) && same_strides(dst[i], dst[i + n]); ++n) {
+            a.cache[n] = side(from[i + n], from_bounds ? from_bounds + i + n : nullptr);
+            if (to) a.cache[n + most] = side(to[i + n], to_bounds ? to_bounds + i + n : nullptr);
         }
         a.from_page = from[i].page_stride * es;
         a.from_head = from[i].head_stride * es;

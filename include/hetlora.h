@@ -905,7 +905,7 @@ int32_t lora_attn(const lora_attn_launch_t* launch, const lora_kv_t* kv,
  *             pair at most, and within a cache (to NULL, or of the same memory)
  *             no page that is written is also read
  * Caches of different memory must not overlap.  One launch for each 192 pairs of
- * 16 caches with the same strides.  Errors: LORA_EINVAL, LORA_ESHAPE, LORA_EPAGE,
+ * 32 caches with the same strides (16 with to).  Errors: LORA_EINVAL, LORA_ESHAPE, LORA_EPAGE,
  * LORA_ENOMEM, LORA_EHIP. */
 int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const lora_kv_t* to,
                      const lora_kv_bounds_t* from_bounds, const lora_kv_bounds_t* to_bounds,
