@@ -1,4 +1,6 @@
 // gfx950 kernel that copies pages of a paged cache, and its C entry point.
+#include <stddef.h>
+
 #include <algorithm>
 #include <new>
 #include <vector>
@@ -19,15 +21,20 @@ struct CopyPair {
 };
 // Caches and pairs travel in the launch's arguments: nothing is staged, and the
 // lists are free again when the call returns.  Copies within caches have one entry
-// to a cache, others the source's and, kCopyCaches / 2 on, the destination's.
-constexpr int kCopyCaches = 32, kCopyPairs = 192;
+// to a cache, others the source's and, CACHES / 2 on, the destination's.  A launch
+// with the few pairs of a decode step has short arguments
+// (one pair in one cache: 4.1 us for 4.5, and 19 for 25 when it is waited for).
+template <int CACHES, int PAIRS>
 struct CopyArgs {
+    static constexpr int kCaches = CACHES, kPairs = PAIRS;
     int64_t from_page, from_head, from_token, to_page, to_head, to_token;  // strides in bytes
     int32_t n_heads, page_shift, token_blocks, bound_bytes, to_cache;
-    CopyCache cache[kCopyCaches];
-    CopyPair pair[kCopyPairs];
+    CopyCache cache[CACHES];
+    CopyPair pair[PAIRS];
 };
-static_assert(sizeof(CopyArgs) <= 4096, "a kernel's arguments are at most 4 KiB");
+typedef CopyArgs<8, 16> CopyFew;
+typedef CopyArgs<32, 192> CopyMany;
+static_assert(sizeof(CopyMany) <= 4096, "a kernel's arguments are at most 4 KiB");
 
 // VPR lanes take a token of a head, 16 bytes of its key and of its value each, and a
 // workgroup 256 / VPR tokens: of one head, or where a page holds fewer of several
@@ -38,8 +45,8 @@ static_assert(sizeof(CopyArgs) <= 4096, "a kernel's arguments are at most 4 KiB"
 // and four such steps to a workgroup take 26.5 and 27.9 us (fork).  Stores go past
 // the caches (without: 32.7 and 174); loads do not, the pages of a fork having been
 // written a step before (with: 26.3 and 155).
-template <int VPR, bool SCALES>
-__global__ __launch_bounds__(256) void kv_copy_kernel(CopyArgs a) {
+template <int VPR, bool SCALES, typename Args>
+__global__ __launch_bounds__(256) void kv_copy_kernel(Args a) {
     constexpr int ROWS = 256 / VPR;
     const CopyCache &c = a.cache[blockIdx.z], &t = a.cache[blockIdx.z + a.to_cache];
     const CopyPair p = a.pair[blockIdx.y];
@@ -120,6 +127,55 @@ int32_t check_pairs(int32_t n, const int32_t* from, const int32_t* to, const int
     return LORA_OK;
 }
 
+// Every argument has been checked; within caches (not `across`) `to` is `from`.
+template <typename Args>
+int32_t copy_pages(bool across, int32_t n_caches, const lora_kv_t* from, const lora_kv_t* to, const lora_kv_bounds_t* from_bounds,
+                   const lora_kv_bounds_t* to_bounds, int32_t n_pairs, const int32_t* from_page, const int32_t* to_page,
+                   const int32_t* tokens, void* hip_stream) {
+    const lora_kv_t& c = from[0];
+    const bool e4m3 = c.dtype == LORA_KV_E4M3;
+    const int es = e4m3 ? 1 : 2, vpr = c.head_dim * es / 16, rows = 256 / vpr;
+    const int32_t block = std::min(c.page_tokens, rows);  // tokens of a workgroup
+    const int32_t token_blocks = c.page_tokens / block, heads = rows / block;
+    Args a;
+    memset(&a, 0, offsetof(Args, cache));
+    a.n_heads = c.n_kv_heads;
+    a.page_shift = __builtin_ctz((unsigned)c.page_tokens);
+    a.token_blocks = token_blocks;
+    a.bound_bytes = 2 * c.head_dim;
+    const int32_t most = across ? Args::kCaches / 2 : Args::kCaches;  // caches of a launch
+    a.to_cache = across ? most : 0;
+    typedef void (*fn_t)(Args);
+    const fn_t fn = e4m3 ? (vpr == 8 ? kv_copy_kernel<8, true, Args> : kv_copy_kernel<4, true, Args>)
+                         : (vpr == 16 ? kv_copy_kernel<16, false, Args> : kv_copy_kernel<8, false, Args>);
+    const unsigned gx = (unsigned)(token_blocks * ((c.n_kv_heads + heads - 1) / heads));
+    for (int32_t i = 0; i < n_caches;) {
+        int32_t n = 0;  // caches of one launch: those on end with the same strides
+        for (; i + n < n_caches && n < most && same_strides(from[i], from[i + n]) && same_strides(to[i], to[i + n]); ++n) {
+            a.cache[n] = side(from[i + n], from_bounds ? from_bounds + i + n : nullptr);
+            if (across) a.cache[n + most] = side(to[i + n], to_bounds ? to_bounds + i + n : nullptr);
+        }
+        a.from_page = from[i].page_stride * es;
+        a.from_head = from[i].head_stride * es;
+        a.from_token = from[i].token_stride * es;
+        a.to_page = to[i].page_stride * es;
+        a.to_head = to[i].head_stride * es;
+        a.to_token = to[i].token_stride * es;
+        for (int32_t j = 0; j < n_pairs;) {
+            int32_t m = 0;
+            for (; j < n_pairs && m < Args::kPairs; ++j) {
+                const int32_t count = tokens ? tokens[j] : c.page_tokens;
+                if (count > 0) a.pair[m++] = CopyPair{from_page[j], to_page[j], count};
+            }
+            if (m > 0 && launch(fn, dim3(gx, (unsigned)m, (unsigned)n), dim3(256),
+                                reinterpret_cast<hipStream_t>(hip_stream), a) != hipSuccess)
+                return LORA_EHIP;
+        }
+        i += n;
+    }
+    return LORA_OK;
+}
+
 }  // namespace
 
 extern "C" int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const lora_kv_t* to,
@@ -147,45 +203,7 @@ extern "C" int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const l
     const int32_t st = check_pairs(n_pairs, from_page, to_page, tokens, c.n_pages, dst->n_pages, c.page_tokens, shared);
     if (st != LORA_OK) return st;
 
-    const bool e4m3 = c.dtype == LORA_KV_E4M3;
-    const int es = e4m3 ? 1 : 2, vpr = c.head_dim * es / 16, rows = 256 / vpr;
-    const int32_t block = std::min(c.page_tokens, rows);  // tokens of a workgroup
-    const int32_t token_blocks = c.page_tokens / block, heads = rows / block;
-    CopyArgs a;
-    memset(&a, 0, sizeof(a));
-    a.n_heads = c.n_kv_heads;
-    a.page_shift = __builtin_ctz((unsigned)c.page_tokens);
-    a.token_blocks = token_blocks;
-    a.bound_bytes = 2 * c.head_dim;
-    const int32_t most = to ? kCopyCaches / 2 : kCopyCaches;  // caches of a launch
-    a.to_cache = to ? most : 0;
-    typedef void (*fn_t)(CopyArgs);
-    const fn_t fn = e4m3 ? (vpr == 8 ? kv_copy_kernel<8, true> : kv_copy_kernel<4, true>)
-                         : (vpr == 16 ? kv_copy_kernel<16, false> : kv_copy_kernel<8, false>);
-    const unsigned gx = (unsigned)(token_blocks * ((c.n_kv_heads + heads - 1) / heads));
-    for (int32_t i = 0; i < n_caches;) {
-        int32_t n = 0;  // caches of one launch: those on end with the same strides
-        for (; i + n < n_caches && n < most && same_strides(from[i], from[i + n]) && same_strides(dst[i], dst[i + n]); ++n) {
-            a.cache[n] = side(from[i + n], from_bounds ? from_bounds + i + n : nullptr);
-            if (to) a.cache[n + most] = side(to[i + n], to_bounds ? to_bounds + i + n : nullptr);
-        }
-        a.from_page = from[i].page_stride * es;
-        a.from_head = from[i].head_stride * es;
-        a.from_token = from[i].token_stride * es;
-        a.to_page = dst[i].page_stride * es;
-        a.to_head = dst[i].head_stride * es;
-        a.to_token = dst[i].token_stride * es;
-        for (int32_t j = 0; j < n_pairs;) {
-            int32_t m = 0;
-            for (; j < n_pairs && m < kCopyPairs; ++j) {
-                const int32_t count = tokens ? tokens[j] : c.page_tokens;
-                if (count > 0) a.pair[m++] = CopyPair{from_page[j], to_page[j], count};
-            }
-            if (m > 0 && launch(fn, dim3(gx, (unsigned)m, (unsigned)n), dim3(256),
-                                reinterpret_cast<hipStream_t>(hip_stream), a) != hipSuccess)
-                return LORA_EHIP;
-        }
-        i += n;
-    }
-    return LORA_OK;
+    const int32_t most = to ? CopyFew::kCaches / 2 : CopyFew::kCaches;
+    const auto copy = n_pairs <= CopyFew::kPairs && n_caches <= most ? copy_pages<CopyFew> : copy_pages<CopyMany>;
+    return copy(to != nullptr, n_caches, from, dst, from_bounds, dst_bounds, n_pairs, from_page, to_page, tokens, hip_stream);
 }

@@ -88,6 +88,25 @@ def test_to_other_caches(dtype):
     run_case(10, caches, to=to, whole=True)
 
 
+def test_bounds_to_others_of_the_same_cache():
+    """The same caches on both sides, bounds of different memory; few pairs and many."""
+    rng = np.random.default_rng(11)
+    cache = make_cache(rng, 80, 2, 16, 64, "bf16")
+    for pairs in (5, 30):
+        order = rng.permutation(80)
+        src, dst = order[:pairs], order[pairs:2 * pairs]
+        a, b = make_bounds(rng, cache), make_bounds(rng, cache)
+        before, codes, exps = raw(cache), b.codes.clone(), b.exps.clone()
+        kept = a.codes.clone()
+        copy = KvCopy([cache], [a], [cache], [b])
+        copy._args = (copy._args[0], copy._args[0], *copy._args[2:])  # one array for both sides
+        copy.copy(src, dst)
+        torch.cuda.synchronize()
+        check(before, before, raw(cache), src, dst, [16] * pairs, 16)
+        codes[dst], exps[dst] = a.codes[src], a.exps[src]
+        assert torch.equal(b.codes, codes) and torch.equal(b.exps, exps) and torch.equal(a.codes, kept)
+
+
 def test_one_page_to_many():
     rng = np.random.default_rng(5)
     run_case(9, [make_cache(rng, 20, 2, 16, 128, "bf16")], one_source=True)
