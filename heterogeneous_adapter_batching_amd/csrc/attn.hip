@@ -113,48 +113,63 @@ __device__ __forceinline__ float finite_abs(float x) {
     x = fabsf(x);
     return x < INFINITY ? x : 0.f;
 }
-// The e4m3 code of x * inv (inv a power of two), as lora_kv_t describes it.
-__device__ __forceinline__ float e4m3_input(float x, float inv) {
-    const float y = fminf(fmaxf(x * inv, -448.f), 448.f);
-    return fabsf(x) < INFINITY ? y : __builtin_nanf("");
+// f over the 8 or 16 lanes that a head lies in, the same in all of them: neighbours,
+// pairs, fours and eights swapped by moves between lanes.
+template <int LPV, typename T, typename F>
+__device__ __forceinline__ T head_reduce(T x, F f) {
+#define AT_SWAP(ctrl) \
+    x = f(x, __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, 0xF, 0xF, true)))
+    AT_SWAP(0xB1);
+    AT_SWAP(0x4E);
+    AT_SWAP(0x141);
+    if constexpr (LPV == 16) AT_SWAP(0x140);
+#undef AT_SWAP
+    return x;
 }
-
-// The sum of all elements of a head that lies in LPV lanes.
 template <int LPV>
 __device__ __forceinline__ float head_sum(f32x4_t x, f32x4_t y) {
     x += y;
-    float t = (x[0] + x[1]) + (x[2] + x[3]);
-#pragma unroll
-    for (int o = 1; o < LPV; o <<= 1) t += __shfl_xor(t, o);
-    return t;
+    return head_reduce<LPV>((x[0] + x[1]) + (x[2] + x[3]), [](float u, float v) { return u + v; });
+}
+template <int LPV, typename T>
+__device__ __forceinline__ T head_max(T x) {
+    return head_reduce<LPV>(x, [](T u, T v) { return max(u, v); });
 }
 // x and y, a lane's elements of a head, become (x - m) / sqrt(mean((x - m)^2) + eps)
-// times their weights, m the head's mean (CENTRED) or zero.  The head is scaled
-// by the power of two of its largest element first, so that squares of the
-// largest and smallest elements stay in range; down to 2^-40 only, where the
-// squares are nothing beside eps (2^80 eps after the scaling) or still in range.
-// The sum under the root is at least the least normal number: a centred head of
-// equal elements is zero, though its scaled eps may have gone under.
+// times their weights, m the head's mean (CENTRED) or zero.  Where squares leave the
+// middle of fp32's range in any head of the wave, all are scaled by the power of two
+// of their largest element first; down to 2^-40 only, where the squares are nothing
+// beside eps (2^80 eps after the scaling) or still in range.  The sum under the root
+// is at least the least normal number: a centred head of equal elements is zero,
+// though its scaled eps may have gone under.
 template <int LPV, bool CENTRED>
 __device__ __forceinline__ void norm_head(f32x4_t& x, f32x4_t& y, f32x4_t wx, f32x4_t wy, float eps) {
-    float top = 0.f;
+    const auto squares = [](f32x4_t& u, f32x4_t& v) {
+        if (CENTRED) {
+            const float m = head_sum<LPV>(u, v) * (1.f / (8 * LPV));
+            u -= m;
+            v -= m;
+        }
+        return head_sum<LPV>(u * u, v * v) * (1.f / (8 * LPV));
+    };
+    f32x4_t u = x, v = y;
+    float sum = squares(u, v);
+    if (__ballot(!(sum >= 8.6736174e-19f && sum <= 1.2676506e30f))) {  // 2^-60, 2^100
+        float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(y[j])));
-#pragma unroll
-    for (int o = 1; o < LPV; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-    const int t = min(max((int)(__float_as_uint(top) >> 23) - 127, -40), 126);
-    const float unit = __uint_as_float((uint32_t)(127 - t) << 23);
-    x *= unit;
-    y *= unit;
-    if (CENTRED) {
-        const float m = head_sum<LPV>(x, y) * (1.f / (8 * LPV));
-        x -= m;
-        y -= m;
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(y[j])));
+        top = head_max<LPV>(top);
+        const int t = min(max((int)(__float_as_uint(top) >> 23) - 127, -40), 126);
+        const float unit = __uint_as_float((uint32_t)(127 - t) << 23);
+        u = x * unit;
+        v = y * unit;
+        sum = squares(u, v);
+        eps = eps * unit * unit;
     }
-    const float sum = head_sum<LPV>(x * x, y * y) * (1.f / (8 * LPV)) + eps * unit * unit;
+    sum += eps;
     const float r = __builtin_amdgcn_rsqf(sum < 1.17549435e-38f ? 1.17549435e-38f : sum);  // NaN stays
-    x = x * r * wx;
-    y = y * r * wy;
+    x = u * r * wx;
+    y = v * r * wy;
 }
 
 // D/8 lanes take one head's vector, 8 elements each: the pair elements c and c +
@@ -163,7 +178,10 @@ __device__ __forceinline__ void norm_head(f32x4_t& x, f32x4_t& y, f32x4_t wx, f3
 // every product is rounded, as in the formula's plain evaluation in fp32, so
 // that codes next to a rounding border do not depend on how it is evaluated.
 // Bound by memory: 16 prompts of 128 to 2048 tokens (32 heads, fp32 in, e4m3
-// cache) take 96 us, 5.8 TB/s; 64 single tokens 4 us, a launch.
+// cache) take 96 us, 5.8 TB/s; 64 single tokens 4 us, a launch.  With norms (bf16 in)
+// the same prompts take 77 us, 4.5 TB/s, with the arithmetic close behind: 88 with
+// sums over lanes by way of LDS, 82 with every head scaled first and every element
+// asked whether it is finite; two heads to a lane 79, four 115.
 template <int D, bool F32, bool E4M3, int NORM>
 __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
     constexpr int LPV = D / 8, VPB = 256 / LPV;
@@ -214,22 +232,42 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
         *reinterpret_cast<u32x2_t*>(o + c0) = u32x2_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
         *reinterpret_cast<u32x2_t*>(o + c1) = u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
     } else {
-        float top = 0.f;
+        // the largest |x|, as bits; what is not finite comes out above all that is
+        uint32_t bits = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(finite_abs(x[j]), finite_abs(y[j])));
+        for (int j = 0; j < 4; ++j)
+            bits = max(bits, max(__float_as_uint(x[j]) & 0x7FFFFFFFu, __float_as_uint(y[j]) & 0x7FFFFFFFu));
+        bits = head_max<LPV>(bits);
+        const bool odd = __ballot(bits >= 0x7F800000u) != 0;  // in any head of the wave
+        if (odd) {
+            float top = 0.f;
 #pragma unroll
-        for (int o = 1; o < LPV; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+            for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(finite_abs(x[j]), finite_abs(y[j])));
+            bits = head_max<LPV>(__float_as_uint(top));
+        }
         // least e with top <= 1.75 * 2^8 * 2^e, from the bits of top = m * 2^t
         // (a subnormal top reads as t = -127, which the clamp covers)
-        const uint32_t bits = __float_as_uint(top);
         int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
         e = min(max(e, -100), 119);
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        f32x4_t u, v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u[j] = __builtin_amdgcn_fmed3f(x[j] * inv, -448.f, 448.f);
+            v[j] = __builtin_amdgcn_fmed3f(y[j] * inv, -448.f, 448.f);
+        }
+        if (odd) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u[j] = fabsf(x[j]) < INFINITY ? u[j] : __builtin_nanf("");
+                v[j] = fabsf(y[j]) < INFINITY ? v[j] : __builtin_nanf("");
+            }
+        }
         uint32_t lo = 0, hi = 0;
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_input(x[0], inv), e4m3_input(x[1], inv), lo, false);
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_input(x[2], inv), e4m3_input(x[3], inv), lo, true);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_input(y[0], inv), e4m3_input(y[1], inv), hi, false);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_input(y[2], inv), e4m3_input(y[3], inv), hi, true);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(u[0], u[1], lo, false);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(u[2], u[3], lo, true);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], hi, false);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], hi, true);
         if (!held) return;
         char* o = cache + kv_off(a.kv, page, head, place);
         *reinterpret_cast<uint32_t*>(o + c0) = lo;
