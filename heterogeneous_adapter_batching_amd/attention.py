@@ -136,7 +136,7 @@ class AttnBatch:
             t.record_stream(s)
 
     def __del__(self):
-        if sys.is_finalizing() or not hasattr(self, "_host"):
+        if sys is None or sys.is_finalizing() or not hasattr(self, "_host"):  # None: past the end of the interpreter
             return
         if self._pending:
             _held.append((self._host, self._copied))

@@ -1182,7 +1182,7 @@ struct StagedTile {
 };
 
 // SHARE waves take the item's tiles in turn.  Tiles of a wave that is alone with its
-// item (SHARE 1) are StagedTiles: vt has the values, and behind them the keys.
+// item (SHARE 1) are StagedTiles: vt has the keys, and then the values.
 template <int D, bool E4M3, bool CAREFUL, int SHARE>
 __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, int pos, int p_lo, int p_hi, int head,
                                             int w, const u32x4_t (&qf)[D / 32], char* vt, f32x4_t (&acc)[D / 16],
@@ -1209,7 +1209,14 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
         const int t0 = tile(i);
         f32x4_t s[2] = {f32x4_t{}, f32x4_t{}};
         if constexpr (STAGED) {
-            x.store_k(vt + T * RB);
+            wave_sync();
+            x.store_k(vt);
+            wave_sync();
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) s[b] = mfma16(Tile::key(vt, b, k), qf[k], s[b]);
+            wave_sync();
         } else {
 #pragma unroll
             for (int k = 0; k < KS; ++k)
@@ -1222,12 +1229,6 @@ __device__ __forceinline__ bool narrow_pass(const AttnArgs& a, const Item& it, i
             x.look_up(a.kv, it, tile(i + 2));
             x.load_k(a.kv, head);
             x.load_v(a.kv, head);
-        }
-        if constexpr (STAGED) {
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) s[b] = mfma16(Tile::key(vt + T * RB, b, k), qf[k], s[b]);
         }
         if (none_sees(a, p_lo, p_hi, t0, t0 + T - 1)) continue;
 
@@ -1407,13 +1408,16 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
     }
 }
 
-// The same with a wave to an item, for many items: those that are under way at
-// once are four times as many, so that neighbours which see the same pages (of a
-// sparse attention) find them in the caches more often, and nothing is joined.
+// The same with a wave to an item, for many items (of a sparse attention: the pages
+// that many tokens see come from the L2, and its loads have to be wide to be fast).
+// Nothing is joined.  920 new tokens of 64/8 heads, 16 pages of 64 in 33k tokens, take
+// 226 us, 3.9 GB of keys and values at 17 TB/s: 77% of them from the L2, the LDS, which a
+// tile passes twice, busy most of the time (e4m3 takes as long).  The narrow kernel
+// takes 458, and as long with a wave to an item: its loads are served 16 bytes at a time.
 template <int D, bool E4M3>
-__global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_solo_kernel(AttnArgs a, int32_t n_items) {
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_solo_kernel(AttnArgs a, int32_t n_items) {
     constexpr int DB = D / 16, KS = D / 32, T = 32;
-    __shared__ __align__(16) char lds[4][2 * T * 2 * D];
+    __shared__ __align__(16) char lds[4][T * 2 * D];
     const int head = blockIdx.x % a.kv.n_kv_heads, lane = threadIdx.x & 63, w = wave_id();
     const int col = lane & 15, g = lane >> 4, item = 4 * (blockIdx.x / a.kv.n_kv_heads) + w;
     Item it;
@@ -1706,7 +1710,17 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     return LORA_OK;
 }
 
-constexpr int64_t kSoloItems = 2048;
+// Items (of all kv heads) from which on each has a wave to itself.  us for 1024, 2048
+// and 4096 items of 16 pages of 64, shared by four waves and a wave each:
+//   head_dim 128, bf16   64/40    119/58    230/111   (512: 34/37)
+//                 e4m3   39/45     70/60    130/111
+//             64, bf16   31/30     61/36    117/55    (512: 17/29)
+//                 e4m3   19/30     32/40     58/60    (8192: 112/110): never
+int64_t solo_items(const lora_kv_t& kv) {
+    if (kv.dtype == LORA_KV_BF16) return kv.head_dim == 128 ? 768 : 1024;
+    return kv.head_dim == 128 ? 2048 : INT64_MAX;
+}
+
 
 extern "C" int32_t lora_sparse_attn(const lora_sparse_launch_t* L, const lora_kv_t* kv, const uint16_t* q, int64_t ldq,
                                     const int32_t* selected, uint16_t* out, int64_t ldo, float scale, float* workspace,
@@ -1736,13 +1750,11 @@ extern "C" int32_t lora_sparse_attn(const lora_sparse_launch_t* L, const lora_kv
     a.work = reinterpret_cast<const lora_attn_work_t*>(L->attn.meta + S.off_work);
     const bool e4m3 = kv->dtype == LORA_KV_E4M3;
     // (a page's rows lie within 32 bits of its first one)
-    if ((int64_t)S.n_work * hk >= kSoloItems && kv->token_stride <= INT32_MAX / 2048) {
-        typedef void (*fn_t)(AttnArgs, int32_t);
-        static const fn_t solo[2][2] = {{attn_solo_kernel<64, false>, attn_solo_kernel<64, true>},
-                                        {attn_solo_kernel<128, false>, attn_solo_kernel<128, true>}};
+    if ((int64_t)S.n_work * hk >= solo_items(*kv) && kv->token_stride <= INT32_MAX / 2048) {
+        const auto solo = d == 64 ? attn_solo_kernel<64, false> : e4m3 ? attn_solo_kernel<128, true> : attn_solo_kernel<128, false>;
         int32_t n = S.n_work;
         void* p[] = {&a, &n};
-        if (hipLaunchKernel(reinterpret_cast<const void*>(solo[d == 128][e4m3]), dim3((unsigned)((n + 3) / 4 * hk)),
+        if (hipLaunchKernel(reinterpret_cast<const void*>(solo), dim3((unsigned)((n + 3) / 4 * hk)),
                             dim3(256), p, 0, s) != hipSuccess)
             return LORA_EHIP;
     } else if (launch(kNarrow.narrow[d == 128][e4m3], dim3((unsigned)(S.n_work * hk)), dim3(256), s, a) != hipSuccess) {
