@@ -62,13 +62,12 @@ struct PageBounds {
         const char* base = c.k + (E4M3 ? 1 : 2) * kv_off(c, page, head, 0) + 16 * (lane % LPT);
         const uint8_t* scales = c.k_scale + (E4M3 ? scale_off(c, page, head, 0) : 0);
         const int64_t step = (E4M3 ? 1 : 2) * c.token_stride;
-        for (int t = lane / LPT; t < n; t += AHEAD * TOKENS) {
+        for (int t = AHEAD * (lane / LPT); t < n; t += AHEAD * TOKENS) {  // n is a multiple of AHEAD
             u32x4_t x[AHEAD][N / 4];
+            uint32_t exps = 0;
+            if constexpr (E4M3) __builtin_memcpy(&exps, scales + t, AHEAD);
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int token = min(t + i * TOKENS, n - 1);  // the last one again changes nothing
-                values(base + token * step, E4M3 ? scales[token] : 0, x[i]);
-            }
+            for (int i = 0; i < AHEAD; ++i) values(base + (t + i) * step, exps >> 8 * i & 255, x[i]);
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) use(x[i]);
         }
