@@ -68,13 +68,25 @@ AT_FN int at_inside(const lora_attn_work_t* w, int32_t n_seq, int32_t n_rows, in
 // ------------------------------------------------------------------ sparse attention
 #define SP_MIN_PAGE 16       // fewest tokens of a page: under that its bounds are as much as its keys
 #define SP_EXP 100           // exponents of bounds are within +-SP_EXP
-// Keys (scores) that a selecting workgroup holds in LDS at most, and tiles of 16
-// rows (query heads of its tokens) that it scores at once.
+// Keys (scores) that a selecting workgroup of several tokens holds in LDS at most, and
+// tiles of 16 rows (query heads of its tokens) that it scores one after another.
+// (512 tokens over 16000 in pages of 32, 32/8 heads: one tile at a time 24.3 us, two
+// 14.6, four 19.0, eight 54: then too few workgroups are left to fill the chip.)
 #define SP_LDS_KEYS 12288
 #define SP_ROW_TILES 2
-#define SP_SLAB_KEYS (1 << 24)  // keys in memory at once, where LDS does not hold one token's
+// Of a single token's keys, which one workgroup scores where it holds them; more are
+// scored by many workgroups, into memory, and chosen from by another launch.  us in
+// LDS and through memory, one token of each sequence, 8 kv heads of 8 query heads:
+//   pages         500       1000       2000       4000       8000
+//   1 sequence   7.5/11.9   9.9/12.7  14.5/13.4  28.6/14.9  50.7/16.7
+//   16           8.0/12.5  11.3/14.3  18.3/20.3  37.4/30.6  73.5/55.7
+//   64          18.8/23.5  29.7/34.2  53.2/59.4
+#define SP_ONE_KEYS 2048
+#define SP_SLAB_KEYS (1 << 24)  // keys in memory at once
 
-AT_FN int sp_in_lds(int32_t max_scored, int32_t item_tokens) { return (int64_t)max_scored * item_tokens <= SP_LDS_KEYS; }
+AT_FN int sp_in_lds(int32_t max_scored, int32_t item_tokens) {
+    return (int64_t)max_scored * item_tokens <= (item_tokens > 1 ? SP_LDS_KEYS : SP_ONE_KEYS);
+}
 // items of one launch, where the keys of each (of one token, all heads') go through memory
 AT_FN int64_t sp_slab(int64_t per_item, int64_t n_items) {
     const int64_t fit = SP_SLAB_KEYS / per_item;

@@ -226,7 +226,7 @@ def test_pages_past_what_lds_holds(heads, kv_heads, new):
     q = normal(rng, new, heads * 64)
     bounds = KvBounds.empty(cache)
     batch = SparseBatch(cache, heads, 100).refresh([new], [16 * n - 3], table, bounded=[0])
-    assert not batch.sparse_info.max_scored * batch.sparse_info.item_tokens <= 12288
+    assert batch.sparse_info.item_tokens == 1 and batch.sparse_info.max_scored > 12288
     batch.bounds(bounds)
     chosen, out = batch.empty_selected(), torch.zeros_like(q)
     batch.select(q, bounds, chosen)
@@ -239,6 +239,22 @@ def test_pages_past_what_lds_holds(heads, kv_heads, new):
     want = expected_choice(batch, bounds, table, q, [new], [16 * n - 3])
     assert np.array_equal(chosen.cpu().numpy(), want)
     check(out, *expected_out(cache, q, want, [new], [16 * n - 3], heads, 0.125))
+
+
+@pytest.mark.parametrize("heads,kv_heads,new,kv", [(8, 8, 70, 16 * 2400), (2, 2, 300, 16 * 2500), (6, 1, 1, 16 * 2050)])
+def test_many_pages(heads, kv_heads, new, kv):
+    """Tokens on either side of what LDS holds of one, and of several at once."""
+    rng = np.random.default_rng(kv)
+    n = kv // 16
+    cache = make_cache(rng, n, kv_heads, 16, 64, "bf16")
+    table, q = rng.permutation(n).astype(np.int32)[None], normal(rng, new, heads * 64)
+    bounds = KvBounds.empty(cache)
+    batch = SparseBatch(cache, heads, 40, 2, 3).refresh([new], [kv], table, bounded=[0])
+    batch.bounds(bounds)
+    chosen = batch.empty_selected()
+    batch.select(q, bounds, chosen)
+    torch.cuda.synchronize()
+    assert np.array_equal(chosen.cpu().numpy(), expected_choice(batch, bounds, table, q, [new], [kv]))
 
 
 def test_split_contexts():

@@ -42,6 +42,8 @@ def check_sparse(s, sp, q_len, kv_len, table, bounded, staging, attn, info):
     while pad < min(group, 16):
         pad *= 2
     assert info.item_tokens * pad <= 64 and (info.item_tokens == 1 or info.item_tokens * info.max_scored <= 12288)
+    if info.item_tokens == 1 and info.max_scored > 2048:  # through memory
+        assert attn.workspace_floats >= hk * info.max_scored
     # attention items: every row and head over every tile once
     tiles, parts = {}, 0
     for w in ints(staging, info.off_work, info.n_work, hl.ATTN_WORK_INTS):
