@@ -1411,9 +1411,12 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
 // The same with a wave to an item, for many items (of a sparse attention: the pages
 // that many tokens see come from the L2, and its loads have to be wide to be fast).
 // Nothing is joined.  920 new tokens of 64/8 heads, 16 pages of 64 in 33k tokens, take
-// 226 us, 3.9 GB of keys and values at 17 TB/s: 77% of them from the L2, the LDS, which a
-// tile passes twice, busy most of the time (e4m3 takes as long).  The narrow kernel
-// takes 458, and as long with a wave to an item: its loads are served 16 bytes at a time.
+// 226 us, 3.9 GB of keys and values at 17 TB/s, 77% of them from the L2: a compute unit
+// takes 340 cycles for a tile, of which the path of its loads needs 256 (64 bytes a
+// cycle), LDS as many, and no wave waits for memory (e4m3 takes as long: its LDS traffic
+// is the same).  The narrow kernel takes 458, and as long with a wave to an item: its
+// loads are served 16 bytes at a time.  Keys turned by moves between lanes, past LDS:
+// 235; the values of the next tile sent for after this one's product: 255.
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_solo_kernel(AttnArgs a, int32_t n_items) {
     constexpr int DB = D / 16, KS = D / 32, T = 32;
