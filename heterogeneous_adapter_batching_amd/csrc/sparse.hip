@@ -40,7 +40,12 @@ struct BoundsArgs {
 
 // A wave takes a page of one head: 16 bytes of a token to a lane, so LPT lanes to
 // a token and 64 / LPT tokens at once, joined over the lanes at the end.  Largest
-// and smallest are kept as ordered 16-bit integers, two to a register.
+// and smallest are kept as ordered 16-bit integers, two to a register: three
+// instructions an element and a half.  Bound by memory: the pages of 48 sequences of
+// up to 16384 tokens (8 kv heads, e4m3, pages of 64, 167 MB) take 38 us, 4.4 TB/s, those
+// of 16 prompts of up to 2048 (32 heads, bf16, pages of 16, 73 MB, part of them in the
+// caches) 13.1 us, 5.5 TB/s.  Two or eight loads of a lane under way instead of four: 41
+// and 38 us for the first; loads past the caches 34 and 14.2 us.
 template <int D, bool E4M3>
 struct PageBounds {
     static constexpr int LPT = D * (E4M3 ? 1 : 2) / 16, TOKENS = 64 / LPT, N = E4M3 ? 8 : 4;  // registers of elements
@@ -587,7 +592,13 @@ __device__ __forceinline__ void select_token(const SelectArgs& a, const SelectIt
 
 // Scores in LDS, and the choice, in one: of a single token (ONE) by 16 waves, the
 // first kTeam of which choose, or of several by eight, each of which chooses for tokens of
-// its own.
+// its own.  The bounds' bytes are what has to move, but a call ends long before they
+// bound it: one token over 500 pages, 8 kv heads, takes 7.5 us, of which 3 are a launch
+// and most of the rest the first pass through the code and the chain item, page ids,
+// bounds; 32 tokens over up to 2048 pages of 16 16.3 us, 2.4 TB/s; 512 tokens over 500
+// pages 14.6.  (32 tokens with operands loaded as the matrix unit wants them, 16 bytes of
+// each page to a lane: 22.7; with codes of the queries made by every wave for itself:
+// 18.9.)  Teams of 8 or 16 waves to choose are within 5% of four.
 constexpr int kTeam = 4;
 template <int D, bool ONE>
 __global__ __launch_bounds__(ONE ? 1024 : 512, 4) void select_kernel(SelectArgs a) {
@@ -720,23 +731,27 @@ extern "C" int32_t lora_sparse_select(const lora_sparse_launch_t* L, const lora_
     const lora_sparse_item_t* items = reinterpret_cast<const lora_sparse_item_t*>(L->attn.meta + S.off_items);
     const hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
     if (sp_in_lds(S.max_scored, S.item_tokens)) {
-        if ((int64_t)S.n_items * hk > kMaxBlocks) return LORA_EINVAL;
-        a.items = items;
         void* p[] = {&a};
         const bool one = S.item_tokens == 1;
         typedef void (*fn_t)(SelectArgs);
         static const fn_t fn[2][2] = {{select_kernel<64, false>, select_kernel<64, true>},
                                       {select_kernel<128, false>, select_kernel<128, true>}};
         const size_t lds = sizeof(uint32_t) * (size_t)S.max_scored * (size_t)S.item_tokens;
-        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn[d == 128][one]),
-                                             dim3((unsigned)(S.n_items * hk)), dim3(one ? 1024 : 512), p, lds, stream);
-        return e == hipSuccess ? LORA_OK : LORA_EHIP;
+        const int64_t most = std::max<int64_t>(1, kMaxBlocks / 4 / hk);  // items of a launch, of up to 1024 threads
+        for (int64_t i = 0; i < S.n_items; i += most) {
+            a.items = items + i;
+            const dim3 grid((unsigned)(std::min<int64_t>(most, S.n_items - i) * hk));
+            if (hipLaunchKernel(reinterpret_cast<const void*>(fn[d == 128][one]), grid, dim3(one ? 1024 : 512), p, lds,
+                                stream) != hipSuccess)
+                return LORA_EHIP;
+        }
+        return LORA_OK;
     }
     if (workspace_floats < I.workspace_floats) return LORA_ECAPACITY;
     if (!workspace || !aligned16(workspace)) return LORA_EINVAL;
     if (S.item_tokens != 1) return LORA_EINVAL;
     const int64_t per = (int64_t)S.max_scored * hk, slab = sp_slab(per, S.n_items);
-    if (slab * per > I.workspace_floats || slab * hk > kMaxBlocks) return LORA_EINVAL;
+    if (slab * per > I.workspace_floats || slab * hk > kMaxBlocks / 4) return LORA_EINVAL;
     a.keys = reinterpret_cast<uint32_t*>(workspace);
     const int64_t parts = (S.max_scored + 16 * kScoreTiles - 1) / (16 * kScoreTiles);
     for (int64_t i = 0; i < S.n_items; i += slab) {

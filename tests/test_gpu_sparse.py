@@ -257,6 +257,27 @@ def test_many_pages(heads, kv_heads, new, kv):
     assert np.array_equal(chosen.cpu().numpy(), expected_choice(batch, bounds, table, q, [new], [kv]))
 
 
+def test_more_items_than_a_launch_takes():
+    """16500 tokens of 128 kv heads: two launches, the same choice for the same query."""
+    rng = np.random.default_rng(11)
+    rows, some = 16500, 12
+    cache = make_cache(rng, 8, 128, 16, 64, "bf16")
+    table = np.tile(rng.permutation(8).astype(np.int32)[:5], (rows, 1))
+    few = normal(rng, some, 128 * 64)
+    q = few.repeat(rows // some, 1)
+    bounds = KvBounds.empty(cache)
+    batch = SparseBatch(cache, 128, 3).refresh([1] * rows, [75] * rows, table, bounded=[0] + [75] * (rows - 1))
+    assert batch.sparse_info.n_items == rows
+    batch.bounds(bounds)
+    chosen = batch.empty_selected()
+    chosen.fill_(-2)
+    batch.select(q, bounds, chosen)
+    torch.cuda.synchronize()
+    assert torch.equal(chosen, chosen[:some].repeat(rows // some, 1, 1))
+    want = expected_choice(batch, bounds, table, few, [1] * some, [75] * some)
+    assert np.array_equal(chosen[:some].cpu().numpy(), want)
+
+
 def test_split_contexts():
     batch, *_ = run_case([(1, 3000), (2, 1500), (1, 40)], 8, 2, 128, 64, "bf16", 30)
     assert batch.sparse_info.n_merge > 0
