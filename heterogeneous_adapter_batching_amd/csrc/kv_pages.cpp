@@ -20,7 +20,7 @@ struct lora_kv_pages {
     std::vector<Seq> seqs;
     std::vector<int32_t> users;       // sequences that hold each page
     std::vector<int32_t> free_pages;  // stack; room for all pages, so that a push takes no memory
-    std::vector<uint8_t> listed;      // scratch of append: sequences seen so far
+    std::vector<uint8_t> listed;      // scratch of append and fork: sequences seen so far
 
     int32_t pages_for(int64_t tokens) const { return (int32_t)((tokens + page_tokens - 1) / page_tokens); }
     void drop(int32_t page) {
@@ -70,10 +70,9 @@ int32_t append(lora_kv_pages& P, int32_t n, const int32_t* seqs, const int32_t* 
     std::vector<int32_t> left;  // (page) of splits, once each
     left.reserve((size_t)n);
     for (int32_t i = 0; i < n; ++i) {
-        lora_kv_pages::Seq& s = P.seqs[(size_t)seqs[i]];
+        const lora_kv_pages::Seq& s = P.seqs[(size_t)seqs[i]];
         const int32_t pages = P.pages_for((int64_t)s.tokens + tokens[i]);
         need += pages - (int32_t)s.pages.size();
-        s.pages.reserve((size_t)pages);
         if (P.splits(s, tokens[i])) left.push_back(s.pages.back());
     }
     std::sort(left.begin(), left.end());
@@ -84,6 +83,10 @@ int32_t append(lora_kv_pages& P, int32_t n, const int32_t* seqs, const int32_t* 
         i = end;
     }
     if (need > (int64_t)P.free_pages.size()) return LORA_ECAPACITY;
+    for (int32_t i = 0; i < n; ++i) {
+        lora_kv_pages::Seq& s = P.seqs[(size_t)seqs[i]];
+        s.pages.reserve((size_t)P.pages_for((int64_t)s.tokens + tokens[i]));
+    }
 
     int32_t copies = 0;
     for (int32_t i = 0; i < n; ++i) {
@@ -183,11 +186,15 @@ extern "C" int32_t lora_kv_pages_append(lora_kv_pages_t* P, int32_t n, const int
 
 extern "C" int32_t lora_kv_pages_fork(lora_kv_pages_t* P, int32_t parent, int32_t n, const int32_t* children) {
     if (!P || n < 0 || (n > 0 && !children) || !P->has(parent)) return LORA_EINVAL;
-    for (int32_t i = 0; i < n; ++i) {
-        if (!P->has(children[i]) || children[i] == parent || P->seqs[(size_t)children[i]].tokens != 0) return LORA_EINVAL;
-        for (int32_t j = 0; j < i; ++j)
-            if (children[j] == children[i]) return LORA_EINVAL;
+    bool good = true;
+    for (int32_t i = 0; i < n && good; ++i) {
+        good = P->has(children[i]) && children[i] != parent && P->seqs[(size_t)children[i]].tokens == 0 &&
+               !P->listed[(size_t)children[i]];
+        if (good) P->listed[(size_t)children[i]] = 1;
     }
+    for (int32_t i = 0; i < n; ++i)
+        if (P->has(children[i])) P->listed[(size_t)children[i]] = 0;
+    if (!good) return LORA_EINVAL;
     return guarded([&] {
         const lora_kv_pages::Seq& from = P->seqs[(size_t)parent];
         for (int32_t i = 0; i < n; ++i) P->seqs[(size_t)children[i]].pages.reserve(from.pages.size());
