@@ -106,6 +106,27 @@ bool same_strides(const lora_kv_t& a, const lora_kv_t& b) {
     return a.page_stride == b.page_stride && a.head_stride == b.head_stride && a.token_stride == b.token_stride;
 }
 
+// The tensors that are written: of one cache each.  `shared`: some are read too.
+int32_t check_tensors(int32_t n, const lora_kv_t* from, const lora_kv_t* to, const lora_kv_bounds_t* to_bounds,
+                      bool& shared) {
+    try {
+        std::vector<const void*> written;
+        for (int32_t i = 0; i < n; ++i) {
+            written.push_back(to[i].k);
+            if (to[i].v != to[i].k) written.push_back(to[i].v);
+            if (to_bounds) written.push_back(to_bounds[i].codes);
+        }
+        std::sort(written.begin(), written.end());
+        if (std::adjacent_find(written.begin(), written.end()) != written.end()) return LORA_EINVAL;
+        for (int32_t i = 0; i < n && !shared; ++i)
+            shared = std::binary_search(written.begin(), written.end(), from[i].k) ||
+                     std::binary_search(written.begin(), written.end(), from[i].v);
+    } catch (const std::bad_alloc&) {
+        return LORA_ENOMEM;
+    }
+    return LORA_OK;
+}
+
 // Every page that is written is written once, and none is read that is also
 // written where source and destination share memory.
 int32_t check_pairs(int32_t n, const int32_t* from, const int32_t* to, const int32_t* tokens, int32_t from_pages,
@@ -194,13 +215,13 @@ extern "C" int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const l
         if (st == LORA_OK && from_bounds) st = check_bounds(from_bounds[i], from[i]);
         if (st == LORA_OK && dst_bounds) st = check_bounds(dst_bounds[i], dst[i]);
         if (st != LORA_OK) return st;
-        shared = shared || from[i].k == dst[i].k || from[i].v == dst[i].v;
     }
     const lora_kv_t& c = from[0];
     if (dst->dtype != c.dtype || dst->head_dim != c.head_dim || dst->n_kv_heads != c.n_kv_heads ||
         dst->page_tokens != c.page_tokens)
         return LORA_ESHAPE;
-    const int32_t st = check_pairs(n_pairs, from_page, to_page, tokens, c.n_pages, dst->n_pages, c.page_tokens, shared);
+    int32_t st = to ? check_tensors(n_caches, from, to, to_bounds, shared) : LORA_OK;
+    if (st == LORA_OK) st = check_pairs(n_pairs, from_page, to_page, tokens, c.n_pages, dst->n_pages, c.page_tokens, shared);
     if (st != LORA_OK) return st;
 
     const int32_t most = to ? CopyFew::kCaches / 2 : CopyFew::kCaches;

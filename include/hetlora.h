@@ -902,11 +902,11 @@ int32_t lora_attn(const lora_attn_launch_t* launch, const lora_kv_t* kv,
  *             (tokens[i] == page_tokens), or NULL; to_bounds with to only
  *   from_page, to_page, tokens  host int32 [n_pairs]; tokens NULL: whole pages.
  *             They are read before the call returns.  A page is written by one
- *             pair at most, and within a cache (to NULL, or of the same memory)
+ *             pair at most, and within caches (to NULL, or any of to among from)
  *             no page that is written is also read
- * Caches of different memory must not overlap.  One launch for each 192 pairs of
- * 32 caches with the same strides (16 with to).  Errors: LORA_EINVAL, LORA_ESHAPE, LORA_EPAGE,
- * LORA_ENOMEM, LORA_EHIP. */
+ * No two of to share a tensor or bounds, and caches of different memory must not
+ * overlap.  One launch for each 192 pairs of 32 caches with the same strides (16
+ * with to).  Errors: LORA_EINVAL, LORA_ESHAPE, LORA_EPAGE, LORA_ENOMEM, LORA_EHIP. */
 int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const lora_kv_t* to,
                      const lora_kv_bounds_t* from_bounds, const lora_kv_bounds_t* to_bounds,
                      int32_t n_pairs, const int32_t* from_page, const int32_t* to_page,

@@ -155,6 +155,22 @@ def test_copy_refuses_pages():
     assert copy([], []) == hl.LORA_OK and copy([1, 1], [2, 3], [0, 0]) == hl.LORA_OK  # nothing to launch
 
 
+def test_copy_refuses_memory_written_twice_or_read_and_written():
+    one, two, three = (kv(k=i << 20, v=i + 8 << 20) for i in (1, 2, 3))
+    for to in ([three, three], [three, kv(k=3 << 20, v=12 << 20)], [three, kv(k=4 << 20, v=11 << 20)],
+               [three, kv(k=11 << 20, v=4 << 20)]):
+        assert copy([], [], caches=[one, two], to=to) == hl.LORA_EINVAL
+    assert copy([], [], caches=[one, one], to=[two, three]) == hl.LORA_OK
+    assert copy([1], [1], [0], caches=[one, two], to=[kv(k=4 << 20, v=5 << 20), three]) == hl.LORA_OK
+    for to in ([two, one], [three, one], [two, three]):  # crosswise
+        assert copy([1], [1], [0], caches=[one, two], to=to) == hl.LORA_EINVAL
+        assert copy([1, 2], [2, 3], [0, 0], caches=[one, two], to=to) == hl.LORA_EINVAL
+        assert copy([1, 1], [2, 3], [0, 0], caches=[one, two], to=to) == hl.LORA_OK
+    b = [bounds(codes=i << 20) for i in (21, 22, 23)]
+    assert copy([], [], caches=[one, one], to=[two, three], b=[b[0], b[0]], to_b=[b[1], b[1]]) == hl.LORA_EINVAL
+    assert copy([], [], caches=[one, one], to=[two, three], b=[b[0], b[0]], to_b=[b[1], b[2]]) == hl.LORA_OK
+
+
 @pytest.mark.parametrize("change,code", [
     (dict(k=None), hl.LORA_EINVAL), (dict(v=0x2008), hl.LORA_EINVAL), (dict(dtype=2), hl.LORA_EINVAL),
     (dict(page_tokens=12), hl.LORA_ESHAPE), (dict(page_tokens=2048), hl.LORA_ESHAPE), (dict(head_dim=96), hl.LORA_ESHAPE),
