@@ -233,11 +233,16 @@ int32_t sparse_impl(const lora_attn_shape_t& s, const lora_sparse_shape_t& sp, i
             if (pages > sp.select) out.max_scored = std::max(out.max_scored, (int32_t)(pages - always));
             rows += q_len[b];
         }
-    // Tokens of an item: their rows fill the tiles that are scored at once, their
-    // scores fit LDS, and there are items enough to fill the chip.
+    // Tokens of an item: their rows fill the tiles that are scored one after another,
+    // their scores fit LDS, and there are items enough to fill the chip.
     const int64_t spread = rows * s.n_kv_heads / kSelectItems;
     out.item_tokens = (int32_t)std::max<int64_t>(
         1, std::min({(int64_t)(16 * SP_ROW_TILES / pad), (int64_t)(SP_LDS_KEYS / std::max(1, out.max_scored)), spread}));
+    if (out.item_tokens > SP_WAVES) {  // as many to each wave, and two workgroups to a compute unit
+        int32_t n = SP_WAVES;
+        while (2 * n <= out.item_tokens && 2 * n * (int64_t)out.max_scored <= (n == SP_WAVES ? 2 : 1) * SP_FEW_KEYS) n *= 2;
+        out.item_tokens = n;
+    }
 
     std::vector<lora_sparse_item_t> items;
     std::vector<Tile> tiles;

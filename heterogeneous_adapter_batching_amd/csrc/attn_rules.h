@@ -68,12 +68,23 @@ AT_FN int at_inside(const lora_attn_work_t* w, int32_t n_seq, int32_t n_rows, in
 // ------------------------------------------------------------------ sparse attention
 #define SP_MIN_PAGE 16       // fewest tokens of a page: under that its bounds are as much as its keys
 #define SP_EXP 100           // exponents of bounds are within +-SP_EXP
-// Keys (scores) that a selecting workgroup of several tokens holds in LDS at most, and
-// tiles of 16 rows (query heads of its tokens) that it scores one after another.
-// (512 tokens over 16000 in pages of 32, 32/8 heads: one tile at a time 24.3 us, two
-// 14.6, four 19.0, eight 54: then too few workgroups are left to fill the chip.)
+// Keys (scores) that a selecting workgroup of several tokens holds in LDS at most, tiles
+// of 16 rows (query heads of its tokens) that it scores one after another at most, and
+// its waves, each of which chooses for a token.  More tokens than waves only as 2 or 4
+// times as many, and with few keys: us of 2048 tokens, 8 kv heads of 2 query heads, over
+//              8 tokens   16   24
+//   282 pages      36.5 28.5 46.0
+//   560            53.1 69.9
+// and of 512 tokens, 32 kv heads of their own, over
+//              8 tokens   16   32
+//   70 pages      25.4 18.1 15.0
+//   250           34.4 24.7 29.7
+//   500           50.2 35.8
+// 2048 tokens, 64/8 heads, over 282 pages: two tiles at most 67.7, four 54.7.
 #define SP_LDS_KEYS 12288
-#define SP_ROW_TILES 2
+#define SP_ROW_TILES 4
+#define SP_WAVES 8
+#define SP_FEW_KEYS 4096
 // Of a single token's keys, which one workgroup scores where it holds them; more are
 // scored by many workgroups, into memory, and chosen from by another launch.  us in
 // LDS and through memory, one token of each sequence, 8 kv heads of 8 query heads:

@@ -600,9 +600,10 @@ __device__ __forceinline__ void select_token(const SelectArgs& a, const SelectIt
 // each page to a lane: 22.7; with codes of the queries made by every wave for itself:
 // 18.9.)  Teams of 8 or 16 waves to choose are within 5% of four.
 constexpr int kTeam = 4;
-template <int D, bool ONE>
-__global__ __launch_bounds__(ONE ? 1024 : 512, 4) void select_kernel(SelectArgs a) {
-    constexpr int WAVES = ONE ? 16 : 8, R = ONE ? 1 : SP_ROW_TILES;
+template <int D, int R>
+__global__ __launch_bounds__(R == 1 ? 1024 : 64 * SP_WAVES, 4) void select_kernel(SelectArgs a) {
+    constexpr bool ONE = R == 1;
+    constexpr int WAVES = ONE ? 16 : SP_WAVES;
     extern __shared__ uint32_t keys[];
     __shared__ SelectScratch<kTeam> s[ONE ? 1 : WAVES];
     __shared__ ScoreLds<D, R, WAVES> lds;
@@ -734,14 +735,15 @@ extern "C" int32_t lora_sparse_select(const lora_sparse_launch_t* L, const lora_
         void* p[] = {&a};
         const bool one = S.item_tokens == 1;
         typedef void (*fn_t)(SelectArgs);
-        static const fn_t fn[2][2] = {{select_kernel<64, false>, select_kernel<64, true>},
-                                      {select_kernel<128, false>, select_kernel<128, true>}};
+        static const fn_t fn[2][3] = {{select_kernel<64, 1>, select_kernel<64, 2>, select_kernel<64, 4>},
+                                      {select_kernel<128, 1>, select_kernel<128, 2>, select_kernel<128, 4>}};
+        const int form = one ? 0 : S.item_tokens << a.pad_shift <= 32 ? 1 : 2;  // 1, 2 or 4 tiles of rows
         const size_t lds = sizeof(uint32_t) * (size_t)S.max_scored * (size_t)S.item_tokens;
         const int64_t most = std::max<int64_t>(1, kMaxBlocks / 4 / hk);  // items of a launch, of up to 1024 threads
         for (int64_t i = 0; i < S.n_items; i += most) {
             a.items = items + i;
             const dim3 grid((unsigned)(std::min<int64_t>(most, S.n_items - i) * hk));
-            if (hipLaunchKernel(reinterpret_cast<const void*>(fn[d == 128][one]), grid, dim3(one ? 1024 : 512), p, lds,
+            if (hipLaunchKernel(reinterpret_cast<const void*>(fn[d == 128][form]), grid, dim3(one ? 1024 : 64 * SP_WAVES), p, lds,
                                 stream) != hipSuccess)
                 return LORA_EHIP;
         }
