@@ -244,6 +244,37 @@ def test_batch_plans_and_refuses(world, monkeypatch):  # noqa: F811
             sparse.SparseBatch(cache(), 4, *args)
 
 
+def test_another_device_than_the_current_one(world, monkeypatch):  # noqa: F811
+    """The default stream is the current device's: launched there, the work would not be the tensors' device's."""
+    import types
+    from heterogeneous_adapter_batching_amd import pages
+    from test_attn_batch import Stream
+    now = [0]
+    monkeypatch.setattr(pages, "torch", types.SimpleNamespace(cuda=types.SimpleNamespace(
+        is_initialized=lambda: True, current_device=lambda: now[0])))
+    monkeypatch.setattr(sparse, "_lib", hl._lib)
+    batch = sparse.SparseBatch(cache(), 4, 3)
+    batch._use(None)
+    now[0] = 1
+    with pytest.raises(ValueError):
+        batch._use(None)
+    with pytest.raises(ValueError):
+        pages.check_device(DEVICE, 0)
+    batch._use(Stream(7))
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_sparse_planner_under_address_and_ub_sanitizers(tmp_path):
+    exe = tmp_path / "sparse_sanitize"
+    csrc = os.path.join(REPO, "heterogeneous_adapter_batching_amd", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+                    "-I", os.path.join(REPO, "include"), os.path.join(csrc, "attn_plan.cpp"),
+                    os.path.join(REPO, "tests", "sparse_sanitize.cpp"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "sparse planner ok" in r.stdout
+
+
 # ---------------------------------------------------------------- the oracle
 def test_oracle_codes_and_exponents():
     assert [oracle.exponent_ref(x) for x in (127.0, 127.5, 1.0, 0.0, 1e38, 2.0 ** -120)] == [0, 1, -6, -100, 100, -100]
