@@ -32,6 +32,13 @@ def _one(x, name):
     return int(a.reshape(-1)[0])
 
 
+def check_device(device, handle):
+    """A launch on the default stream goes to the current device."""
+    if handle == 0 and torch.cuda.is_initialized() and torch.cuda.current_device() != device.index:
+        raise ValueError(f"{device} is not the current device, whose default stream this is: make it current, or give "
+                         "a stream of it")
+
+
 class KvPages:
     """Pages 0 .. n_pages-1 of ``page_tokens`` tokens, and the sequences 0 ..
     n_seqs-1 that hold them.  One manager serves all layers' caches.  Serves one
@@ -153,6 +160,7 @@ class KvCopy:
             raise ValueError("src, dst and tokens have different lengths")
         s, d, t = s.copy(), d.copy(), None if t is None else t.copy()
         h = (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        check_device(self.device, h)
         args = (self._n, *self._args, s.shape[0], s.ctypes.data, d.ctypes.data, None if t is None else t.ctypes.data, h)
         call = _lib.lora_kv_copy
 

@@ -14,6 +14,7 @@ import torch
 
 from . import (LORA_OK, _lib, as_int32, check_status, lora_kv_bounds_t, lora_sparse_launch_t, lora_sparse_shape_t)
 from .attention import AttnBatch
+from .pages import check_device
 
 
 class KvBounds:
@@ -74,6 +75,11 @@ class SparseBatch(AttnBatch):
         if self._bounded is not None and self._bounded.shape != as_int32(q_len, "q_len").shape:
             raise ValueError("bounded [n_seq]")
         return super().refresh(q_len, kv_len, block_table, stream)
+
+    def _use(self, stream):
+        s = super()._use(stream)
+        check_device(self.device, s.cuda_stream)
+        return s
 
     def _prepare(self, ql, kl, tab, staging, capacity, dev, h):
         return _lib.lora_sparse_prepare(ctypes.byref(self.shape), ctypes.byref(self.sparse_shape), ql.shape[0],
