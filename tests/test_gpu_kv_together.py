@@ -4,6 +4,9 @@ sequences that end, a cache that is compacted.  After each step every sequence's
 keys and values are the ones it has written, the new ones are the oracle's within
 the tolerances of test_gpu_kv_norm.py, bounds and choice are the oracle's, and the
 attention is within that of test_gpu_attn.py."""
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -138,3 +141,16 @@ def test_a_server_of_forking_requests(heads, kv_heads, dim, dtype):
     s.step([6], [1])
     s.free([6])
     assert s.pages.stats() == (PAGES, 0, 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+def test_shared_prompt_example(dtype):
+    """Runs; over all pages it is lora_attn's sum in another order: each output is off by
+    its rounding to bf16 (2^-8 at most) and, on both sides, by 2^-12 of what its tokens' values reach."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "shared_prompt.py")
+    spec = importlib.util.spec_from_file_location("shared_prompt", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    off, used, alone = mod.run(dtype, 300, 6, 4)
+    assert np.isfinite(off) and used < alone
+    assert mod.run(dtype, 300, 6, 300)[0] <= 2 * U
