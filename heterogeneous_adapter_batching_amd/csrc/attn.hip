@@ -1724,7 +1724,6 @@ int64_t solo_items(const lora_kv_t& kv) {
     return kv.head_dim == 128 ? 2048 : INT64_MAX;
 }
 
-
 extern "C" int32_t lora_sparse_attn(const lora_sparse_launch_t* L, const lora_kv_t* kv, const uint16_t* q, int64_t ldq,
                                     const int32_t* selected, uint16_t* out, int64_t ldo, float scale, float* workspace,
                                     int64_t workspace_floats, void* hip_stream) {

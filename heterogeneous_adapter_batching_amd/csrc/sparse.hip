@@ -1,6 +1,6 @@
 // gfx950 kernels of the sparse attention's first two steps, and their C entry
 // points: the bounds of pages' keys, and the choice of pages by them.  (The
-// attention over the chosen pages is lora_attn's kernel, in attn.hip.)
+// attention over the chosen pages is in attn.hip.)
 #include <algorithm>
 
 #include "kv_device.h"
@@ -595,10 +595,11 @@ __device__ __forceinline__ void select_token(const SelectArgs& a, const SelectIt
 // its own.  The bounds' bytes are what has to move, but a call ends long before they
 // bound it: one token over 500 pages, 8 kv heads, takes 7.5 us, of which 3 are a launch
 // and most of the rest the first pass through the code and the chain item, page ids,
-// bounds; 32 tokens over up to 2048 pages of 16 16.3 us, 2.4 TB/s; 512 tokens over 500
-// pages 14.6.  (32 tokens with operands loaded as the matrix unit wants them, 16 bytes of
-// each page to a lane: 22.7; with codes of the queries made by every wave for itself:
-// 18.9.)  Teams of 8 or 16 waves to choose are within 5% of four.
+// bounds; 32 tokens over up to 2048 pages of 16 16.3 us, 2.4 TB/s; 512 tokens of 32/8
+// heads over 500 pages 14.5, 920 of 64/8 over up to 512 37.  (32 tokens with operands
+// loaded as the matrix unit wants them, 16 bytes of each page to a lane: 22.7; with codes
+// of the queries made by every wave for itself: 18.9.)  Teams of 8 or 16 waves to choose
+// are within 5% of four.  Of 37 us the choice is a quarter.
 constexpr int kTeam = 4;
 template <int D, int R>
 __global__ __launch_bounds__(R == 1 ? 1024 : 64 * SP_WAVES, 4) void select_kernel(SelectArgs a) {
