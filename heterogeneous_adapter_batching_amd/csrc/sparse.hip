@@ -38,19 +38,30 @@ struct BoundsArgs {
     int32_t n_pages;
 };
 
-// A wave takes a page of one head: 16 bytes of a token to a lane, so LPT lanes to
-// a token and 64 / LPT tokens at once, joined over the lanes at the end.  Largest
-// and smallest are kept as ordered 16-bit integers, two to a register: three
-// instructions an element and a half.  Bound by memory: the pages of 48 sequences of
-// up to 16384 tokens (8 kv heads, e4m3, pages of 64, 167 MB) take 38 us, 4.4 TB/s, those
-// of 16 prompts of up to 2048 (32 heads, bf16, pages of 16, 73 MB, part of them in the
-// caches) 13.1 us, 5.5 TB/s.  Two or eight loads of a lane under way instead of four: 41
-// and 38 us for the first; loads past the caches 34 and 14.2 us.
-template <int D, bool E4M3>
+// 16 bytes of a token to a lane, so LPT lanes to a token, four tokens to a lane, and as
+// many lanes to a page of one head as it has work for: G pages' heads to a wave.  The
+// largest and the least are kept as 16-bit integers of the same order, two to a
+// register.  The first exchange between lanes leaves the largest to one half of a
+// page's lanes and the least (its complement, so that both are maxima) to the other;
+// they join and code one of them each.
+// Bound by memory, but for the exchanges in small pages: the pages of 48 sequences of up
+// to 16384 tokens (8 kv heads, e4m3, pages of 64, 167 MB) take 37 us, 4.5 TB/s, those of
+// 16 prompts of up to 2048 (32 heads, bf16, pages of 16, 73 MB, part of them in the
+// caches) 13.1 us, 5.5 TB/s; 32000 tokens of 16 heads, e4m3 in pages of 16, of 128
+// elements 17.5 us, of 64 10.8.  (With a wave to a page whatever its size, all lanes
+// joining both through LDS: 39 and 13.1, 39.5 and 40.4.)  Of that form: two or eight
+// loads of a lane under way instead of four 41 and 38 us for the first; loads past the
+// caches 34 and 14.2.
+template <int D, bool E4M3, int G>
 struct PageBounds {
-    static constexpr int LPT = D * (E4M3 ? 1 : 2) / 16, TOKENS = 64 / LPT, N = E4M3 ? 8 : 4;  // registers of elements
+    static constexpr int LPT = D * (E4M3 ? 1 : 2) / 16, LANES = 64 / G, TOKENS = LANES / LPT;
+    static constexpr int N = E4M3 ? 8 : 4, E = 2 * N;  // registers and elements of a lane
     static constexpr int AHEAD = 4;  // loads of a lane that are under way
-    s16x2_t hi[N], lo[N];
+    static_assert(TOKENS * AHEAD >= 16, "");
+
+    // the lane has the least, not the largest; and it is the one of several that writes
+    __device__ __forceinline__ static bool least() { return (threadIdx.x & (G == 1 ? 32 : G == 2 ? 16 : 4)) != 0; }
+    __device__ __forceinline__ static bool first() { return (int)(threadIdx.x & (G == 1 ? 31 : G == 2 ? 15 : 11)) < LPT; }
 
     __device__ __forceinline__ static void values(const char* from, uint32_t scale, u32x4_t (&x)[N / 4]) {
         const u32x4_t raw = *reinterpret_cast<const u32x4_t*>(from);
@@ -63,7 +74,7 @@ struct PageBounds {
     }
     template <typename F>
     __device__ __forceinline__ static void each_token(const Kv& c, int32_t page, int32_t head, F use) {
-        const int lane = threadIdx.x & 63, n = 1 << c.page_shift;
+        const int lane = threadIdx.x % LANES, n = 1 << c.page_shift;
         const char* base = c.k + (E4M3 ? 1 : 2) * kv_off(c, page, head, 0) + 16 * (lane % LPT);
         const uint8_t* scales = c.k_scale + (E4M3 ? scale_off(c, page, head, 0) : 0);
         const int64_t step = (E4M3 ? 1 : 2) * c.token_stride;
@@ -77,7 +88,29 @@ struct PageBounds {
             for (int i = 0; i < AHEAD; ++i) use(x[i]);
         }
     }
-    __device__ __forceinline__ void find(const Kv& c, int32_t page, int32_t head) {
+    __device__ __forceinline__ static s16x2_t joined(s16x2_t x, s16x2_t y) { return __builtin_elementwise_max(x, y); }
+    // x and y of this half of the lanes and the other (of 32, or of each 32), or the
+    // lower half's x and the upper half's y of both
+    template <int HALF>
+    __device__ __forceinline__ static s16x2_t across(s16x2_t x, s16x2_t y) {
+        const uint32_t a = __builtin_bit_cast(uint32_t, x), b = __builtin_bit_cast(uint32_t, y);
+        const auto r = HALF == 32 ? __builtin_amdgcn_permlane32_swap(a, b, false, false)
+                                  : __builtin_amdgcn_permlane16_swap(a, b, false, false);
+        return joined(__builtin_bit_cast(s16x2_t, (uint32_t)r[0]), __builtin_bit_cast(s16x2_t, (uint32_t)r[1]));
+    }
+    template <int BY>  // lanes of each 16
+    __device__ __forceinline__ static s16x2_t around(s16x2_t x) {
+        return joined(x, __builtin_bit_cast(s16x2_t, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + BY, 0xF,
+                                                                               0xF, false)));
+    }
+    __device__ __forceinline__ static s16x2_t in_row(s16x2_t x) {
+        if constexpr (LPT <= 4) x = around<4>(x);
+        if constexpr (LPT <= 8) x = around<8>(x);
+        return x;
+    }
+    // The largest or the least, two bf16 to a register, and their largest absolute value as bits.
+    __device__ __forceinline__ static uint32_t find(const Kv& c, int32_t page, int32_t head, uint32_t (&out)[N]) {
+        s16x2_t hi[N], lo[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             hi[j] = s16x2_t{-32768, -32768};
@@ -87,27 +120,41 @@ struct PageBounds {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const s16x2_t y = ordered(__builtin_bit_cast(s16x2_t, (uint32_t)x[j / 4][j % 4]));
-                hi[j] = __builtin_elementwise_max(hi[j], y);
+                hi[j] = joined(hi[j], y);
                 lo[j] = __builtin_elementwise_min(lo[j], y);
             }
         });
+        s16x2_t most = {0, 0};
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-            for (int o = LPT; o < 64; o <<= 1) {
-                hi[j] = __builtin_elementwise_max(
-                    hi[j], __builtin_bit_cast(s16x2_t, __shfl_xor(__builtin_bit_cast(int, hi[j]), o)));
-                lo[j] = __builtin_elementwise_min(
-                    lo[j], __builtin_bit_cast(s16x2_t, __shfl_xor(__builtin_bit_cast(int, lo[j]), o)));
+        for (int j = 0; j < N; ++j) {
+            s16x2_t x;
+            if constexpr (G == 1) {
+                x = across<32>(hi[j], ~lo[j]);
+                x = in_row(across<16>(x, x));
+            } else if constexpr (G == 2) {
+                x = in_row(across<16>(hi[j], ~lo[j]));
+            } else {
+                const s16x2_t y = in_row(hi[j]), z = in_row(~lo[j]);
+                x = least() ? z : y;
             }
+            x = ordered(least() ? ~x : x);
+            out[j] = __builtin_bit_cast(uint32_t, x);
+            most = joined(most, x & (short)0x7FFF);
+        }
+        // (a row holds the largest or the least of all elements, or both)
+        most = around<1>(around<2>(around<4>(around<8>(most))));
+        if constexpr (G == 2) most = across<16>(most, most);
+        if constexpr (G == 1) most = across<32>(most, most);
+        return (uint32_t)max((int)most[0], (int)most[1]);
     }
 };
 
 // Pages with infinities or NaN: the largest and smallest of what is not NaN, and
 // the largest finite absolute value, element by element.
-template <int D, bool E4M3, int E>
-__device__ __forceinline__ uint32_t careful_bounds(const Kv& c, int32_t page, int32_t head, float (&hi)[E], float (&lo)[E]) {
-    typedef PageBounds<D, E4M3> P;
+template <typename P>
+__device__ __forceinline__ uint32_t careful_bounds(const Kv& c, int32_t page, int32_t head, uint32_t (&out)[P::N]) {
+    constexpr int E = P::E;
+    float hi[E], lo[E];
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
@@ -127,58 +174,46 @@ __device__ __forceinline__ uint32_t careful_bounds(const Kv& c, int32_t page, in
 #pragma unroll
     for (int j = 0; j < E; ++j) {
 #pragma unroll
-        for (int o = P::LPT; o < 64; o <<= 1) {
+        for (int o = P::LPT; o < P::LANES; o <<= 1) {
             hi[j] = fmaxf(hi[j], __shfl_xor(hi[j], o));
             lo[j] = fminf(lo[j], __shfl_xor(lo[j], o));
         }
         if (hi[j] < lo[j]) hi[j] = lo[j] = 0.f;  // nothing but NaN
     }
-    for (int o = 1; o < 64; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+#pragma unroll
+    for (int j = 0; j < E; j += 2)
+        out[j / 2] = __float_as_uint(P::least() ? lo[j] : hi[j]) >> 16 |
+                     (__float_as_uint(P::least() ? lo[j + 1] : hi[j + 1]) & 0xFFFF0000u);
+    for (int o = 1; o < P::LANES; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
     return top;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int G>
 __global__ __launch_bounds__(256) void kv_bounds_kernel(BoundsArgs a) {
-    typedef PageBounds<D, E4M3> P;
-    constexpr int E = 2 * P::N;  // elements of a lane
-    const int lane = threadIdx.x & 63;
-    const int64_t units = (int64_t)a.n_pages * a.kv.n_kv_heads;
-    for (int64_t u = (int64_t)blockIdx.x * 4 + wave_id(); u < units; u += (int64_t)gridDim.x * 4) {
-        const int32_t page = clamp_page(a.kv, a.pages[u / a.kv.n_kv_heads]), head = (int32_t)(u % a.kv.n_kv_heads);
-        P p;
-        p.find(a.kv, page, head);
-        float hi[E], lo[E];
-        uint32_t top = 0;
+    typedef PageBounds<D, E4M3, G> P;
+    const uint32_t units = (uint32_t)a.n_pages * (uint32_t)a.kv.n_kv_heads;
+    const uint32_t u = (blockIdx.x * 4 + (G > 1 ? threadIdx.x >> 6 : (uint32_t)wave_id())) * G + (threadIdx.x & 63) / P::LANES;
+    if (u - (threadIdx.x & 63) / P::LANES >= units) return;  // (the last wave's other pages: of the last one again)
+    const uint32_t unit_of = min(u, units - 1);
+    const int32_t page = clamp_page(a.kv, a.pages[unit_of / (uint32_t)a.kv.n_kv_heads]);
+    const int32_t head = (int32_t)(unit_of % (uint32_t)a.kv.n_kv_heads);
+    uint32_t x[P::N];
+    uint32_t top = P::find(a.kv, page, head, x);
+    if (__ballot(top >= 0x7F80u)) top = careful_bounds<P>(a.kv, page, head, x);
+    const int e = code_exponent(top);
+    const float unit = power(-e);
+    const int64_t at = (int64_t)page * a.kv.n_kv_heads + head;
+    if (P::first()) {
+        uint32_t w[P::N / 2];
 #pragma unroll
-        for (int j = 0; j < P::N; ++j) {
-            const uint32_t h = __builtin_bit_cast(uint32_t, ordered(p.hi[j])), l = __builtin_bit_cast(uint32_t, ordered(p.lo[j]));
-            hi[2 * j] = bf16_lo(h);
-            hi[2 * j + 1] = bf16_hi(h);
-            lo[2 * j] = bf16_lo(l);
-            lo[2 * j + 1] = bf16_hi(l);
-            top = max(max(top, max(h & 0x7FFFu, l & 0x7FFFu)), max(h >> 16 & 0x7FFFu, l >> 16 & 0x7FFFu));
-        }
-#pragma unroll
-        for (int o = 1; o < P::LPT; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-        if (top >= 0x7F80u) top = careful_bounds<D, E4M3, E>(a.kv, page, head, hi, lo);
-        const int e = code_exponent(top);
-        const float unit = power(-e);
-        const int64_t at = (int64_t)page * a.kv.n_kv_heads + head;
-        if (lane < 2 * P::LPT) {  // the first token's lanes have the largest, the second's the smallest
-            uint32_t w[E / 4];
-#pragma unroll
-            for (int j = 0; j < E; j += 4) {
-                int x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = code(lane < P::LPT ? hi[j + i] : lo[j + i], unit);
-                w[j / 4] = pack4(x[0], x[1], x[2], x[3]);
-            }
-            int8_t* to = a.codes + at * 2 * D + E * lane;
-            if constexpr (E4M3) *reinterpret_cast<u32x4_t*>(to) = u32x4_t{w[0], w[1], w[2], w[3]};
-            else *reinterpret_cast<u32x2_t*>(to) = u32x2_t{w[0], w[1]};
-        }
-        if (lane == 0) a.exps[at] = (uint8_t)(e + 127);
+        for (int j = 0; j < P::N; j += 2)
+            w[j / 2] = pack4(code(bf16_lo(x[j]), unit), code(bf16_hi(x[j]), unit), code(bf16_lo(x[j + 1]), unit),
+                             code(bf16_hi(x[j + 1]), unit));
+        int8_t* to = a.codes + (2 * at + P::least()) * D + P::E * (threadIdx.x % P::LPT);
+        if constexpr (E4M3) *reinterpret_cast<u32x4_t*>(to) = u32x4_t{w[0], w[1], w[2], w[3]};
+        else *reinterpret_cast<u32x2_t*>(to) = u32x2_t{w[0], w[1]};
     }
+    if (threadIdx.x % P::LANES == 0) a.exps[at] = (uint8_t)(e + 127);
 }
 
 // ------------------------------------------------------------------ select
@@ -685,15 +720,25 @@ extern "C" int32_t lora_kv_bounds(const lora_sparse_launch_t* L, const lora_kv_t
     if (st == LORA_OK) st = check_bounds(bounds, L->attn.info.shape);
     if (st != LORA_OK) return st;
     if (L->info.n_fresh == 0) return LORA_OK;
-    BoundsArgs a{to_kv(*kv), bounds->codes, bounds->exps, L->attn.meta + L->info.off_fresh, L->info.n_fresh};
+    BoundsArgs a{to_kv(*kv), bounds->codes, bounds->exps, nullptr, 0};
     typedef void (*fn_t)(BoundsArgs);
-    static const fn_t fn[2][2] = {{kv_bounds_kernel<64, false>, kv_bounds_kernel<64, true>},
-                                  {kv_bounds_kernel<128, false>, kv_bounds_kernel<128, true>}};
-    const int64_t blocks = ((int64_t)a.n_pages * a.kv.n_kv_heads + 3) / 4;
-    const hipError_t e = launch(fn[kv->head_dim == 128][kv->dtype == LORA_KV_E4M3],
-                                dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256),
-                                reinterpret_cast<hipStream_t>(hip_stream), a);
-    return e == hipSuccess ? LORA_OK : LORA_EHIP;
+    // by the lanes that a page of one head has work for, 16 bytes of four tokens each
+    static const fn_t fn[2][2][3] = {{{kv_bounds_kernel<64, false, 1>, kv_bounds_kernel<64, false, 2>, nullptr},
+                                      {kv_bounds_kernel<64, true, 1>, kv_bounds_kernel<64, true, 2>, kv_bounds_kernel<64, true, 4>}},
+                                     {{kv_bounds_kernel<128, false, 1>, nullptr, nullptr},
+                                      {kv_bounds_kernel<128, true, 1>, kv_bounds_kernel<128, true, 2>, nullptr}}};
+    const bool e4m3 = kv->dtype == LORA_KV_E4M3;
+    const int lanes = kv->head_dim * (e4m3 ? 1 : 2) / 16 * kv->page_tokens / 4, form = lanes >= 64 ? 0 : lanes >= 32 ? 1 : 2;
+    const int32_t hk = kv->n_kv_heads, most = std::max(1, (int32_t)(kMaxBlocks / hk));  // pages of a launch
+    for (int32_t i = 0; i < L->info.n_fresh; i += a.n_pages) {
+        a.pages = L->attn.meta + L->info.off_fresh + i;
+        a.n_pages = std::min(most, L->info.n_fresh - i);
+        const int64_t units = (int64_t)a.n_pages * hk, per = 4 << form;
+        if (launch(fn[kv->head_dim == 128][e4m3][form], dim3((unsigned)((units + per - 1) / per)), dim3(256),
+                   reinterpret_cast<hipStream_t>(hip_stream), a) != hipSuccess)
+            return LORA_EHIP;
+    }
+    return LORA_OK;
 }
 
 extern "C" int32_t lora_sparse_select(const lora_sparse_launch_t* L, const lora_kv_bounds_t* bounds, const uint16_t* q,

@@ -190,6 +190,24 @@ def test_bounds_of_every_kind_of_value(dim, dtype):
     check_bounds(cache, bounds, list(range(n)), before)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 32, 64, 1024])
+@pytest.mark.parametrize("dim,kv_heads,n", [(64, 3, 7), (128, 1, 3), (64, 1, 1), (128, 5, 9)])
+def test_bounds_of_pages_that_share_a_wave(dim, kv_heads, n, page, dtype):
+    """Numbers of pages and heads that leave the last wave part of them; one page with NaN beside others."""
+    rng = np.random.default_rng([dim, page, n])
+    cache = make_cache(rng, n + 2, kv_heads, page, dim, dtype, token_major=n == 7)
+    table = rng.permutation(n + 2).astype(np.int32)[None, :n]
+    codes = cache.k.view(torch.uint8 if dtype == "e4m3" else torch.int16)
+    codes[int(table[0, n // 2]), 0, 5, 7] = 0x7F if dtype == "e4m3" else 0x7FC0
+    bounds = make_bounds(rng, cache)
+    before = bounds.codes.clone(), bounds.exps.clone()
+    batch = SparseBatch(cache, kv_heads, 2).refresh([0], [n * page], table, bounded=[0])
+    batch.bounds(bounds)
+    torch.cuda.synchronize()
+    check_bounds(cache, bounds, [int(p) for p in table[0]], before)
+
+
 def test_choice_of_every_kind_of_query():
     rng = np.random.default_rng(3)
     q = torch.from_numpy(rng.standard_normal((12, 4 * 64)).astype(np.float32))
