@@ -634,7 +634,8 @@ __device__ __forceinline__ void select_token(const SelectArgs& a, const SelectIt
 // heads over 500 pages 14.5, 920 of 64/8 over up to 512 37.  (32 tokens with operands
 // loaded as the matrix unit wants them, 16 bytes of each page to a lane: 22.7; with codes
 // of the queries made by every wave for itself: 18.9.)  Teams of 8 or 16 waves to choose
-// are within 5% of four.  Of 37 us the choice is a quarter.
+// are within 5% of four.  Two tiles of a wave under way instead of one: no faster (heads
+// of 64), or spilled (128: 19.8 -> 26.7).  Of the 37 us the choice is a quarter.
 constexpr int kTeam = 4;
 template <int D, int R>
 __global__ __launch_bounds__(R == 1 ? 1024 : 64 * SP_WAVES, 4) void select_kernel(SelectArgs a) {
