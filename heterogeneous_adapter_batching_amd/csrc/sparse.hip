@@ -45,14 +45,20 @@ struct BoundsArgs {
 // page's lanes and the least (its complement, so that both are maxima) to the other;
 // they join and code one of them each.
 // Bound by memory, but for the exchanges in small pages: the pages of 48 sequences of up
-// to 16384 tokens (8 kv heads, e4m3, pages of 64, 167 MB) take 37 us, 4.5 TB/s, those of
+// to 16384 tokens (8 kv heads, e4m3, pages of 64, 167 MB) take 32 us, 5.2 TB/s, those of
 // 16 prompts of up to 2048 (32 heads, bf16, pages of 16, 73 MB, part of them in the
 // caches) 13.1 us, 5.5 TB/s; 32000 tokens of 16 heads, e4m3 in pages of 16, of 128
 // elements 17.5 us, of 64 10.8.  (With a wave to a page whatever its size, all lanes
 // joining both through LDS: 39 and 13.1, 39.5 and 40.4.)  Of that form: two or eight
-// loads of a lane under way instead of four 41 and 38 us for the first; loads past the
-// caches 34 and 14.2.
-template <int D, bool E4M3, int G>
+// loads of a lane under way instead of four 41 and 38 us for the first.
+// From kBoundsPast bytes of keys on, loads go past the caches, which they would only
+// fill: us without and with that, two sets of 16 heads in turn,
+//   bf16, 128, pages of 64   133 MB 23.0/23.4   166 31.8/28.7   266 51.8/45.5   533 101/88
+//         64           16     87    14.8/16.2   139 22.3/25.5   174 36.6/32.2   557 114/107
+//   e4m3, 128          64    136    27.2/27.9   170 39.3/34.6   272 62.2/57.8   545 117/115
+//         64           16    117    26.7/31.2   150 40.4/38.9   299 76.9/78.1
+constexpr int64_t kBoundsPast = 160000000;
+template <int D, bool E4M3, int G, bool PAST>
 struct PageBounds {
     static constexpr int LPT = D * (E4M3 ? 1 : 2) / 16, LANES = 64 / G, TOKENS = LANES / LPT;
     static constexpr int N = E4M3 ? 8 : 4, E = 2 * N;  // registers and elements of a lane
@@ -64,7 +70,8 @@ struct PageBounds {
     __device__ __forceinline__ static bool first() { return (int)(threadIdx.x & (G == 1 ? 31 : G == 2 ? 15 : 11)) < LPT; }
 
     __device__ __forceinline__ static void values(const char* from, uint32_t scale, u32x4_t (&x)[N / 4]) {
-        const u32x4_t raw = *reinterpret_cast<const u32x4_t*>(from);
+        const u32x4_t* at = reinterpret_cast<const u32x4_t*>(from);
+        const u32x4_t raw = PAST ? __builtin_nontemporal_load(at) : *at;
         if constexpr (E4M3) {
             x[0] = dequant8(u32x2_t{raw[0], raw[1]}, scale_of(scale));
             x[1] = dequant8(u32x2_t{raw[2], raw[3]}, scale_of(scale));
@@ -188,9 +195,9 @@ __device__ __forceinline__ uint32_t careful_bounds(const Kv& c, int32_t page, in
     return top;
 }
 
-template <int D, bool E4M3, int G>
+template <int D, bool E4M3, int G, bool PAST>
 __global__ __launch_bounds__(256) void kv_bounds_kernel(BoundsArgs a) {
-    typedef PageBounds<D, E4M3, G> P;
+    typedef PageBounds<D, E4M3, G, PAST> P;
     const uint32_t units = (uint32_t)a.n_pages * (uint32_t)a.kv.n_kv_heads;
     const uint32_t u = (blockIdx.x * 4 + (G > 1 ? threadIdx.x >> 6 : (uint32_t)wave_id())) * G + (threadIdx.x & 63) / P::LANES;
     if (u - (threadIdx.x & 63) / P::LANES >= units) return;  // (the last wave's other pages: of the last one again)
@@ -724,18 +731,22 @@ extern "C" int32_t lora_kv_bounds(const lora_sparse_launch_t* L, const lora_kv_t
     BoundsArgs a{to_kv(*kv), bounds->codes, bounds->exps, nullptr, 0};
     typedef void (*fn_t)(BoundsArgs);
     // by the lanes that a page of one head has work for, 16 bytes of four tokens each
-    static const fn_t fn[2][2][3] = {{{kv_bounds_kernel<64, false, 1>, kv_bounds_kernel<64, false, 2>, nullptr},
-                                      {kv_bounds_kernel<64, true, 1>, kv_bounds_kernel<64, true, 2>, kv_bounds_kernel<64, true, 4>}},
-                                     {{kv_bounds_kernel<128, false, 1>, nullptr, nullptr},
-                                      {kv_bounds_kernel<128, true, 1>, kv_bounds_kernel<128, true, 2>, nullptr}}};
+#define SP_FORMS(d, e4m3, g) {kv_bounds_kernel<d, e4m3, g, false>, kv_bounds_kernel<d, e4m3, g, true>}
+    static const fn_t fn[2][2][3][2] = {{{SP_FORMS(64, false, 1), SP_FORMS(64, false, 2), {}},
+                                         {SP_FORMS(64, true, 1), SP_FORMS(64, true, 2), SP_FORMS(64, true, 4)}},
+                                        {{SP_FORMS(128, false, 1), {}, {}},
+                                         {SP_FORMS(128, true, 1), SP_FORMS(128, true, 2), {}}}};
+#undef SP_FORMS
     const bool e4m3 = kv->dtype == LORA_KV_E4M3;
     const int lanes = kv->head_dim * (e4m3 ? 1 : 2) / 16 * kv->page_tokens / 4, form = lanes >= 64 ? 0 : lanes >= 32 ? 1 : 2;
-    const int32_t hk = kv->n_kv_heads, most = std::max(1, (int32_t)(kMaxBlocks / hk));  // pages of a launch
+    const int32_t hk = kv->n_kv_heads;
+    const bool past = (int64_t)L->info.n_fresh * kv->page_tokens * hk * kv->head_dim * (e4m3 ? 1 : 2) >= kBoundsPast;
+    const int32_t most = std::max(1, (int32_t)(kMaxBlocks / hk));  // pages of a launch
     for (int32_t i = 0; i < L->info.n_fresh; i += a.n_pages) {
         a.pages = L->attn.meta + L->info.off_fresh + i;
         a.n_pages = std::min(most, L->info.n_fresh - i);
         const int64_t units = (int64_t)a.n_pages * hk, per = 4 << form;
-        if (launch(fn[kv->head_dim == 128][e4m3][form], dim3((unsigned)((units + per - 1) / per)), dim3(256),
+        if (launch(fn[kv->head_dim == 128][e4m3][form][past], dim3((unsigned)((units + per - 1) / per)), dim3(256),
                    reinterpret_cast<hipStream_t>(hip_stream), a) != hipSuccess)
             return LORA_EHIP;
     }

@@ -208,6 +208,23 @@ def test_bounds_of_pages_that_share_a_wave(dim, kv_heads, n, page, dtype):
     check_bounds(cache, bounds, [int(p) for p in table[0]], before)
 
 
+@pytest.mark.parametrize("dim,page,dtype", [(128, 64, "bf16"), (64, 16, "e4m3"), (64, 16, "bf16"), (128, 16, "e4m3"),
+                                            (64, 32, "e4m3")])
+def test_bounds_of_many_pages(dim, page, dtype):
+    """A call of 160 MB of keys and more: the same pages many times over."""
+    rng = np.random.default_rng([dim, page])
+    n, hk = 20, 8
+    each = page * hk * dim * (2 if dtype == "bf16" else 1)
+    cache = make_cache(rng, n, hk, page, dim, dtype)
+    table = np.resize(rng.permutation(n).astype(np.int32), (1, 165000000 // each))
+    bounds = make_bounds(rng, cache)
+    before = bounds.codes.clone(), bounds.exps.clone()
+    batch = SparseBatch(cache, hk, 2).refresh([0], [table.shape[1] * page], table, bounded=[0])
+    batch.bounds(bounds)
+    torch.cuda.synchronize()
+    check_bounds(cache, bounds, list(range(n)), before)
+
+
 def test_choice_of_every_kind_of_query():
     rng = np.random.default_rng(3)
     q = torch.from_numpy(rng.standard_normal((12, 4 * 64)).astype(np.float32))
