@@ -40,12 +40,16 @@ static_assert(sizeof(CopyMany) <= 4096, "a kernel's arguments are at most 4 KiB"
 // workgroup 256 / VPR tokens: of one head, or where a page holds fewer of several
 // heads side by side.  Bound by memory: 64 forks inside pages of 16 (8 kv heads,
 // bf16, 32 layers: 132 MB moved) take 24.7 us, 5.4 TB/s; 700 whole e4m3 pages of 64
-// of 4 layers, with scales and bounds (751 MB), 163 us, 4.6 TB/s in four launches.
+// of 4 layers, with scales and bounds (751 MB), 154 us, 4.9 TB/s in four launches.
 // Small workgroups, since all of a launch's copies are under way at once anyway: two
 // and four such steps to a workgroup take 26.5 and 27.9 us (fork).  Stores go past
-// the caches (without: 32.7 and 174); loads do not, the pages of a fork having been
-// written a step before (with: 26.3 and 155).
-template <int VPR, bool SCALES, typename Args>
+// the caches (without: 32.7 and 174); loads, of pages that may have been written a step
+// before, from kCopyPast bytes of a call on.  us without and with that, 8 caches of 8
+// heads of 128, whole pages:
+//   bf16, pages of 16   64 MB 20.0/24.4   129 43.1/51.5   160 59.0/63.4   200 79.7/79.1   500 209/205
+//   e4m3,          64   64    21.1/24.9   130 41.1/48.0   161 55.0/59.5   201 75.5/74.6   503 197/193
+constexpr int64_t kCopyPast = 200000000;
+template <int VPR, bool SCALES, bool PAST, typename Args>
 __global__ __launch_bounds__(256) void kv_copy_kernel(Args a) {
     constexpr int ROWS = 256 / VPR;
     const CopyCache &c = a.cache[blockIdx.z], &t = a.cache[blockIdx.z + a.to_cache];
@@ -57,7 +61,8 @@ __global__ __launch_bounds__(256) void kv_copy_kernel(Args a) {
     if (token < p.tokens && head < a.n_heads) {
         const int64_t at = p.from * a.from_page + head * a.from_head + token * a.from_token + 16 * col;
         const int64_t to = p.to * a.to_page + head * a.to_head + token * a.to_token + 16 * col;
-        const u32x4_t k = *reinterpret_cast<const u32x4_t*>(c.k + at), v = *reinterpret_cast<const u32x4_t*>(c.v + at);
+        const u32x4_t *kp = reinterpret_cast<const u32x4_t*>(c.k + at), *vp = reinterpret_cast<const u32x4_t*>(c.v + at);
+        const u32x4_t k = PAST ? __builtin_nontemporal_load(kp) : *kp, v = PAST ? __builtin_nontemporal_load(vp) : *vp;
         if (SCALES && col == 0) {
             const int64_t s = (((int64_t)p.from * a.n_heads + head) << a.page_shift) + token;
             const int64_t d = (((int64_t)p.to * a.n_heads + head) << a.page_shift) + token;
@@ -167,8 +172,14 @@ int32_t copy_pages(bool across, int32_t n_caches, const lora_kv_t* from, const l
     const int32_t most = across ? Args::kCaches / 2 : Args::kCaches;  // caches of a launch
     a.to_cache = across ? most : 0;
     typedef void (*fn_t)(Args);
-    const fn_t fn = e4m3 ? (vpr == 8 ? kv_copy_kernel<8, true, Args> : kv_copy_kernel<4, true, Args>)
-                         : (vpr == 16 ? kv_copy_kernel<16, false, Args> : kv_copy_kernel<8, false, Args>);
+    static const fn_t fns[2][2][2] = {{{kv_copy_kernel<8, false, false, Args>, kv_copy_kernel<8, false, true, Args>},
+                                       {kv_copy_kernel<16, false, false, Args>, kv_copy_kernel<16, false, true, Args>}},
+                                      {{kv_copy_kernel<4, true, false, Args>, kv_copy_kernel<4, true, true, Args>},
+                                       {kv_copy_kernel<8, true, false, Args>, kv_copy_kernel<8, true, true, Args>}}};
+    int64_t bytes = 0;
+    for (int32_t j = 0; j < n_pairs; ++j) bytes += tokens ? tokens[j] : c.page_tokens;
+    bytes *= (int64_t)2 * n_caches * c.n_kv_heads * c.head_dim * es;
+    const fn_t fn = fns[e4m3][c.head_dim == 128][bytes >= kCopyPast];
     const unsigned gx = (unsigned)(token_blocks * ((c.n_kv_heads + heads - 1) / heads));
     for (int32_t i = 0; i < n_caches;) {
         int32_t n = 0;  // caches of one launch: those on end with the same strides

@@ -69,6 +69,21 @@ def test_copy(dim, kv_heads, page, dtype):
         run_case(pairs, [make_cache(rng, 20, kv_heads, page, dim, dtype)], whole=whole)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("dim,page,pairs,layers", [(128, 1024, 16, 7), (64, 64, 230, 14)])
+def test_large_copies(dim, page, pairs, layers, dtype):
+    """200 MB and more, of few pairs and of many."""
+    caches = [KvCache.empty(2 * pairs + 1, 8, page, dim, dtype) for _ in range(layers)]
+    for c in caches:
+        for t in (c.k, c.v):
+            t.view(torch.uint8).random_(generator=torch.Generator("cuda").manual_seed(pairs))
+        for t in (c.k_scale, c.v_scale):
+            if t is not None:
+                t.random_(100, 150)
+    assert 2 * layers * pairs * 8 * page * dim * caches[0].k.element_size() >= 200e6
+    run_case(pairs, caches, whole=True)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_layers_strides_and_bounds(dtype):
     """More caches and pairs than one launch takes; layouts that change between caches."""
