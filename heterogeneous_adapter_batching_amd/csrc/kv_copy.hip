@@ -2,6 +2,7 @@
 #include <stddef.h>
 
 #include <algorithm>
+#include <functional>
 #include <new>
 #include <vector>
 
@@ -111,21 +112,69 @@ bool same_strides(const lora_kv_t& a, const lora_kv_t& b) {
     return a.page_stride == b.page_stride && a.head_stride == b.head_stride && a.token_stride == b.token_stride;
 }
 
-// The tensors that are written: of one cache each.  `shared`: some are read too.
-int32_t check_tensors(int32_t n, const lora_kv_t* from, const lora_kv_t* to, const lora_kv_bounds_t* to_bounds,
-                      bool& shared) {
+// A tensor that is written, and where from; strides of the pages' tensors, and of
+// the others a number for their kind.
+struct Written {
+    const void *to, *from;
+    int32_t cache;
+    int64_t page_stride, head_stride, token_stride;
+    bool operator<(const Written& o) const { return std::less<const void*>()(to, o.to); }
+    bool alike(const Written& o) const {
+        return from == o.from && page_stride == o.page_stride && head_stride == o.head_stride && token_stride == o.token_stride;
+    }
+};
+// Memory that is read and also written: of keys, values or scales, of bounds by
+// their own copy, and of bounds by another cache's.
+struct Shared {
+    bool pages, bounds, others_bounds;
+};
+
+// No memory is written twice, but by copies that write the same: of keys and values
+// that are one tensor on both sides, and within caches (which may be listed twice)
+// wherever the layouts are the same.  Scales and exponents count where there is
+// something to copy.
+int32_t check_tensors(bool within, bool any, int32_t n, const lora_kv_t* from, const lora_kv_t* to,
+                      const lora_kv_bounds_t* from_bounds, const lora_kv_bounds_t* to_bounds, Shared& shared) {
+    shared = {within, false, false};
+    if (within && std::all_of(from, from + n, [&](const lora_kv_t& c) { return same_strides(c, from[0]); })) return LORA_OK;
     try {
-        std::vector<const void*> written;
+        std::vector<Written> written;
         for (int32_t i = 0; i < n; ++i) {
-            written.push_back(to[i].k);
-            if (to[i].v != to[i].k) written.push_back(to[i].v);
-            if (to_bounds) written.push_back(to_bounds[i].codes);
+            const auto add = [&](const void* t, const void* f, int64_t page, int64_t head, int64_t token) {
+                if (t) written.push_back({t, f, i, page, head, token});
+            };
+            add(to[i].k, from[i].k, to[i].page_stride, to[i].head_stride, to[i].token_stride);
+            add(to[i].v, from[i].v, to[i].page_stride, to[i].head_stride, to[i].token_stride);
+            if (within) continue;
+            if (to_bounds) add(to_bounds[i].codes, from_bounds[i].codes, -1, 0, 0);
+            if (!any) continue;
+            if (to[i].dtype == LORA_KV_E4M3) {
+                add(to[i].k_scale, from[i].k_scale, -2, 0, 0);
+                add(to[i].v_scale, from[i].v_scale, -2, 0, 0);
+            }
+            if (to_bounds) add(to_bounds[i].exps, from_bounds[i].exps, -3, 0, 0);
         }
         std::sort(written.begin(), written.end());
-        if (std::adjacent_find(written.begin(), written.end()) != written.end()) return LORA_EINVAL;
-        for (int32_t i = 0; i < n && !shared; ++i)
-            shared = std::binary_search(written.begin(), written.end(), from[i].k) ||
-                     std::binary_search(written.begin(), written.end(), from[i].v);
+        for (size_t i = 1; i < written.size(); ++i) {
+            const Written &x = written[i - 1], &y = written[i];
+            if (x.to == y.to && !((within || x.cache == y.cache) && x.alike(y))) return LORA_EINVAL;
+        }
+        if (within) return LORA_OK;
+        const auto find = [&](const void* p) {  // the cache by which it is written, or -1
+            const auto at = std::lower_bound(written.begin(), written.end(), Written{p, nullptr, 0, 0, 0, 0});
+            return p && at != written.end() && at->to == p ? at->cache : -1;
+        };
+        for (int32_t i = 0; i < n; ++i) {
+            for (const void* p : {(const void*)from[i].k, (const void*)from[i].v, (const void*)from[i].k_scale,
+                                  (const void*)from[i].v_scale})
+                shared.pages |= find(p) >= 0;
+            if (!from_bounds) continue;
+            for (const void* p : {(const void*)from_bounds[i].codes, (const void*)from_bounds[i].exps}) {
+                const int32_t by = find(p);
+                shared.bounds |= by == i;
+                shared.others_bounds |= by >= 0 && by != i;
+            }
+        }
     } catch (const std::bad_alloc&) {
         return LORA_ENOMEM;
     }
@@ -133,20 +182,34 @@ int32_t check_tensors(int32_t n, const lora_kv_t* from, const lora_kv_t* to, con
 }
 
 // Every page that is written is written once, and none is read that is also
-// written where source and destination share memory.
+// written where source and destination share memory.  (Bounds go with whole pages
+// only, and may stay where they are.)
 int32_t check_pairs(int32_t n, const int32_t* from, const int32_t* to, const int32_t* tokens, int32_t from_pages,
-                    int32_t to_pages, int32_t page_tokens, bool shared) {
+                    int32_t to_pages, int32_t page_tokens, const Shared& shared) {
     for (int32_t i = 0; i < n; ++i) {
         if (from[i] < 0 || from[i] >= from_pages || to[i] < 0 || to[i] >= to_pages) return LORA_EPAGE;
         if (tokens && (tokens[i] < 0 || tokens[i] > page_tokens)) return LORA_EINVAL;
     }
-    if (n < 2 && !(n == 1 && shared)) return LORA_OK;
+    const bool bounds = shared.bounds || shared.others_bounds;
+    if (n < 2 && !(n == 1 && (shared.pages || bounds))) return LORA_OK;
     try {
         std::vector<int32_t> written(to, to + n);
         std::sort(written.begin(), written.end());
         if (std::adjacent_find(written.begin(), written.end()) != written.end()) return LORA_EINVAL;
-        for (int32_t i = 0; i < n && shared; ++i)
-            if (std::binary_search(written.begin(), written.end(), from[i])) return LORA_EINVAL;
+        if (shared.pages) {
+            for (int32_t i = 0; i < n; ++i)
+                if (std::binary_search(written.begin(), written.end(), from[i])) return LORA_EINVAL;
+        } else if (bounds) {
+            const auto whole = [&](int32_t i) { return !tokens || tokens[i] == page_tokens; };
+            written.clear();
+            for (int32_t i = 0; i < n; ++i)
+                if (whole(i)) written.push_back(to[i]);
+            std::sort(written.begin(), written.end());
+            for (int32_t i = 0; i < n; ++i)
+                if (whole(i) && (shared.others_bounds || from[i] != to[i]) &&
+                    std::binary_search(written.begin(), written.end(), from[i]))
+                    return LORA_EINVAL;
+        }
     } catch (const std::bad_alloc&) {
         return LORA_ENOMEM;
     }
@@ -219,7 +282,6 @@ extern "C" int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const l
     if (to && (from_bounds != nullptr) != (to_bounds != nullptr)) return LORA_EINVAL;
     const lora_kv_t* dst = to ? to : from;
     const lora_kv_bounds_t* dst_bounds = to ? to_bounds : from_bounds;
-    bool shared = !to;
     for (int32_t i = 0; i < n_caches; ++i) {
         int32_t st = check_cache(from[i], from[0]);
         if (st == LORA_OK && to) st = check_cache(to[i], to[0]);
@@ -231,7 +293,8 @@ extern "C" int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const l
     if (dst->dtype != c.dtype || dst->head_dim != c.head_dim || dst->n_kv_heads != c.n_kv_heads ||
         dst->page_tokens != c.page_tokens)
         return LORA_ESHAPE;
-    int32_t st = to ? check_tensors(n_caches, from, to, to_bounds, shared) : LORA_OK;
+    Shared shared;
+    int32_t st = check_tensors(!to, n_pairs > 0, n_caches, from, dst, from_bounds, dst_bounds, shared);
     if (st == LORA_OK) st = check_pairs(n_pairs, from_page, to_page, tokens, c.n_pages, dst->n_pages, c.page_tokens, shared);
     if (st != LORA_OK) return st;
 

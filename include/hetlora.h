@@ -904,9 +904,13 @@ int32_t lora_attn(const lora_attn_launch_t* launch, const lora_kv_t* kv,
  *             They are read before the call returns.  A page is written by one
  *             pair at most, and within caches (to NULL, or any of to among from)
  *             no page that is written is also read
- * No two of to share a tensor or bounds, and caches of different memory must not
- * overlap.  One launch for each 192 pairs of 32 caches with the same strides (16
- * with to).  Errors: LORA_EINVAL, LORA_ESHAPE, LORA_EPAGE, LORA_ENOMEM, LORA_EHIP. */
+ * No memory is written twice: no two of to share k, v, scales or bounds, a k that
+ * is also its v comes from such a one, and a tensor listed twice within caches has
+ * one layout.  Bounds that are read and written may stay where they are (their
+ * page's number does not change), otherwise as above for whole pages.  Sharing is
+ * seen by addresses: tensors at different ones must not overlap.
+ * One launch for each 192 pairs of 32 caches with the same strides (16 with to).
+ * Errors: LORA_EINVAL, LORA_ESHAPE, LORA_EPAGE, LORA_ENOMEM, LORA_EHIP. */
 int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const lora_kv_t* to,
                      const lora_kv_bounds_t* from_bounds, const lora_kv_bounds_t* to_bounds,
                      int32_t n_pairs, const int32_t* from_page, const int32_t* to_page,

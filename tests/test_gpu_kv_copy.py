@@ -122,6 +122,23 @@ def test_bounds_to_others_of_the_same_cache():
         assert torch.equal(b.codes, codes) and torch.equal(b.exps, exps) and torch.equal(a.codes, kept)
 
 
+def test_bounds_that_both_caches_share():
+    """Whole pages that keep their numbers, and parts of pages, whose bounds stay where they are."""
+    rng = np.random.default_rng(12)
+    one, two = (make_cache(rng, 12, 2, 16, 64, "e4m3") for _ in range(2))
+    bounds = make_bounds(rng, one)
+    codes, exps = bounds.codes.clone(), bounds.exps.clone()
+    copy = KvCopy([one], [bounds], [two], [bounds])
+    for src, dst, n in (([1, 2, 5], [1, 2, 5], [16, 16, 16]), ([1, 2, 5], [2, 3, 6], [5, 15, 1])):
+        source, before = raw(one), raw(two)
+        copy.copy(src, dst, n)
+        torch.cuda.synchronize()
+        check(source, before, raw(two), src, dst, n, 16)
+        assert torch.equal(bounds.codes, codes) and torch.equal(bounds.exps, exps)
+    with pytest.raises(hl.LoraError):
+        copy.copy([1, 2], [2, 3])
+
+
 def test_one_page_to_many():
     rng = np.random.default_rng(5)
     run_case(9, [make_cache(rng, 20, 2, 16, 128, "bf16")], one_source=True)
