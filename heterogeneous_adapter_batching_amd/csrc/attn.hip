@@ -1664,6 +1664,23 @@ static const struct {
               {attn_narrow_kernel<128, false>, attn_narrow_kernel<128, true>}},
              {attn_merge_kernel<64>, attn_merge_kernel<128>}};
 
+// The n items (or merge entries) at `work` for every kv head, `per` to a workgroup of
+// `threads`, in as many launches as they need; more: the kernel takes their number too.
+template <typename... More>
+static bool launch_items(void (*fn)(AttnArgs, More...), AttnArgs& a, const int32_t* work, int64_t n, int32_t per,
+                         unsigned threads, hipStream_t s) {
+    const int64_t most = std::max<int64_t>(1, kMaxBlocks * 256 / threads / a.kv.n_kv_heads) * per;
+    for (int64_t i = 0; i < n; i += most) {
+        int32_t count = (int32_t)std::min(most, n - i);
+        a.work = reinterpret_cast<const lora_attn_work_t*>(work) + i;
+        void* p[] = {&a, &count};
+        if (hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)((count + per - 1) / per * a.kv.n_kv_heads)),
+                            dim3(threads), p, 0, s) != hipSuccess)
+            return false;
+    }
+    return true;
+}
+
 extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, const uint16_t* q, int64_t ldq,
                              uint16_t* out, int64_t ldo, float scale, float* workspace, int64_t workspace_floats,
                              void* hip_stream) {
@@ -1675,8 +1692,8 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     AttnArgs a;
     st = attn_args(L, kv, q, ldq, out, ldo, scale, workspace, workspace_floats, a);
     if (st != LORA_OK) return st;
-    for (const int64_t n : {I.n_work[0], I.n_work[1], I.n_work[2], I.n_merge})
-        if (n < 0 || n * hk > kMaxBlocks) return LORA_EINVAL;
+    for (const int32_t n : {I.n_work[0], I.n_work[1], I.n_work[2], I.n_merge})
+        if (n < 0) return LORA_EINVAL;
     a.table = L->meta + I.off_table;
     a.part_rows = I.part_rows;
     a.n_seq = I.n_seq;
@@ -1698,19 +1715,12 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
     const bool uni = kv->page_tokens >= 64 / (d / 8) && kv->token_stride <= INT32_MAX / 64 &&
                      kv->page_stride <= INT32_MAX && (int64_t)kv->n_pages * kv->page_tokens * hk <= UINT32_MAX;
     for (int kind = LORA_ATTN_KINDS - 1; kind >= 0; --kind) {  // the longer items first
-        if (I.n_work[kind] == 0) continue;
-        a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_work[kind]);
-        const dim3 grid((unsigned)(I.n_work[kind] * hk)), block(kind == LORA_ATTN_PAIR ? 512 : 256);
         const fn_t fn = kind == LORA_ATTN_NARROW ? kNarrow.narrow[d == 128][e4m3]
                                                  : wide[kind == LORA_ATTN_PAIR][d == 128][e4m3][uni];
-        if (launch(fn, grid, block, s, a) != hipSuccess) return LORA_EHIP;
+        if (!launch_items(fn, a, L->meta + I.off_work[kind], I.n_work[kind], 1, kind == LORA_ATTN_PAIR ? 512 : 256, s))
+            return LORA_EHIP;
     }
-    if (I.n_merge > 0) {
-        a.work = reinterpret_cast<const lora_attn_work_t*>(L->meta + I.off_merge);
-        const dim3 grid((unsigned)(I.n_merge * hk));
-        if (launch(kNarrow.merge[d == 128], grid, dim3(256), s, a) != hipSuccess) return LORA_EHIP;
-    }
-    return LORA_OK;
+    return launch_items(kNarrow.merge[d == 128], a, L->meta + I.off_merge, I.n_merge, 1, 256, s) ? LORA_OK : LORA_EHIP;
 }
 
 // Items (of all kv heads) from which on each has a wave to itself.  us for 1024, 2048
@@ -1739,8 +1749,6 @@ extern "C" int32_t lora_sparse_attn(const lora_sparse_launch_t* L, const lora_kv
     AttnArgs a;
     st = attn_args(&L->attn, kv, q, ldq, out, ldo, scale, workspace, workspace_floats, a);
     if (st != LORA_OK) return st;
-    for (const int64_t n : {S.n_work, S.n_merge})
-        if (n * hk > kMaxBlocks) return LORA_EINVAL;
     // every row is a sequence of its own, with a page table for each kv head
     a.table = selected;
     a.table_head = S.shape.select;
@@ -1749,23 +1757,15 @@ extern "C" int32_t lora_sparse_attn(const lora_sparse_launch_t* L, const lora_kv
     a.n_seq = I.n_rows;
     a.max_kv = (int32_t)std::min((int64_t)S.shape.select * I.shape.page_tokens, (int64_t)I.max_kv);
     const hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
-    a.work = reinterpret_cast<const lora_attn_work_t*>(L->attn.meta + S.off_work);
+    const int32_t* work = L->attn.meta + S.off_work;
     const bool e4m3 = kv->dtype == LORA_KV_E4M3;
     // (a page's rows lie within 32 bits of its first one)
     if ((int64_t)S.n_work * hk >= solo_items(*kv) && kv->token_stride <= INT32_MAX / 2048) {
         const auto solo = d == 64 ? attn_solo_kernel<64, false> : e4m3 ? attn_solo_kernel<128, true> : attn_solo_kernel<128, false>;
-        int32_t n = S.n_work;
-        void* p[] = {&a, &n};
-        if (hipLaunchKernel(reinterpret_cast<const void*>(solo), dim3((unsigned)((n + 3) / 4 * hk)),
-                            dim3(256), p, 0, s) != hipSuccess)
-            return LORA_EHIP;
-    } else if (launch(kNarrow.narrow[d == 128][e4m3], dim3((unsigned)(S.n_work * hk)), dim3(256), s, a) != hipSuccess) {
+        if (!launch_items(solo, a, work, S.n_work, 4, 256, s)) return LORA_EHIP;
+    } else if (!launch_items(kNarrow.narrow[d == 128][e4m3], a, work, S.n_work, 1, 256, s)) {
         return LORA_EHIP;
     }
-    if (S.n_merge > 0) {
-        a.work = reinterpret_cast<const lora_attn_work_t*>(L->attn.meta + S.off_merge);
-        if (launch(kNarrow.merge[d == 128], dim3((unsigned)(S.n_merge * hk)), dim3(256), s, a) != hipSuccess)
-            return LORA_EHIP;
-    }
+    if (!launch_items(kNarrow.merge[d == 128], a, L->attn.meta + S.off_merge, S.n_merge, 1, 256, s)) return LORA_EHIP;
     return LORA_OK;
 }

@@ -1055,7 +1055,8 @@ int32_t lora_sparse_prepare(const lora_attn_shape_t* shape, const lora_sparse_sh
                             lora_sparse_launch_t* out);
 
 /* Bounds of the plan's fresh pages (those complete pages of the batch's sequences
- * that hold tokens from `bounded` on).  One launch.  Errors: as lora_kv_write. */
+ * that hold tokens from `bounded` on).  One launch up to 2^23 pages, each kv head's
+ * counted.  Errors: as lora_kv_write. */
 int32_t lora_kv_bounds(const lora_sparse_launch_t* launch, const lora_kv_t* kv, const lora_kv_bounds_t* bounds,
                        void* hip_stream);
 
