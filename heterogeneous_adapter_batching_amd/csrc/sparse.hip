@@ -52,11 +52,13 @@ struct BoundsArgs {
 // joining both through LDS: 39 and 13.1, 39.5 and 40.4.)  Of that form: two or eight
 // loads of a lane under way instead of four 41 and 38 us for the first.
 // From kBoundsPast bytes of keys on, loads go past the caches, which they would only
-// fill: us without and with that, two sets of 16 heads in turn,
-//   bf16, 128, pages of 64   133 MB 23.0/23.4   166 31.8/28.7   266 51.8/45.5   533 101/88
-//         64           16     87    14.8/16.2   139 22.3/25.5   174 36.6/32.2   557 114/107
-//   e4m3, 128          64    136    27.2/27.9   170 39.3/34.6   272 62.2/57.8   545 117/115
-//         64           16    117    26.7/31.2   150 40.4/38.9   299 76.9/78.1
+// fill (a write of so many keys, and of as many values, has left none of them there).
+// us without and with that, 16 heads, the same keys again and again, which the caches
+// hold as far as they can, and three sets of keys in turn:
+//   bf16, 128, pages of 64   132 MB 22/22 26/23   167 27/28 34/29   305 48/50 59/51   508  96/83   96/85
+//         64           16    138    21/24 28/25   175 27/33 37/32   319 63/61 65/58   531 109/101 108/96
+//   e4m3, 128          64    135    26/26 30/27   171 32/34 38/34   312 66/63 65/58   519 113/104 105/95
+//         64           16    148    34/40 36/37   188 43/51 44/45   342 85/87 76/77   571 136/138 125/127: never
 constexpr int64_t kBoundsPast = 160000000;
 template <int D, bool E4M3, int G, bool PAST>
 struct PageBounds {
@@ -732,15 +734,18 @@ extern "C" int32_t lora_kv_bounds(const lora_sparse_launch_t* L, const lora_kv_t
     typedef void (*fn_t)(BoundsArgs);
     // by the lanes that a page of one head has work for, 16 bytes of four tokens each
 #define SP_FORMS(d, e4m3, g) {kv_bounds_kernel<d, e4m3, g, false>, kv_bounds_kernel<d, e4m3, g, true>}
+#define SP_NEVER(d, e4m3, g) {kv_bounds_kernel<d, e4m3, g, false>, nullptr}
     static const fn_t fn[2][2][3][2] = {{{SP_FORMS(64, false, 1), SP_FORMS(64, false, 2), {}},
-                                         {SP_FORMS(64, true, 1), SP_FORMS(64, true, 2), SP_FORMS(64, true, 4)}},
+                                         {SP_NEVER(64, true, 1), SP_NEVER(64, true, 2), SP_NEVER(64, true, 4)}},
                                         {{SP_FORMS(128, false, 1), {}, {}},
                                          {SP_FORMS(128, true, 1), SP_FORMS(128, true, 2), {}}}};
 #undef SP_FORMS
+#undef SP_NEVER
     const bool e4m3 = kv->dtype == LORA_KV_E4M3;
     const int lanes = kv->head_dim * (e4m3 ? 1 : 2) / 16 * kv->page_tokens / 4, form = lanes >= 64 ? 0 : lanes >= 32 ? 1 : 2;
     const int32_t hk = kv->n_kv_heads;
-    const bool past = (int64_t)L->info.n_fresh * kv->page_tokens * hk * kv->head_dim * (e4m3 ? 1 : 2) >= kBoundsPast;
+    const bool past = !(e4m3 && kv->head_dim == 64) &&
+                      (int64_t)L->info.n_fresh * kv->page_tokens * hk * kv->head_dim * (e4m3 ? 1 : 2) >= kBoundsPast;
     const int32_t most = std::max(1, (int32_t)(kMaxBlocks / hk));  // pages of a launch
     for (int32_t i = 0; i < L->info.n_fresh; i += a.n_pages) {
         a.pages = L->attn.meta + L->info.off_fresh + i;
