@@ -1410,13 +1410,17 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : E4M3 ? 3 : 2) void attn_narrow_k
 
 // The same with a wave to an item, for many items (of a sparse attention: the pages
 // that many tokens see come from the L2, and its loads have to be wide to be fast).
-// Nothing is joined.  920 new tokens of 64/8 heads, 16 pages of 64 in 33k tokens, take
-// 226 us, 3.9 GB of keys and values at 17 TB/s, 77% of them from the L2: a compute unit
-// takes 340 cycles for a tile, of which the path of its loads needs 256 (64 bytes a
-// cycle), LDS as many, and no wave waits for memory (e4m3 takes as long: its LDS traffic
-// is the same).  The narrow kernel takes 458, and as long with a wave to an item: its
-// loads are served 16 bytes at a time.  Keys turned by moves between lanes, past LDS:
-// 235; the values of the next tile sent for after this one's product: 255.
+// Nothing is joined.  961 new tokens of 64/8 heads, 16 pages of 64 in 16k to 33k tokens,
+// take 213 us, 4.0 GB of keys and values at 18.6 TB/s, 77% of them from the L2.  By
+// counters (at 2.17 GHz) a wave is there 3280 cycles for each tile, so the eight of a
+// compute unit finish one every 410.  Of these the path of its loads needs 256 (64 bytes
+// a cycle), LDS 195, each vector unit 123 and each matrix unit 104: no unit is full, and
+// two waves to a SIMD cover each other's waits (half of their time) in part only.  The
+// 7688 items are 3.75 rounds of the waves that fit, with no work for 15% of the units'
+// time between the first and the last.  The narrow kernel takes twice as long, also with a
+// wave to an item: its loads are served 16 bytes at a time.  Keys turned by moves between
+// lanes, past LDS: 4% more; the values of the next tile sent for after this one's product:
+// 13% more.  (e4m3 takes as long: its LDS traffic is the same.)
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_solo_kernel(AttnArgs a, int32_t n_items) {
     constexpr int DB = D / 16, KS = D / 32, T = 32;
@@ -1724,7 +1728,8 @@ extern "C" int32_t lora_attn(const lora_attn_launch_t* L, const lora_kv_t* kv, c
 }
 
 // Items (of all kv heads) from which on each has a wave to itself.  us for 1024, 2048
-// and 4096 items of 16 pages of 64, shared by four waves and a wave each:
+// and 4096 items of 16 pages of 64 (the only number and size of pages that was tried),
+// shared by four waves and a wave each:
 //   head_dim 128, bf16   64/40    119/58    230/111   (512: 34/37)
 //                 e4m3   39/45     70/60    130/111
 //             64, bf16   31/30     61/36    117/55    (512: 17/29)

@@ -70,7 +70,7 @@ AT_FN int at_inside(const lora_attn_work_t* w, int32_t n_seq, int32_t n_rows, in
 #define SP_EXP 100           // exponents of bounds are within +-SP_EXP
 // Keys (scores) that a selecting workgroup of several tokens holds in LDS at most, tiles
 // of 16 rows (query heads of its tokens) that it scores one after another at most, and
-// its waves, each of which chooses for a token.  More tokens than waves only as 2 or 4
+// its waves, each of which chooses for a token.  More tokens than waves only as 2, 4 or 8
 // times as many, and with few keys: us of 2048 tokens, 8 kv heads of 2 query heads, over
 //              8 tokens   16   24
 //   282 pages      36.5 28.5 46.0
@@ -92,6 +92,10 @@ AT_FN int at_inside(const lora_attn_work_t* w, int32_t n_seq, int32_t n_rows, in
 //   1 sequence   7.5/11.9   9.9/12.7  14.5/13.4  28.6/14.9  50.7/16.7
 //   16           8.0/12.5  11.3/14.3  18.3/20.3  37.4/30.6  73.5/55.7
 //   64          18.8/23.5  29.7/34.2  53.2/59.4
+// (One sequence alone would gain from some 1900 pages on; the rule is the same for any
+// number of them.)  The batch's longest context decides for all of it: 64/8 heads, pages of
+// 16, 512 tokens over 16512 take 60 us, one over 131072 19, both in one batch 312, with
+// one token to an item; 63 single tokens over 8192 20, one over 40000 14, all 64 32.
 #define SP_ONE_KEYS 2048
 #define SP_SLAB_KEYS (1 << 24)  // keys in memory at once
 

@@ -46,9 +46,12 @@ static_assert(sizeof(CopyMany) <= 4096, "a kernel's arguments are at most 4 KiB"
 // and four such steps to a workgroup take 26.5 and 27.9 us (fork).  Stores go past
 // the caches (without: 32.7 and 174); loads, of pages that may have been written a step
 // before, from kCopyPast bytes of a call on.  us without and with that, 8 caches of 8
-// heads of 128, whole pages:
-//   bf16, pages of 16   64 MB 20.0/24.4   129 43.1/51.5   160 59.0/63.4   200 79.7/79.1   500 209/205
-//   e4m3,          64   64    21.1/24.9   130 41.1/48.0   161 55.0/59.5   201 75.5/74.6   503 197/193
+// heads of 128, whole pages, the same ones again and again, which the caches hold as far
+// as they can, and three sets of pages in turn:
+//   bf16, pages of 16   129 MB 41/50 51/52   160 50/63 64/64   200 65/78 81/79   300 106/119 123/121   500 209/205 208/205
+//   e4m3,          64   130    40/47 46/48   161 49/60 60/60   201 60/73 76/74   302 102/115 118/115   503 196/192 198/193
+// (The gain is small: of pages that were all written right before, a call of 200 to 300 MB
+// loses more than others gain.)
 constexpr int64_t kCopyPast = 200000000;
 template <int VPR, bool SCALES, bool PAST, typename Args>
 __global__ __launch_bounds__(256) void kv_copy_kernel(Args a) {

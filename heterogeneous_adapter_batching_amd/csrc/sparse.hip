@@ -50,7 +50,10 @@ struct BoundsArgs {
 // caches) 13.1 us, 5.5 TB/s; 32000 tokens of 16 heads, e4m3 in pages of 16, of 128
 // elements 17.5 us, of 64 10.8.  (With a wave to a page whatever its size, all lanes
 // joining both through LDS: 39 and 13.1, 39.5 and 40.4.)  Of that form: two or eight
-// loads of a lane under way instead of four 41 and 38 us for the first.
+// loads of a lane under way instead of four 41 and 38 us for the first.  Heads of 64 in
+// e4m3 stay at 3.5 to 4 TB/s: the vector units are busy 81% of the time (61% with heads of
+// 128), since a page of a head has half the bytes and as many joins and exponents; the
+// requests to the cache are as many for each byte.
 // From kBoundsPast bytes of keys on, loads go past the caches, which they would only
 // fill (a write of so many keys, and of as many values, has left none of them there).
 // us without and with that, 16 heads, the same keys again and again, which the caches
@@ -640,11 +643,11 @@ __device__ __forceinline__ void select_token(const SelectArgs& a, const SelectIt
 // bound it: one token over 500 pages, 8 kv heads, takes 7.5 us, of which 3 are a launch
 // and most of the rest the first pass through the code and the chain item, page ids,
 // bounds; 32 tokens over up to 2048 pages of 16 16.3 us, 2.4 TB/s; 512 tokens of 32/8
-// heads over 500 pages 14.5, 920 of 64/8 over up to 512 37.  (32 tokens with operands
+// heads over 500 pages 14.5, 961 of 64/8 over up to 508 32.  (32 tokens with operands
 // loaded as the matrix unit wants them, 16 bytes of each page to a lane: 22.7; with codes
 // of the queries made by every wave for itself: 18.9.)  Teams of 8 or 16 waves to choose
 // are within 5% of four.  Two tiles of a wave under way instead of one: no faster (heads
-// of 64), or spilled (128: 19.8 -> 26.7).  Of the 37 us the choice is a quarter.
+// of 64), or spilled (128: 19.8 -> 26.7).  Of the 32 us the choice is a quarter.
 constexpr int kTeam = 4;
 template <int D, int R>
 __global__ __launch_bounds__(R == 1 ? 1024 : 64 * SP_WAVES, 4) void select_kernel(SelectArgs a) {
