@@ -163,19 +163,25 @@ int32_t check_tensors(bool within, bool any, int32_t n, const lora_kv_t* from, c
             if (x.to == y.to && !((within || x.cache == y.cache) && x.alike(y))) return LORA_EINVAL;
         }
         if (within) return LORA_OK;
-        const auto find = [&](const void* p) {  // the cache by which it is written, or -1
+        const auto find = [&](const void* p) {  // what writes it, or none
             const auto at = std::lower_bound(written.begin(), written.end(), Written{p, nullptr, 0, 0, 0, 0});
-            return p && at != written.end() && at->to == p ? at->cache : -1;
+            return p && at != written.end() && at->to == p ? &*at : nullptr;
         };
         for (int32_t i = 0; i < n; ++i) {
             for (const void* p : {(const void*)from[i].k, (const void*)from[i].v, (const void*)from[i].k_scale,
                                   (const void*)from[i].v_scale})
-                shared.pages |= find(p) >= 0;
+                shared.pages |= find(p) != nullptr;
+            for (const void* p : {from[i].k, from[i].v}) {  // in one layout: others' pages overlap otherwise
+                const Written* by = find(p);
+                if (by && by->page_stride >= 0 && (by->page_stride != from[i].page_stride ||
+                    by->head_stride != from[i].head_stride || by->token_stride != from[i].token_stride))
+                    return LORA_EINVAL;
+            }
             if (!from_bounds) continue;
             for (const void* p : {(const void*)from_bounds[i].codes, (const void*)from_bounds[i].exps}) {
-                const int32_t by = find(p);
-                shared.bounds |= by == i;
-                shared.others_bounds |= by >= 0 && by != i;
+                const Written* by = find(p);
+                shared.bounds |= by && by->cache == i;
+                shared.others_bounds |= by && by->cache != i;
             }
         }
     } catch (const std::bad_alloc&) {

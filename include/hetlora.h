@@ -905,10 +905,11 @@ int32_t lora_attn(const lora_attn_launch_t* launch, const lora_kv_t* kv,
  *             pair at most, and within caches (to NULL, or any of to among from)
  *             no page that is written is also read
  * No memory is written twice: no two of to share k, v, scales or bounds, a k that
- * is also its v comes from such a one, and a tensor listed twice within caches has
- * one layout.  Bounds that are read and written may stay where they are (their
- * page's number does not change), otherwise as above for whole pages.  Sharing is
- * seen by addresses: tensors at different ones must not overlap.
+ * is also its v comes from such a one, and a tensor that is listed twice within
+ * caches, or is read and written, has one layout.  Bounds that are read and written
+ * may stay where they are (their page's number does not change), otherwise as above
+ * for whole pages.  Sharing is seen by addresses: tensors at different ones must not
+ * overlap.
  * One launch for each 192 pairs of 32 caches with the same strides (16 with to).
  * Errors: LORA_EINVAL, LORA_ESHAPE, LORA_EPAGE, LORA_ENOMEM, LORA_EHIP. */
 int32_t lora_kv_copy(int32_t n_caches, const lora_kv_t* from, const lora_kv_t* to,

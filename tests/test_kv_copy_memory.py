@@ -95,3 +95,14 @@ def test_bounds_that_are_read_and_written(name):
     for src, dst in (([1, 2], [2, 3]), ([1], [1])):  # each page's bounds from the other cache
         assert copy(src, dst, None, **crosswise) == hl.LORA_EINVAL
         assert copy(src, dst, [0] * len(src), **crosswise) == hl.LORA_OK
+
+
+@pytest.mark.parametrize("name", ["k", "v"])
+@pytest.mark.parametrize("other", ["k", "v"])
+def test_one_memory_read_in_one_layout_and_written_in_another(name, other):
+    """Page numbers say nothing about what overlaps."""
+    for change in (dict(page_stride=8192), dict(head_stride=4096), dict(token_stride=256)):
+        assert none(caches=[ONE], to=[cache(2, **{name: getattr(ONE, other)}, **change)]) == hl.LORA_EINVAL
+        assert none(caches=[ONE, TWO], to=[cache(2, **change), cache(3, **{name: getattr(ONE, other)}, **change)]) == hl.LORA_EINVAL
+        assert none(caches=[ONE], to=[cache(2, **change)]) == hl.LORA_OK
+    assert none(caches=[ONE], to=[cache(2, **{name: getattr(ONE, other)})]) == hl.LORA_OK
